@@ -52,8 +52,33 @@ enum fd_dtype {
    * per-tensor scale: a scaled cache folds its K scale into q and its V scale
    * into out).  Needs d = 128 and G >= 4 (tensor-core path); the K/V bytes per
    * token halve. */
-  FD_F16_E4M3KV = 2
+  FD_F16_E4M3KV = 2,
+  /* binary16 / bfloat16 q and out over a 4-bit cache: K and V elements are OCP E2M1
+   * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one E4M3 scale per 16
+   * consecutive elements of a head; an element stands for E2M1 value x scale (at most 6
+   * significant bits: exact in both 16-bit types).  d = 64 or 128, every G.  The
+   * cache is made of blocks of 16 tokens of one KV head (9 d bytes; see "4-bit
+   * blocks" below); fd_append writes them.  (3 is not a dtype.) */
+  FD_F16_E2M1KV = 4,
+  FD_BF16_E2M1KV = 5
 };
+
+/*
+ * 4-bit blocks.  Token i of a sequence lies in the block i / 16 of that sequence, at
+ * row r = i mod 16.  A K block and a V block of one KV head have 9 d bytes each:
+ *   K  row r at byte r d/2: element e in byte e / 2, even elements in the low half;
+ *      scale of elements 16 j .. 16 j + 15 at byte 8 d + r d/16 + j.
+ *   V  8 groups of d/8 elements, d bytes each.  In group g, the pair of tokens
+ *      (2 u, 2 u + 1) takes d/8 bytes at position u ^ s, s = 4 if (d = 128 ? g : g / 2) is
+ *      odd, else 0; its tokens follow each other with d/16 bytes each, elements as in K.
+ *      Scale of elements 16 j .. at byte 8 d + 16 j + r.
+ * (In these orders the tensor-core fragments of a thread are contiguous 16- or 8-byte
+ * words that its warp reads without bank conflicts.)  Layouts, in bytes:
+ *   contiguous  [blocks, Hkv, 9 d]; sequence b starts at block
+ *               ceil(L_0 / 16) + ... + ceil(L_{b-1} / 16)
+ *   paged       [num_pages, page_size / 16, Hkv, 9 d]
+ * Bytes of tokens past a sequence's length may hold anything.
+ */
 
 enum fd_status {
   FD_OK = 0,
@@ -220,7 +245,7 @@ int fd_workspace_init(fd_plan_t plan, void* workspace, cudaStream_t stream);
  *
  *   q          device [B, Hq, d] (dtype), contiguous
  *   k, v       device [N, Hkv, d] (dtype; 1-byte E4M3 for FD_F16_E4M3KV), contiguous,
- *              N = sum_b L_b
+ *              N = sum_b L_b; 4-bit dtypes: [sum_b ceil(L_b / 16), Hkv, 9 d] bytes
  *   out        device [B, Hq, d] (dtype), written
  *   lse        device [B, Hq] float, written (natural log); may be NULL
  *   workspace  device, fd_workspace_bytes(plan) bytes, zeroed once beforehand
@@ -243,7 +268,8 @@ int fd_decode(fd_plan_t plan, const void* q, const void* k, const void* v, void*
 /*
  * fd_decode_paged -- fd_decode over a paged KV cache.
  *
- *   k_pages, v_pages  device [num_pages, page_size, Hkv, d] (dtype), contiguous pools
+ *   k_pages, v_pages  device [num_pages, page_size, Hkv, d] (dtype), contiguous pools;
+ *                     4-bit dtypes: [num_pages, page_size / 16, Hkv, 9 d] bytes
  *   num_pages         pages in each pool (num_pages * page_size < 2^31)
  *   block_table       device int32 [B, bt_stride]: row b lists, in order, the pool
  *                     pages holding tokens [j*page_size, (j+1)*page_size) of
@@ -311,6 +337,120 @@ int fd_noalloc_status(fd_plan_t plan, cudaStream_t stream, int32_t* status);
 int fd_workspace_status(fd_plan_t plan, void* workspace, cudaStream_t stream,
                         int32_t* status);
 
+/*
+ * Cache rows: what writes the cache that fd_decode reads, and reads it back.
+ *
+ * fd_rows_plan -- the rows [begin_b, begin_b + count_b) of every sequence b (host only,
+ * no CUDA call).  Token t of a call (0 <= t < T = sum_b count_b) is the t-th of those rows,
+ * sequence by sequence.
+ *
+ *   B, Hq, Hkv, d, dtype   as for fd_plan, with any group Hq / Hkv and with d = 64 as well
+ *                          for FD_F16_E4M3KV
+ *   seqlens       host array [B]: the lengths L_b that the cache is laid out for, the new
+ *                 tokens included (the array a following fd_plan takes)
+ *   begin, count  host arrays [B]; 0 <= begin_b, 0 <= count_b, begin_b + count_b <= L_b
+ *   page_size     0: contiguous cache (rows packed as for fd_decode); else as fd_plan_paged
+ *   out_rows      receives the handle; release it with fd_rows_destroy
+ *
+ * The handle is immutable, owns host memory only and may be shared by threads.
+ */
+typedef struct fd_rows_s* fd_rows_t;
+
+int fd_rows_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32_t* begin,
+                 const int32_t* count, int page_size, int dtype, fd_rows_t* out_rows);
+
+/* Release a handle (NULL is accepted).  No CUDA call. */
+int fd_rows_destroy(fd_rows_t rows);
+
+typedef struct fd_rows_info {
+  int64_t tokens;       /* T */
+  int64_t cache_bytes;  /* bytes of K (and of V): of the contiguous cache, or of one page */
+} fd_rows_info;
+
+int fd_rows_get_info(fd_rows_t rows, fd_rows_info* info);
+
+/* A rotary embedding (host memory, read during the call only). */
+typedef struct fd_rope {
+  int32_t rot_dim;        /* elements [0, rot_dim) of a head rotate: a multiple of 16, <= d (of 32
+                             when a 4-bit cache is written); 0 = none */
+  int32_t interleaved;    /* 0: pair i is elements (i, i + rot_dim / 2); 1: (2 i, 2 i + 1) */
+  const double* inv_freq; /* [rot_dim / 2] radians per position of each pair, at most 2^20 in size */
+  const uint8_t* axis;    /* [rot_dim / 2] position axis of each pair, or NULL (axis 0) */
+  int32_t num_axes;       /* 1 .. 4 */
+  float scale;            /* factor on cos and sin (1 for a plain rotation), not 0 */
+} fd_rope;
+
+/* Arguments of fd_append.  Zero the struct, then set what the call uses. */
+typedef struct fd_append_args {
+  /* Inputs [T, heads, d] in dtype's q type; elements of a head contiguous.  Strides in
+   * elements between tokens and between heads: multiples of 8, >= 0. */
+  const void *q, *k, *v;
+  int64_t q_stride[2], k_stride[2], v_stride[2];
+  /* RMS norm of every head of q / k: x * rsqrt(mean x^2 + eps) * (weight + weight_offset).
+   * Weights [d] in the q type; NULL = ones (then without the offset). */
+  int32_t q_norm, k_norm;
+  const void *q_weight, *k_weight;
+  float eps, weight_offset;
+  /* Rotation of q and k after the norm; NULL = none.  positions: device int32
+   * [num_axes][T], pos_stride elements between axes (any value, negative too); NULL (one
+   * axis only) = the row of the token in its sequence. */
+  const fd_rope* rope;
+  const int32_t* positions;
+  int64_t pos_stride;
+  /* Outputs.  q_out [T, Hq, d] and k_out [T, Hkv, d] in the q type, contiguous; each may be
+   * its own input where that is contiguous too.  The caches: see fd_decode and
+   * fd_decode_paged; rows other than the handle's stay as they were.  NULL = not written. */
+  void *q_out, *k_out;
+  void *k_cache, *v_cache;
+  /* Factors on k and v before they are stored in an E4M3 or 4-bit cache; 1 for 16 bits. */
+  float k_mul, v_mul;
+  /* Paged caches. */
+  int32_t num_pages, bt_stride;
+  const int32_t* block_table;
+  /* Device word or NULL: bit 0 is set (never cleared) when a page index was outside the pool. */
+  uint32_t* status;
+} fd_append_args;
+
+/*
+ * fd_append -- norm, rotation and store of the handle's tokens (one launch on `stream`).
+ *
+ * q_out = rotate(norm(q)); k_out and the K cache = rotate(norm(k)); the V cache = v.  The
+ * arithmetic is fp32, the angle position x inv_freq is off by at most 2^-25 half turns for
+ * every int32 position, and a value is rounded once, where it is stored:
+ *   16 bits   to nearest, ties to even
+ *   E4M3      x mul to nearest, saturating at 448 (NaN stays NaN)
+ *   4 bits    per block of 16 elements y = x mul: scale = E4M3(max |y| / 6), code =
+ *             E2M1(y / scale), both to nearest, ties to even, saturating; codes are 0 where
+ *             the scale rounds to 0 (max |y| <= 6 x 2^-10), and a NaN in a block makes its
+ *             scale, and so all 16 values, NaN
+ *
+ * q and q_out come together, v and v_cache, k_cache and v_cache too; k with k_out or k_cache.
+ * The pages of a call's rows must differ from each other (two rows that share a place in the
+ * pool leave either's bytes there).  A row whose page index lies outside [0, num_pages) is not
+ * stored in the cache (q_out and k_out are).  T = 0 launches nothing.
+ *
+ * FD_ERR_INVALID: a missing pointer, a negative stride, an output that overlaps an input (but
+ * for the in-place case), bt_stride < ceil(L_b / page_size), a bad rope or factor.
+ * FD_ERR_ALIGN: a device pointer not 16-byte aligned (positions, block_table, status: 4) or a
+ * stride not a multiple of 8.  FD_ERR_UNSUPPORTED: rot_dim, num_pages * page_size >= 2^31.
+ * Asynchronous; launched with programmatic dependent launch like fd_decode.
+ */
+int fd_append(fd_rows_t rows, const fd_append_args* args, cudaStream_t stream);
+
+/*
+ * fd_gather -- the handle's rows of K and V read back from a cache of any dtype into
+ * contiguous tensors of the q type (one launch on `stream`).  Every stored value is exact in
+ * the q type.
+ *
+ *   k_cache, v_cache, num_pages, block_table, bt_stride, status   as for fd_append
+ *   k_out, v_out   device [T, Hkv, d] in the q type, contiguous, not overlapping the caches
+ *
+ * A row whose page index lies outside [0, num_pages) reads zeros.  Errors as for fd_append.
+ */
+int fd_gather(fd_rows_t rows, const void* k_cache, const void* v_cache, int num_pages,
+              const int32_t* block_table, int bt_stride, void* k_out, void* v_out,
+              uint32_t* status, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fd_strerror(int status);
 
@@ -327,7 +467,8 @@ typedef struct fd_plan_info {
   uint64_t workspace_bytes;
   uint64_t kv_bytes;       /* bytes of K and V one decode reads */
   int32_t path;            /* 0: CUDA-core (FFMA) consumers, 1: tensor-core (mma.sync),
-                              2: tensor-core over an E4M3 cache, 3: tcgen05 tensor cores */
+                              2: tensor-core over an E4M3 cache, 3: tcgen05 tensor cores,
+                              4: tensor-core over a 4-bit cache */
   int32_t records_per_segment; /* partial records per segment: 1 (chunks merged in a
                                   cluster) or chunks */
   int32_t combine_cluster; /* CTAs per cluster that combine a pair's partials in shared

@@ -21,3 +21,11 @@ from .fd_oracle import (  # noqa: F401
     split_kv_decode,
     widen,
 )
+from .fd_rows_oracle import (  # noqa: F401
+    dequantise,
+    nearest_code,
+    norm_rotate,
+    pack_blocks,
+    quantise,
+    unpack_blocks,
+)

@@ -25,6 +25,8 @@ FD_ERR_TIMEOUT = -7
 FD_F16 = 0
 FD_BF16 = 1
 FD_F16_E4M3KV = 2
+FD_F16_E2M1KV = 4
+FD_BF16_E2M1KV = 5
 FD_PLAN_LITERAL_W = 0x1
 FD_PLAN_DEBUG = 0x2
 FD_PLAN_TWO_LAUNCH = 0x4
@@ -48,13 +50,15 @@ FD_PLAN_SINGLE_COMBINER = FD_PLAN_COMBINERS[1]
 FD_MAX_BATCH = 256
 FD_MAX_PARTIALS = 1024
 
-DTYPES = {"f16": FD_F16, "bf16": FD_BF16, "f16_e4m3kv": FD_F16_E4M3KV}
+DTYPES = {"f16": FD_F16, "bf16": FD_BF16, "f16_e4m3kv": FD_F16_E4M3KV,
+          "f16_e2m1kv": FD_F16_E2M1KV, "bf16_e2m1kv": FD_BF16_E2M1KV}
 
 # Every symbol include/fd.h declares.
 EXPORTED = (
     "fd_plan", "fd_plan_destroy", "fd_workspace_bytes", "fd_workspace_init", "fd_decode",
     "fd_workspace_status", "fd_strerror", "fd_plan_get_info", "fd_plan_get_range", "fd_version",
     "fd_decode_noalloc", "fd_noalloc_status", "fd_plan_paged", "fd_decode_paged",
+    "fd_rows_plan", "fd_rows_destroy", "fd_rows_get_info", "fd_append", "fd_gather",
 )
 FD_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -76,6 +80,37 @@ class PlanInfo(ctypes.Structure):
         ("path", ctypes.c_int32), ("records_per_segment", ctypes.c_int32),
         ("combine_cluster", ctypes.c_int32), ("combiners", ctypes.c_int32),
         ("ctas_per_sm", ctypes.c_int32),
+    ]
+
+
+class RowsInfo(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("cache_bytes", ctypes.c_int64)]
+
+
+class RopeArgs(ctypes.Structure):
+    """fd_rope."""
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("inv_freq", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+        ("num_axes", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class AppendArgs(ctypes.Structure):
+    """fd_append_args."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2),
+        ("v_stride", ctypes.c_int64 * 2),
+        ("q_norm", ctypes.c_int32), ("k_norm", ctypes.c_int32),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+        ("rope", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("pos_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("k_mul", ctypes.c_float), ("v_mul", ctypes.c_float),
+        ("num_pages", ctypes.c_int32), ("bt_stride", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p), ("status", ctypes.c_void_p),
     ]
 
 
@@ -129,6 +164,19 @@ def lib() -> ctypes.CDLL:
             L.fd_decode_noalloc.restype = ctypes.c_int
             L.fd_noalloc_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
             L.fd_noalloc_status.restype = ctypes.c_int
+            L.fd_rows_plan.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                       ctypes.POINTER(i32), ctypes.POINTER(i32),
+                                       ctypes.POINTER(i32), ctypes.c_int, ctypes.c_int,
+                                       ctypes.POINTER(vp)]
+            L.fd_rows_plan.restype = ctypes.c_int
+            L.fd_rows_destroy.argtypes = [vp]
+            L.fd_rows_destroy.restype = ctypes.c_int
+            L.fd_rows_get_info.argtypes = [vp, ctypes.POINTER(RowsInfo)]
+            L.fd_rows_get_info.restype = ctypes.c_int
+            L.fd_append.argtypes = [vp, ctypes.POINTER(AppendArgs), vp]
+            L.fd_append.restype = ctypes.c_int
+            L.fd_gather.argtypes = [vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, vp]
+            L.fd_gather.restype = ctypes.c_int
             L.fd_version.argtypes = []
             L.fd_version.restype = ctypes.c_int
             _lib = L
@@ -282,6 +330,64 @@ def fd_plan_get_range(plan: Plan, b: int, slot: int):
     _check(lib().fd_plan_get_range(plan.handle, int(b), int(slot), ctypes.byref(lo),
                                    ctypes.byref(hi)), "fd_plan_get_range")
     return lo.value, hi.value
+
+
+class Rows:
+    """Owns one fd_rows_t handle (fd_rows_destroy on close / garbage collection)."""
+
+    def __init__(self, handle: int):
+        self.handle = handle
+        info = RowsInfo()
+        _check(lib().fd_rows_get_info(handle, ctypes.byref(info)), "fd_rows_get_info")
+        self.tokens, self.cache_bytes = info.tokens, info.cache_bytes
+
+    def close(self) -> None:
+        if self.handle:
+            lib().fd_rows_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def fd_rows_plan(B, Hq, Hkv, d, seqlens, begin, count, page_size=0, dtype="f16") -> Rows:
+    """fd_rows_plan: the rows [begin_b, begin_b + count_b) of every sequence (host only)."""
+    seqlens, begin, count = list(seqlens), list(begin), list(count)
+    if len(seqlens) != B or len(begin) != B or len(count) != B:
+        raise FdError(FD_ERR_INVALID, "fd_rows_plan: seqlens, begin and count need B entries")
+    handle = ctypes.c_void_p()
+    rc = lib().fd_rows_plan(int(B), int(Hq), int(Hkv), int(d), _i32_array(seqlens, B),
+                            _i32_array(begin, B), _i32_array(count, B), int(page_size),
+                            DTYPES[dtype] if isinstance(dtype, str) else int(dtype),
+                            ctypes.byref(handle))
+    _check(rc, "fd_rows_plan")
+    return Rows(handle.value)
+
+
+def fd_rows_destroy(rows: Rows) -> None:
+    rows.close()
+
+
+def fd_rows_get_info(rows: Rows) -> dict:
+    info = RowsInfo()
+    _check(lib().fd_rows_get_info(rows.handle, ctypes.byref(info)), "fd_rows_get_info")
+    return {"tokens": info.tokens, "cache_bytes": info.cache_bytes}
+
+
+def fd_append(rows: Rows, args: AppendArgs, stream=None) -> None:
+    """fd_append: norm, rotation and store of the handle's tokens (one launch)."""
+    _check(lib().fd_append(rows.handle, ctypes.byref(args), _stream(stream)), "fd_append")
+
+
+def fd_gather(rows: Rows, k_cache, v_cache, num_pages, block_table, bt_stride, k_out, v_out,
+              status=None, stream=None) -> None:
+    """fd_gather: the handle's rows of K and V back in 16 bits (one launch)."""
+    _check(lib().fd_gather(rows.handle, _ptr(k_cache), _ptr(v_cache), int(num_pages),
+                           _ptr(block_table), int(bt_stride), _ptr(k_out), _ptr(v_out),
+                           _ptr(status), _stream(stream)), "fd_gather")
 
 
 def fd_version() -> int:

@@ -64,17 +64,21 @@ int fd::encode_kv_map(CUtensorMap* map, const void* base, int64_t rows, int box_
                       const fd_plan_s* pl) {
   auto enc = tensor_map_encoder();
   if (!enc) return FD_ERR_CUDA;
-  const int es = fd::kv_elem_bytes(pl->path);
-  const cuuint64_t dims[3] = {(cuuint64_t)pl->d, (cuuint64_t)pl->Hkv, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)pl->d * es, (cuuint64_t)pl->Hkv * pl->d * es};
+  const bool kv4 = pl->path == fd::kPathMmaKv4;
+  const int rt = fd::row_tokens(pl->path);
+  const cuuint64_t row = (cuuint64_t)fd::kv_row_bytes(pl->path, pl->d) * rt;
+  const cuuint64_t dims[3] = {(cuuint64_t)(kv4 ? 9 * pl->d / 8 : pl->d),
+                              (cuuint64_t)pl->Hkv, (cuuint64_t)(rows / rt)};
+  const cuuint64_t strides[2] = {row, (cuuint64_t)pl->Hkv * row};
   const cuuint32_t box[3] = {(cuuint32_t)fd::box_cols_for(pl->path, pl->d), 1u,
-                             (cuuint32_t)box_rows};
+                             (cuuint32_t)(box_rows / rt)};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUtensorMapDataType ty = pl->dtype == FD_F16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : pl->dtype == FD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                 : kv4                  ? CU_TENSOR_MAP_DATA_TYPE_UINT64
                                                         : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const CUtensorMapSwizzle swz =
-      fd::is_mma(pl->path) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+      fd::is_mma(pl->path) && !kv4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
   CUresult r = enc(map, ty, 3, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -120,7 +124,8 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
   if (!seqlens || !W) return FD_ERR_INVALID;
   if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || chunks < 0 || num_sms < 0) return FD_ERR_INVALID;
   if (Hq % Hkv != 0) return FD_ERR_INVALID;
-  if (dtype != FD_F16 && dtype != FD_BF16 && dtype != FD_F16_E4M3KV) return FD_ERR_INVALID;
+  const bool kv4 = dtype == FD_F16_E2M1KV || dtype == FD_BF16_E2M1KV;
+  if (dtype != FD_F16 && dtype != FD_BF16 && dtype != FD_F16_E4M3KV && !kv4) return FD_ERR_INVALID;
   if (flags & ~(FD_PLAN_LITERAL_W | FD_PLAN_DEBUG | FD_PLAN_TWO_LAUNCH | FD_PLAN_FFMA |
                 FD_PLAN_NO_PDL | FD_PLAN_WAITS | FD_PLAN_TEST_DROP_FLAG |
                 FD_PLAN_NO_CLUSTER | FD_PLAN_CLUSTER | FD_PLAN_TEST_SKIP_TILE | FD_PLAN_TCGEN05 |
@@ -151,8 +156,9 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
   if (dtype == FD_F16_E4M3KV && (d != 128 || G < 4 || (flags & FD_PLAN_FFMA)))
     return FD_ERR_UNSUPPORTED;
   if ((flags & FD_PLAN_TCGEN05) &&
-      (dtype == FD_F16_E4M3KV || d != 128 || G < 4 || (flags & (FD_PLAN_FFMA | FD_PLAN_MMA_SYNC))))
+      (dtype == FD_F16_E4M3KV || kv4 || d != 128 || G < 4 || (flags & (FD_PLAN_FFMA | FD_PLAN_MMA_SYNC))))
     return FD_ERR_UNSUPPORTED;
+  if (kv4 && (flags & FD_PLAN_FFMA)) return FD_ERR_UNSUPPORTED;  // tensor cores only
   if ((flags & FD_PLAN_MMA_SYNC) && (flags & FD_PLAN_FFMA)) return FD_ERR_INVALID;
   // Tensor cores whenever the GQA group covers at least half of the mma N = 8 tile:
   // mma.sync by default, tcgen05 when asked for.  tcgen05 was the default for G = 16
@@ -161,16 +167,18 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
   // (128 CTAs, one per SM), the same box, three runs each.
   const bool umma = (flags & FD_PLAN_TCGEN05) != 0;
   const int path = dtype == FD_F16_E4M3KV                 ? fd::kPathMmaKv8
+                   : kv4                                  ? fd::kPathMmaKv4
                    : umma                                 ? fd::kPathUmma
                    : (G >= 4 && !(flags & FD_PLAN_FFMA)) ? fd::kPathMma
                                                          : fd::kPathFfma;
 
-  int64_t n_tokens = 0, sum_w = 0;
+  int64_t n_tokens = 0, n_blocks = 0, sum_w = 0;
   int max_w = 0;
   for (int b = 0; b < B; ++b) {
     if (seqlens[b] < 0 || W[b] < 1) return FD_ERR_INVALID;
     if (W[b] > FD_MAX_PARTIALS) return FD_ERR_UNSUPPORTED;
     n_tokens += seqlens[b];
+    n_blocks += ((int64_t)seqlens[b] + fd::kBlockTokens - 1) / fd::kBlockTokens;
     sum_w += W[b];
     max_w = std::max(max_w, (int)W[b]);
   }
@@ -232,6 +240,7 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
       pl->max_pages = std::max(pl->max_pages, (seqlens[b] + page_size - 1) / page_size);
   pl->max_partials = max_w * C;
   pl->n_tokens = n_tokens;
+  pl->n_blocks = n_blocks;
   pl->total_partials = (int64_t)Hq * sum_w * C;
   pl->ctas = (int)ctas;
 
@@ -262,7 +271,8 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
   // they arrive.
   const int64_t rec_bytes = (int64_t)G / nc * max_w * C * fd::record_floats(d) * 4;
   const int64_t ring = (int64_t)fd::ring_bytes_for(pl->path, d, fd::ctas_per_sm_for(path));
-  const bool multi_pass = rec_bytes > (pl->path == fd::kPathMmaKv8 ? 2 : 1) * ring;
+  const bool multi_pass =
+      rec_bytes > (pl->path == fd::kPathMmaKv8 || pl->path == fd::kPathMmaKv4 ? 2 : 1) * ring;
   p.rps = ((multi_pass || (flags & FD_PLAN_CLUSTER)) && C > 1 && C <= kMaxCluster &&
            !(flags & (FD_PLAN_WAITS | FD_PLAN_NO_CLUSTER | FD_PLAN_CLUSTER_COMBINE))) ? 1 : C;
   if (p.rps != C) nc = 1;
@@ -270,7 +280,7 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
   // Many short CTAs on the fused mma.sync path, G <= 8 (more CTAs than two per SM,
   // at most kShallowMaxCtaBytes of K/V each): three CTAs per SM with 64 KB rings.
   {
-    const int64_t kv_bytes = n_tokens * Hkv * d * 2 * fd::kv_elem_bytes(path);
+    const int64_t kv_bytes = n_tokens * Hkv * 2 * fd::kv_row_bytes(path, d);
     const int64_t slots = (int64_t)num_sms * fd::ctas_per_sm_for(path);
     const int64_t wt = (int64_t)max_w * C;
     const bool shallow =
@@ -285,12 +295,15 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
   p.prefetch_ctas = (int32_t)std::min<int64_t>(ctas, (int64_t)num_sms * p.ctas_per_sm);
   p.pair_cluster = pair ? W[0] * C : 0;
   // Paged caches: boundaries on whole tiles, so that every TMA box stays in one page.
-  p.align = page_size ? fd::tile_for(pl->path) : 1;
+  // Contiguous 4-bit caches: boundaries on whole blocks.
+  p.align = page_size ? fd::tile_for(pl->path) : fd::row_tokens(pl->path);
   p.box_rows = page_size ? std::min(fd::tile_for(pl->path), page_size) : fd::tile_for(pl->path);
   p.page_shift = 0;
   while (page_size && (1 << p.page_shift) < page_size) ++p.page_shift;
-  int32_t cu = 0, ub = 0;
+  int32_t cu = 0, ub = 0, blk = 0;
   for (int b = 0; b < B; ++b) {
+    p.blk[b] = blk;
+    blk += (int32_t)(((int64_t)seqlens[b] + fd::kBlockTokens - 1) / fd::kBlockTokens);
     p.cu[b] = cu;
     p.unit_base[b] = ub;
     p.wseg[b] = (uint16_t)W[b];
@@ -345,7 +358,7 @@ int fd_plan_get_info(fd_plan_t pl, fd_plan_info* info) {
   info->num_sms = pl->num_sms; info->ctas = pl->ctas; info->max_partials = pl->max_partials;
   info->total_tokens = pl->n_tokens; info->total_partials = pl->total_partials;
   info->workspace_bytes = pl->ws_bytes;
-  info->kv_bytes = (uint64_t)pl->n_tokens * pl->Hkv * pl->d * 2 * fd::kv_elem_bytes(pl->path);
+  info->kv_bytes = (uint64_t)pl->n_tokens * pl->Hkv * 2 * fd::kv_row_bytes(pl->path, pl->d);
   info->path = pl->path;
   info->records_per_segment = pl->params.rps;
   info->combine_cluster = pl->params.pair_cluster;
@@ -462,7 +475,7 @@ extern "C" {
 int fd_decode(fd_plan_t pl, const void* q, const void* k, const void* v, void* out, float* lse,
               void* workspace, cudaStream_t stream) {
   if (pl && pl->page_size != 0) return FD_ERR_INVALID;  // paged plans use fd_decode_paged
-  return decode_impl(pl, q, k, v, pl ? pl->n_tokens : 0, nullptr, 0, out, lse, workspace, stream);
+  return decode_impl(pl, q, k, v, pl ? fd::contiguous_rows(pl) : 0, nullptr, 0, out, lse, workspace, stream);
 }
 
 int fd_decode_paged(fd_plan_t pl, const void* q, const void* k_pages, const void* v_pages,

@@ -35,19 +35,45 @@ constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kPathFfma = 0;
 constexpr int kPathMma = 1;
 constexpr int kPathMmaKv8 = 2;
+// KV4: the MMA path over a 4-bit cache (E2M1 elements, one E4M3 scale per 16), d = 64 or
+// 128 and every G: blocks of 16 tokens of one KV head (fd.h, "4-bit blocks") land in the
+// ring as they are; every thread widens its mma fragments to f16 and multiplies them by
+// their scales, both exact.
 constexpr int kPathUmma = 3;
+constexpr int kPathMmaKv4 = 4;
 
 FD_HD constexpr bool is_mma(int path) { return path != kPathFfma; }
-// Bytes per stored K/V element.
-FD_HD constexpr int kv_elem_bytes(int path) { return path == kPathMmaKv8 ? 1 : 2; }
+// Bytes of the K (or V) row of one token and KV head.
+FD_HD constexpr int kv_row_bytes(int path, int d) {
+  return path == kPathMmaKv4 ? d * 9 / 16 : path == kPathMmaKv8 ? d : 2 * d;
+}
+// Tokens per row of the TMA view: a 4-bit cache is made of blocks of 16 tokens.
+constexpr int kBlockTokens = 16, kBlockShift = 4;
+FD_HD constexpr int row_tokens(int path) { return path == kPathMmaKv4 ? kBlockTokens : 1; }
 // Tokens per pipeline stage.
 // (FP8: 128-token tiles, two 16-token groups per consumer warp per stage.)
 FD_HD constexpr int tile_for(int path) {
-  return (path == kPathUmma || path == kPathMmaKv8) ? 128 : is_mma(path) ? 64 : 32;
+  return (path == kPathUmma || path == kPathMmaKv8 || path == kPathMmaKv4) ? 128
+         : is_mma(path)                                                    ? 64
+                                                                           : 32;
 }
-// Columns (elements) of one TMA box row: 128-byte swizzled rows on the MMA paths.
+// Bytes of that row in the ring.  A TMA box has to start on a multiple of 128 bytes of shared
+// memory, and with pages of 16 tokens every 4-bit block is a box of its own: a d = 64 block of
+// 576 bytes takes 640 there (the box is wider than the tensor; TMA fills the rest with zeros).
+FD_HD constexpr int ring_row_bytes(int path, int d) {
+  return path == kPathMmaKv4 ? (9 * d + 127) / 128 * 128 / kBlockTokens : kv_row_bytes(path, d);
+}
+// Columns (elements) of one TMA box row: 128-byte swizzled rows on the MMA paths (4-bit
+// blocks: the whole block as it lies in the ring, as 8-byte elements).
 FD_HD constexpr int box_cols_for(int path, int d) {
-  return (path == kPathMma || path == kPathUmma) ? 64 : path == kPathMmaKv8 ? 128 : d;
+  return path == kPathMmaKv4                         ? ring_row_bytes(path, d) * kBlockTokens / 8
+         : (path == kPathMma || path == kPathUmma) ? 64
+         : path == kPathMmaKv8                     ? 128
+                                                   : d;
+}
+// TMA boxes per tensor and tile (when one box holds the tile's rows).
+FD_HD constexpr int boxes_for(int path, int d) {
+  return path == kPathMmaKv4 ? 1 : d / box_cols_for(path, d);
 }
 // Ring slots per tile: the tcgen05 path keeps K and V of a tile in separate slots
 // (the K slot is released when S^T is computed, the V slot after P.V).
@@ -73,11 +99,14 @@ FD_HD constexpr int ctas_per_sm_for(int path) { return path == kPathUmma ? 1 : 2
 // tokens per CTA, and every one-wave plan, slower.)
 constexpr int kShallowCtasPerSm = 3;
 constexpr int kShallowRingBytes = 64 * 1024;
+// CTAs per SM that the split kernels of a path are built for, short CTAs aside.  (tcgen05:
+// the registers of two, though only one is resident.)
+FD_HD constexpr int build_ctas_for(int path) { return path == kPathUmma ? 2 : ctas_per_sm_for(path); }
 FD_HD constexpr int ring_target_bytes(int path, int cps) {
   return path == kPathUmma ? 2 * kRingBytes : cps == kShallowCtasPerSm ? kShallowRingBytes : kRingBytes;
 }
 FD_HD constexpr int slot_bytes_for(int path, int d) {
-  return (2 / loads_per_tile(path)) * tile_for(path) * d * kv_elem_bytes(path);
+  return (2 / loads_per_tile(path)) * tile_for(path) * ring_row_bytes(path, d);
 }
 // `cps`: resident CTAs per SM the kernel is built for (ctas_per_sm_for, or
 // kShallowCtasPerSm).
@@ -162,6 +191,7 @@ struct Params {
   int32_t cu[FD_MAX_BATCH + 1];         // token prefix sums
   int32_t unit_base[FD_MAX_BATCH + 1];  // prefix sums of Hkv * W_b * C (CTA index base)
   uint16_t wseg[FD_MAX_BATCH];          // W_b
+  int32_t blk[FD_MAX_BATCH];            // contiguous 4-bit caches: first block of each sequence
 };
 static_assert(sizeof(Params) <= 4096, "kernel parameters must stay within 4 KB");
 
@@ -200,6 +230,10 @@ cudaError_t launch_f16_ffma(const Params& p, int d, int G, int mode, bool pdl, i
                             cudaStream_t s);
 cudaError_t launch_bf16_ffma(const Params& p, int d, int G, int mode, bool pdl, int grid,
                              cudaStream_t s);
+cudaError_t launch_kv4_f16(const Params& p, int d, int G, int mode, bool pdl, int grid,
+                           cudaStream_t s);
+cudaError_t launch_kv4_bf16(const Params& p, int d, int G, int mode, bool pdl, int grid,
+                            cudaStream_t s);
 cudaError_t launch_umma_f16(const Params& p, int d, int G, int mode, bool pdl, int grid,
                             cudaStream_t s);
 cudaError_t launch_umma_bf16(const Params& p, int d, int G, int mode, bool pdl, int grid,

@@ -24,6 +24,8 @@
 //       MMA over an E4M3 cache (fp16 q/out): the same mma.sync, fragments
 //            loaded straight from the byte rows and widened in registers by the
 //            hardware E4M3 -> f16 conversion.
+//       MMA over a 4-bit cache (fp16 or bf16 q/out, every G): the same, with the E2M1
+//            conversion and one exact multiplication by the block scales.
 //       FFMA (G <= 2, or forced): lanes form groups of LPT lanes, a group owns
 //            one token at a time, scores use FFMA plus an xor-shuffle reduction.
 //     Each warp (MMA) or token group (FFMA) keeps its own running (m, l, acc)
@@ -284,6 +286,33 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t& lo, uint32
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(x));
+}
+
+// Eight E2M1 values (the half-bytes of x, low half first) widened to four f16 pairs.
+__device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t x, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(x));
+}
+// Two E4M3 values (bytes 0 and 1 of x) widened to an f16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+      : "=r"(r)
+      : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Two fp32 values rounded (RN) to one packed 16-bit pair: lo in bits 0-15.
@@ -1047,7 +1076,7 @@ __device__ __forceinline__ void finish_cta(const Params& p, const Work& wk, floa
 // that combines them through distributed shared memory.
 // CPS: resident CTAs per SM the kernel is built for; 3 (kShallowCtasPerSm) gives it
 // the 64 KB ring of plans of many short CTAs (mma.sync path, fused), else 2.
-template <typename T, int D, int G, int PATH, int MODE, int CPS = 2>
+template <typename T, int D, int G, int PATH, int MODE, int CPS = build_ctas_for(PATH)>
 __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_constant__ Params p) {
   constexpr bool kSeg = MODE == 4 || MODE == 5;
   constexpr bool kPair = MODE == 6;
@@ -1056,18 +1085,21 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
   constexpr int LPT = loads_per_tile(PATH);       // ring slots per tile (2: K and V apart)
   constexpr int NSLOT = ring_slots_for(PATH, D, CPS);  // ring slots
   constexpr int BOXC = box_cols_for(PATH, D);   // columns per TMA box
-  constexpr int NBOX = D / BOXC;                // boxes per tensor per stage
-  constexpr int KVES = kv_elem_bytes(PATH);     // bytes per stored K/V element
-  constexpr uint32_t kRowsBytes = TILE * D * KVES;  // one tile of K (or V) rows
+  constexpr int NBOX = boxes_for(PATH, D);      // boxes per tensor per stage
+  constexpr int RT = row_tokens(PATH);          // tokens per row of the TMA view
+  constexpr int kBoxRowBytes = ring_row_bytes(PATH, D) / NBOX;  // one token row of one box
+  constexpr uint32_t kRowsBytes = TILE * ring_row_bytes(PATH, D);  // one tile of K (or V) rows
   constexpr uint32_t kSlotBytes = (2 / LPT) * kRowsBytes;  // K rows then V rows, or one of them
   constexpr uint32_t kRing = NSLOT * kSlotBytes;
   constexpr uint32_t kExtra = extra_bytes_for(PATH);
-  static_assert(NSLOT >= 2 && kRowsBytes % 1024 == 0, "slots hold whole swizzle atoms");
+  static_assert(NSLOT >= 2 && kRowsBytes % (PATH == kPathMmaKv4 ? 128 : 1024) == 0,
+                "slots hold whole swizzle atoms");
   static_assert((2 * NSLOT + 5 + kCombineBars) * 8 + 1024 <= kRingMetaBytes, "ring metadata must fit");
   static_assert(kRing == ring_bytes_for(PATH, D, CPS), "ring layout");
   constexpr int NGRP_FFMA = kConsumerWarps * (32 / ((G * D > 512) ? 16 : 8));
   constexpr int NGRP = PATH == kPathUmma ? 1 : is_mma(PATH) ? kConsumerWarps : NGRP_FFMA;
-  static_assert(PATH == kPathFfma || G >= 4, "the MMA path needs G >= 4 heads on N");
+  static_assert(PATH == kPathFfma || PATH == kPathMmaKv4 || G >= 4,
+                "the MMA path needs G >= 4 heads on N");
   static_assert(NGRP * G * D * 4 + 4 * NGRP * G * 4 + 3 * G * 4 + G * record_floats(D) * 4 <= kRing,
                 "group merge and the segment-merge record must fit in the ring");
 
@@ -1122,12 +1154,12 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
     if ((int)blockIdx.x < p.prefetch_ctas) {
       const int npf = min(ntiles, kL2PrefetchTokens / TILE);
       if (p.block_table == nullptr) {
-        const int row0 = p.cu[wk.b] + wk.t0;
+        const int row0 = RT == 1 ? p.cu[wk.b] + wk.t0 : p.blk[wk.b] + wk.t0 / RT;
         for (int kt = 0; kt < npf; ++kt) {
 #pragma unroll
           for (int bx = 0; bx < NBOX; ++bx) {
-            tma_prefetch_l2_3d(&p.tm_k, bx * BOXC, wk.kvh, row0 + kt * TILE);
-            tma_prefetch_l2_3d(&p.tm_v, bx * BOXC, wk.kvh, row0 + kt * TILE);
+            tma_prefetch_l2_3d(&p.tm_k, bx * BOXC, wk.kvh, row0 + kt * (TILE / RT));
+            tma_prefetch_l2_3d(&p.tm_v, bx * BOXC, wk.kvh, row0 + kt * (TILE / RT));
           }
         }
       } else if (p.box_rows == TILE) {
@@ -1148,8 +1180,8 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
             const int row = pg * (1 << p.page_shift) + ((a + r) & ((1 << p.page_shift) - 1));
 #pragma unroll
             for (int bx = 0; bx < NBOX; ++bx) {
-              tma_prefetch_l2_3d(&p.tm_k, bx * BOXC, wk.kvh, row);
-              tma_prefetch_l2_3d(&p.tm_v, bx * BOXC, wk.kvh, row);
+              tma_prefetch_l2_3d(&p.tm_k, bx * BOXC, wk.kvh, RT == 1 ? row : row >> kBlockShift);
+              tma_prefetch_l2_3d(&p.tm_v, bx * BOXC, wk.kvh, RT == 1 ? row : row >> kBlockShift);
             }
           }
         }
@@ -1169,7 +1201,7 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
     // ---------------- TMA producer ----------------
     if (lane == 0 && ntiles > 0) {
       const uint64_t policy = l2_evict_first_policy();
-      const int row0 = p.cu[wk.b] + wk.t0;
+      const int row0 = RT == 1 ? p.cu[wk.b] + wk.t0 : p.blk[wk.b] + wk.t0 / RT;
       // Load j goes to slot j mod NSLOT.  One load per tile: its K rows, then its V
       // rows; two loads per tile (tcgen05 path): K rows (j even), then V rows.
       const int nload = ntiles * LPT;
@@ -1192,9 +1224,9 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
           for (int h = h0; h < h1; ++h) {  // K rows, then V rows
 #pragma unroll
             for (int bx = 0; bx < NBOX; ++bx)
-              tma_load_3d(dst + (h - h0) * kRowsBytes + bx * (TILE * BOXC * KVES),
-                          h ? &p.tm_v : &p.tm_k, bx * BOXC, wk.kvh, row0 + kt * TILE, full_bar(s),
-                          policy);
+              tma_load_3d(dst + (h - h0) * kRowsBytes + bx * (TILE * kBoxRowBytes),
+                          h ? &p.tm_v : &p.tm_k, bx * BOXC, wk.kvh, row0 + kt * (TILE / RT),
+                          full_bar(s), policy);
           }
         } else {
           // Paged: one box per page piece of the tile.  Tiles start on multiples of
@@ -1210,8 +1242,9 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
             for (int h = h0; h < h1; ++h) {  // K rows, then V rows
 #pragma unroll
               for (int bx = 0; bx < NBOX; ++bx)
-                tma_load_3d(dst + (h - h0) * kRowsBytes + bx * (TILE * BOXC * KVES) + r * BOXC * KVES,
-                            h ? &p.tm_v : &p.tm_k, bx * BOXC, wk.kvh, row, full_bar(s), policy);
+                tma_load_3d(dst + (h - h0) * kRowsBytes + bx * (TILE * kBoxRowBytes) + r * kBoxRowBytes,
+                            h ? &p.tm_v : &p.tm_k, bx * BOXC, wk.kvh,
+                            RT == 1 ? row : row >> kBlockShift, full_bar(s), policy);
             }
           }
         }
@@ -1675,6 +1708,281 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
         }
       }
     }
+  } else if constexpr (PATH == kPathMmaKv4) {
+    // ---------------- MMA consumers over a 4-bit (E2M1) cache ----------------
+    // The tile is 8 blocks of 16 tokens.  As on the E4M3 path, index permutations make
+    // each thread's fragment bytes contiguous: thread quad t covers elements
+    // t D/4 + 4 kk + {0, 1} (a0/a1/b0) and + {2, 3} (a2/a3/b1) in k-step kk of S = K q^T;
+    // row g / g + 8 of m-tile mi of O^T is dim g D/8 + 2 mi / + 1.  An element is E2M1 value
+    // x E4M3 scale, at most 6 significant bits and 2^-10 .. 2688 in size: exact in f16, so
+    // both products run on f16 mma whatever q's type.  bf16 q is brought to f16 range by a
+    // power of two per head (its 8 significant bits stay; elements below 2^-14 of the
+    // head's largest lose at most 2^-25 of it, the size of fp32's own rounding).
+    constexpr int KT = D / 16;              // k-steps of S, m-tiles of O^T
+    constexpr int NT = G >= 8 ? G / 8 : 1;  // N tiles of 8 query heads
+    constexpr int NW = D / 64;              // K words (of 8 elements) per thread and row, x 2
+    constexpr int BLK = 16 * ring_row_bytes(PATH, D);  // bytes between blocks in the ring
+    static_assert(BLK % 128 == 0, "every block can be the destination of a TMA box");
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    const int g = lane >> 2, t = lane & 3, qcol = 2 * t;
+    uint32_t qb[NT][KT][2];
+    float scA[NT], scB[NT];  // log2-domain logit scales of this thread's two heads
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int head = nt * 8 + g;
+      const uint2* qh = reinterpret_cast<const uint2*>(
+          reinterpret_cast<const T*>(p.q) + ((int64_t)wk.b * p.Hq + wk.kvh * G + (head < G ? head : 0)) * D +
+          t * (D / 4));
+      float scale = p.scale_log2;
+      if constexpr (kBf16) {
+        float2 f[KT][2];
+        float mx = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+          const uint2 x = head < G ? qh[kk] : make_uint2(0u, 0u);
+          f[kk][0] = Elem<T>::to_f2(x.x);
+          f[kk][1] = Elem<T>::to_f2(x.y);
+          mx = fmaxf(mx, fmaxf(fmaxf(fabsf(f[kk][0].x), fabsf(f[kk][0].y)),
+                               fmaxf(fabsf(f[kk][1].x), fabsf(f[kk][1].y))));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // Exponent of the largest |q|, kept where 2^e and 2^-e are normal; infinite q: 0.
+        int e = (int)(__float_as_uint(mx) >> 23) - 127;
+        e = e == 128 ? 0 : max(-126, min(126, e));
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+          qb[nt][kk][0] = pack2<__half>(f[kk][0].x * down, f[kk][0].y * down);
+          qb[nt][kk][1] = pack2<__half>(f[kk][1].x * down, f[kk][1].y * down);
+        }
+        scale *= __uint_as_float((uint32_t)(127 + e) << 23);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+          const uint2 x = head < G ? qh[kk] : make_uint2(0u, 0u);
+          qb[nt][kk][0] = x.x;
+          qb[nt][kk][1] = x.y;
+        }
+      }
+      scA[nt] = __shfl_sync(0xffffffffu, scale, 4 * qcol);
+      scB[nt] = __shfl_sync(0xffffffffu, scale, 4 * qcol + 4);
+    }
+    float o[NT][KT][4];
+    // l: sums of the fp32 weights (for lse); lr: of the f16 weights P.V uses (for out).
+    float mA[NT], mB[NT], lA[NT], lB[NT], lrA[NT], lrB[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mi = 0; mi < KT; ++mi) o[nt][mi][0] = o[nt][mi][1] = o[nt][mi][2] = o[nt][mi][3] = 0.f;
+      mA[nt] = mB[nt] = -INFINITY;
+      lA[nt] = lB[nt] = lrA[nt] = lrB[nt] = 0.f;
+    }
+    constexpr int SUB = TILE / (kConsumerWarps * 16);  // blocks of 16 tokens per warp and tile
+    static_assert(SUB * kConsumerWarps * 16 == TILE, "the tile splits into 16-token blocks");
+    const int tok0 = warp * 16 * SUB;
+    // This thread's byte offsets in a block (fd.h, "4-bit blocks").
+    const int k_at = g * (D / 2) + t * (D / 8), ks_at = 8 * D + g * (D / 16) + t * (D / 64);
+    const int vg = g * D, vswap = ((D == 128 ? g : g >> 1) & 1) << 2;
+    const int v_at0 = vg + (t ^ vswap) * (D / 8), v_at1 = vg + ((t + 4) ^ vswap) * (D / 8);
+    const int vs_at = 8 * D + (D == 128 ? g : g >> 1) * 16 + 2 * t;
+
+    for (int kt = 0; kt < ntiles; ++kt) {
+      const int s = kt % NSLOT;
+      const bool ok = mbar_wait(full_bar(s), (kt / NSLOT) & 1);
+      if (__any_sync(0xffffffffu, !ok || *(volatile int*)&sm_abort != 0)) {
+        if (!ok) {
+          atomicOr(p.status, kStatusTimeout);
+          *(volatile int*)&sm_abort = 1;
+        }
+        break;
+      }
+      const int ntok = min(TILE, wk.t1 - (wk.t0 + kt * TILE));
+      if (tok0 < ntok) {
+        const uint8_t* kblk = smem + (size_t)s * kSlotBytes + warp * SUB * BLK;
+        const uint8_t* vblk = kblk + kRowsBytes;
+        float sc[SUB][NT][4];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          // K: rows g and g + 8 of block u; kw words of 8 elements, ks the scales as pairs.
+          uint32_t kw[2][2 * NW], ks[2][NW];
+#pragma unroll
+          for (int rh = 0; rh < 2; ++rh) {
+            const uint8_t* row = kblk + u * BLK + rh * (4 * D) + k_at;
+            const uint8_t* srow = kblk + u * BLK + rh * (D / 2) + ks_at;
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(row);
+              kw[rh][0] = x.x; kw[rh][1] = x.y; kw[rh][2] = x.z; kw[rh][3] = x.w;
+              const uint32_t z = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(srow));
+              ks[rh][0] = __byte_perm(z, z, 0x1010);
+              ks[rh][1] = __byte_perm(z, z, 0x3232);
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(row);
+              kw[rh][0] = x.x; kw[rh][1] = x.y;
+              const uint32_t z = e4m3x2_to_f16x2(*srow);
+              ks[rh][0] = __byte_perm(z, z, 0x1010);
+            }
+          }
+          // Two accumulators (even and odd words) halve the chains of dependent mma.
+          float sd[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[u][nt][i] = sd[nt][i] = 0.f;
+#pragma unroll
+          for (int wi = 0; wi < 2 * NW; ++wi) {  // a word: k-steps 2 wi and 2 wi + 1
+            uint32_t x0[4], x1[4];
+            e2m1x8_to_f16x8(kw[0][wi], x0);
+            e2m1x8_to_f16x8(kw[1][wi], x1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a[4] = {hmul2(x0[2 * h], ks[0][wi >> 1]), hmul2(x1[2 * h], ks[1][wi >> 1]),
+                                     hmul2(x0[2 * h + 1], ks[0][wi >> 1]), hmul2(x1[2 * h + 1], ks[1][wi >> 1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<__half>(h ? sd[nt] : sc[u][nt], a, qb[nt][2 * wi + h][0], qb[nt][2 * wi + h][1]);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[u][nt][i] += sd[nt][i];
+        }
+        uint32_t pb0[SUB][NT], pb1[SUB][NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float sA0[SUB], sB0[SUB], sA1[SUB], sB1[SUB];
+          float xA = -INFINITY, xB = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {
+            // Tokens past the end are selected away: their bytes may be anything.
+            const bool v0 = tok0 + 16 * u + g < ntok, v1 = tok0 + 16 * u + g + 8 < ntok;
+            sA0[u] = v0 ? sc[u][nt][0] * scA[nt] : -INFINITY;
+            sB0[u] = v0 ? sc[u][nt][1] * scB[nt] : -INFINITY;
+            sA1[u] = v1 ? sc[u][nt][2] * scA[nt] : -INFINITY;
+            sB1[u] = v1 ? sc[u][nt][3] * scB[nt] : -INFINITY;
+            xA = fmaxf(xA, fmaxf(sA0[u], sA1[u]));
+            xB = fmaxf(xB, fmaxf(sB0[u], sB1[u]));
+          }
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, off));
+            xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, off));
+          }
+          if (xA > mA[nt] + kRescaleThreshold) {
+            const float corr = ex2(mA[nt] - xA);
+            lA[nt] *= corr;
+            lrA[nt] *= corr;
+#pragma unroll
+            for (int mi = 0; mi < KT; ++mi) { o[nt][mi][0] *= corr; o[nt][mi][2] *= corr; }
+            mA[nt] = xA;
+          }
+          if (xB > mB[nt] + kRescaleThreshold) {
+            const float corr = ex2(mB[nt] - xB);
+            lB[nt] *= corr;
+            lrB[nt] *= corr;
+#pragma unroll
+            for (int mi = 0; mi < KT; ++mi) { o[nt][mi][1] *= corr; o[nt][mi][3] *= corr; }
+            mB[nt] = xB;
+          }
+          // Row tok0 is valid, so the column maxima (and mA, mB) are finite here.
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {
+            const float pA0 = ex2(sA0[u] - mA[nt]), pB0 = ex2(sB0[u] - mB[nt]);
+            const float pA1 = ex2(sA1[u] - mA[nt]), pB1 = ex2(sB1[u] - mB[nt]);
+            lA[nt] += pA0 + pA1;
+            lB[nt] += pB0 + pB1;
+            const uint32_t r0 = pack2<__half>(pA0, pB0), r1 = pack2<__half>(pA1, pB1);
+            // lr sums the same f16 weights that P.V multiplies.
+            const float2 w0 = Elem<__half>::to_f2(r0), w1 = Elem<__half>::to_f2(r1);
+            lrA[nt] += w0.x + w1.x;
+            lrB[nt] += w0.y + w1.y;
+            pb0[u][nt] = movmatrix_trans(r0);
+            pb1[u][nt] = movmatrix_trans(r1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          // V^T: tokens 2t, 2t + 1 (words e[0], scales vs[0]) and 2t + 8, 2t + 9 (e[1], vs[1]).
+          uint32_t ve[2][NW], vo[2][NW], vs[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* at = vblk + u * BLK + (i ? v_at1 : v_at0);
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(at);
+              ve[i][0] = x.x; ve[i][1] = x.y; vo[i][0] = x.z; vo[i][1] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(at);
+              ve[i][0] = x.x; vo[i][0] = x.y;
+            }
+            vs[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(vblk + u * BLK + vs_at + 8 * i));
+            const int left = ntok - (tok0 + 16 * u + 8 * i + 2 * t);  // valid tokens of the pair
+            // A weight of 0 times a NaN scale would be NaN: scales past the end become 0.
+            if (left < 2) vs[i] = left < 1 ? 0u : vs[i] & 0xffffu;
+          }
+#pragma unroll
+          for (int wi = 0; wi < NW; ++wi) {
+            // Half-bytes of the two tokens of a pair side by side: even dims in x, odd in y.
+            uint32_t f[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a = ve[i][wi], b = vo[i][wi];
+              e2m1x8_to_f16x8((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), f[i][0]);
+              e2m1x8_to_f16x8(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), f[i][1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a[4] = {hmul2(f[0][0][j], vs[0]), hmul2(f[0][1][j], vs[0]),
+                                     hmul2(f[1][0][j], vs[1]), hmul2(f[1][1][j], vs[1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<__half>(o[nt][4 * wi + j], a, pb0[u][nt], pb1[u][nt]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(s));
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        lA[nt] += __shfl_xor_sync(0xffffffffu, lA[nt], off);
+        lB[nt] += __shfl_xor_sync(0xffffffffu, lB[nt], off);
+        lrA[nt] += __shfl_xor_sync(0xffffffffu, lrA[nt], off);
+        lrB[nt] += __shfl_xor_sync(0xffffffffu, lrB[nt], off);
+      }
+    }
+    __syncthreads();  // ring drained: reuse it for the per-warp states
+    if (*(volatile int*)&sm_abort == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hA = nt * 8 + qcol;
+        if (hA < G) {
+          float* accA = sm_acc + (warp * G + hA) * D + g * (D / 8);
+#pragma unroll
+          for (int mi = 0; mi < KT; ++mi) {
+            accA[2 * mi] = o[nt][mi][0];
+            accA[2 * mi + 1] = o[nt][mi][2];
+            if (G > 1) {
+              accA[D + 2 * mi] = o[nt][mi][1];
+              accA[D + 2 * mi + 1] = o[nt][mi][3];
+            }
+          }
+          if (g == 0) {
+            sm_m[warp * G + hA] = mA[nt];
+            sm_l[warp * G + hA] = lA[nt];
+            sm_lr[warp * G + hA] = lrA[nt];
+            if (G > 1) {
+              sm_m[warp * G + hA + 1] = mB[nt];
+              sm_l[warp * G + hA + 1] = lB[nt];
+              sm_lr[warp * G + hA + 1] = lrB[nt];
+            }
+          }
+        }
+      }
+    }
   } else if constexpr (PATH == kPathMma) {
     // ---------------- MMA consumers ----------------
     constexpr int KT = D / 16;            // k-steps of S = K Q^T, m-tiles of O^T
@@ -2005,7 +2313,7 @@ template <typename T, int D, int G, int PATH>
 __global__ void __launch_bounds__(kThreads, 2) fd_combine_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw;  // bulk copies need 16-byte alignment only
-  constexpr uint32_t kBytes = (uint32_t)ring_bytes_for(PATH, D, 2);
+  constexpr uint32_t kBytes = (uint32_t)ring_bytes_for(PATH, D, build_ctas_for(PATH));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBytes);  // kCombineBars of them
   static_assert(kCombineBars * 8 <= kRingMetaBytes, "combine barriers fit after the ring");
   pdl_launch_dependents();
@@ -2029,7 +2337,8 @@ cudaError_t launch_dgp(const Params& p, int mode, bool pdl, int grid, cudaStream
   // planner asks for it nowhere else; at G = 16 it would not fit its registers).
   constexpr bool kHasShallow = PATH == kPathMma && G <= 8;
   const bool shallow = kHasShallow && mode == 0 && p.ctas_per_sm == kShallowCtasPerSm;
-  const size_t smem = smem_bytes_for(PATH, D, shallow ? kShallowCtasPerSm : 2);
+  constexpr int kCps = build_ctas_for(PATH);
+  const size_t smem = smem_bytes_for(PATH, D, shallow ? kShallowCtasPerSm : kCps);
   // The split kernels of plans that merge segments in clusters are separate
   // instantiations (kernel modes 4 and 5).
   // Mode 6 (every partial of a pair in one cluster) comes from the host; the split
@@ -2041,7 +2350,7 @@ cudaError_t launch_dgp(const Params& p, int mode, bool pdl, int grid, cudaStream
     case 0: fn = reinterpret_cast<const void*>(&dev::fd_split_kernel<T, D, G, PATH, 0>); break;
     case 7:
       fn = reinterpret_cast<const void*>(
-          &dev::fd_split_kernel<T, D, G, PATH, 0, kHasShallow ? kShallowCtasPerSm : 2>);
+          &dev::fd_split_kernel<T, D, G, PATH, 0, kHasShallow ? kShallowCtasPerSm : kCps>);
       break;
     case 1: fn = reinterpret_cast<const void*>(&dev::fd_split_kernel<T, D, G, PATH, 1>); break;
     case 2: fn = reinterpret_cast<const void*>(&dev::fd_combine_kernel<T, D, G, PATH>); break;
@@ -2122,6 +2431,18 @@ cudaError_t launch_typed_mma(const Params& p, int d, int G, int path, int mode, 
   if constexpr (std::is_same<T, __half>::value) {
     FD_CASE(128, 4, kPathMmaKv8) FD_CASE(128, 8, kPathMmaKv8) FD_CASE(128, 16, kPathMmaKv8)
   }
+#undef FD_CASE
+  return cudaErrorInvalidValue;
+}
+
+// The consumers over a 4-bit cache; their own translation units.
+template <typename T>
+cudaError_t launch_typed_kv4(const Params& p, int d, int G, int mode, bool pdl, int grid,
+                             cudaStream_t s) {
+#define FD_CASE(DD, GG) \
+  if (d == DD && G == GG) return launch_dgp<T, DD, GG, kPathMmaKv4>(p, mode, pdl, grid, s);
+  FD_CASE(64, 1) FD_CASE(64, 2) FD_CASE(64, 4) FD_CASE(64, 8) FD_CASE(64, 16)
+  FD_CASE(128, 1) FD_CASE(128, 2) FD_CASE(128, 4) FD_CASE(128, 8) FD_CASE(128, 16)
 #undef FD_CASE
   return cudaErrorInvalidValue;
 }

@@ -1,0 +1,9 @@
+// f16 instantiations of the decode kernels over a 4-bit cache.
+#include "fd_kernel.cuh"
+
+namespace fd {
+cudaError_t launch_kv4_f16(const Params& p, int d, int G, int mode, bool pdl, int grid,
+                           cudaStream_t s) {
+  return launch_typed_kv4<__half>(p, d, G, mode, pdl, grid, s);
+}
+}  // namespace fd

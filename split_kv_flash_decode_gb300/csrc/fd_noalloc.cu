@@ -109,8 +109,8 @@ extern "C" int fd_decode_noalloc(fd_plan_t pl, const void* q, const void* k, con
 
   fd::Params p = pl->params;
   if (pl->n_tokens > 0) {
-    rc = fd::encode_kv_map(&p.tm_k, k, pl->n_tokens, p.box_rows, pl);
-    if (rc == FD_OK) rc = fd::encode_kv_map(&p.tm_v, v, pl->n_tokens, p.box_rows, pl);
+    rc = fd::encode_kv_map(&p.tm_k, k, fd::contiguous_rows(pl), p.box_rows, pl);
+    if (rc == FD_OK) rc = fd::encode_kv_map(&p.tm_v, v, fd::contiguous_rows(pl), p.box_rows, pl);
     if (rc != FD_OK) return rc;
   }
   uint8_t* ws = static_cast<uint8_t*>(scratch);

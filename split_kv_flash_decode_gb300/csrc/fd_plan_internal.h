@@ -7,12 +7,13 @@ struct fd_plan_s {
   int B, Hq, Hkv, d, G, dtype;
   uint32_t flags;
   int C;
-  int path;       // fd::kPathFfma, kPathMma, kPathMmaKv8 or kPathUmma
+  int path;       // fd::kPathFfma, kPathMma, kPathMmaKv8, kPathUmma or kPathMmaKv4
   int page_size;  // 0: contiguous K/V; else tokens per page of a paged cache
   int max_pages;  // max_b ceil(L_b / page_size) (paged plans)
   int num_sms;
   int max_partials;
   int64_t n_tokens;
+  int64_t n_blocks;  // 4-bit caches: sum_b ceil(L_b / 16)
   int64_t total_partials;
   int ctas;
   size_t off_counters, off_flags, off_part, ws_bytes;
@@ -21,9 +22,14 @@ struct fd_plan_s {
 
 namespace fd {
 // Encode the 3-D TMA view (d, Hkv, rows) of a [rows, Hkv, d] K or V tensor (or page
-// pool) at `base`; one box is `box_rows` token rows of one head.
+// pool) at `base`; one box is `box_rows` token rows of one head.  4-bit caches: the view
+// (9 d / 8 words, Hkv, blocks), `rows` and `box_rows` still in tokens.
 int encode_kv_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows,
                   const fd_plan_s* pl);
+// Token rows of the plan's contiguous cache.
+inline int64_t contiguous_rows(const fd_plan_s* pl) {
+  return pl->path == kPathMmaKv4 ? pl->n_blocks * kBlockTokens : pl->n_tokens;
+}
 }  // namespace fd
 
 namespace fd {
@@ -48,6 +54,9 @@ inline cudaError_t launch_plan(const fd_plan_s* pl, const Params& p, int mode, i
   if (pl->path == kPathUmma)
     return pl->dtype == FD_BF16 ? launch_umma_bf16(p, pl->d, pl->G, mode, pdl, grid, s)
                                 : launch_umma_f16(p, pl->d, pl->G, mode, pdl, grid, s);
+  if (pl->path == kPathMmaKv4)
+    return pl->dtype == FD_BF16_E2M1KV ? launch_kv4_bf16(p, pl->d, pl->G, mode, pdl, grid, s)
+                                       : launch_kv4_f16(p, pl->d, pl->G, mode, pdl, grid, s);
   if (pl->path == kPathFfma)
     return pl->dtype == FD_BF16 ? launch_bf16_ffma(p, pl->d, pl->G, mode, pdl, grid, s)
                                 : launch_f16_ffma(p, pl->d, pl->G, mode, pdl, grid, s);

@@ -1,0 +1,647 @@
+// Cache rows: fd_append (norm, rotation and store of new tokens) and fd_gather (rows of a
+// cache back in 16 bits).  See fd.h for the contract.
+//
+// Both are bound by the bytes they move.  A head row of d elements is handled by d / 8
+// lanes with 8 elements each, so that a rotation pair never leaves its lane: a lane's two
+// runs of 4 elements are the two halves of its pairs.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <initializer_list>
+#include <new>
+
+#include "fd_kernel.cuh"
+
+struct fd_rows_s {
+  int B, Hq, Hkv, d, dtype, page_size, max_pages;
+  int64_t T, cache_bytes;
+  int32_t cu[FD_MAX_BATCH + 1];   // prefix sums of count
+  int32_t begin[FD_MAX_BATCH];    // row in its sequence of the first token
+  int32_t base[FD_MAX_BATCH];     // contiguous caches: cache row of the sequence's row 0
+};
+
+namespace fd {
+namespace {
+
+constexpr int kRowsThreads = 128;
+constexpr int kMaxAxes = 4;
+constexpr int kMaxPairs = 64;
+constexpr double kMaxFreq = 1 << 20;
+// Warps that an append is split into while it has enough head rows: 32 on each of 152 SMs.
+constexpr int64_t kAppendWarps = 32 * 152;
+
+enum KvKind { kKv16 = 0, kKvE4m3 = 1, kKvE2m1 = 2 };
+
+// Where the rows of a call lie.
+struct RowMap {
+  int32_t B, Hkv, page_shift, num_pages, bt_stride;
+  const int32_t* block_table;  // nullptr: contiguous
+  uint32_t* status;
+  int32_t cu[FD_MAX_BATCH + 1];
+  int32_t begin[FD_MAX_BATCH];
+  int32_t base[FD_MAX_BATCH];
+};
+
+struct AppendParams {
+  RowMap m;
+  const void *q, *k, *v, *q_weight, *k_weight;
+  int64_t q_stride[2], k_stride[2], v_stride[2];
+  void *q_out, *k_out, *k_cache, *v_cache;
+  const int32_t* positions;
+  int64_t pos_stride;
+  float eps, weight_offset, k_mul, v_mul, rope_scale;
+  int32_t T, Hq, q_norm, k_norm, rot, interleaved;
+  int32_t rows_per_warp, splits;   // head rows of one warp; warps per token
+  uint64_t freq[kMaxPairs];        // turns per position, in units of 2^-64
+  uint8_t axis[kMaxPairs];
+};
+static_assert(sizeof(AppendParams) <= 4096, "kernel parameters must stay within 4 KB");
+
+struct GatherParams {
+  RowMap m;
+  const void *k_cache, *v_cache;
+  void *k_out, *v_out;
+  int32_t T;
+};
+
+// Sequence of token t: the last b with cu[b] <= t (sequences without tokens are skipped).
+__device__ __forceinline__ int find_sequence(const RowMap& m, int t) {
+  int lo = 0, hi = m.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (m.cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Cache row (token units) of row r of sequence b, or -1 when its page is outside the pool.
+__device__ __forceinline__ int64_t cache_row(const RowMap& m, int b, int r) {
+  if (m.block_table == nullptr) return (int64_t)m.base[b] + r;
+  const int pg = m.block_table[(int64_t)b * m.bt_stride + (r >> m.page_shift)];
+  if ((uint32_t)pg >= (uint32_t)m.num_pages) {
+    if (m.status != nullptr) atomicOr(m.status, 1u);
+    return -1;
+  }
+  return ((int64_t)pg << m.page_shift) + (r & ((1 << m.page_shift) - 1));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Four values rounded to E4M3 (saturating) or E2M1, first value in the low bits.
+__device__ __forceinline__ uint32_t to_e4m3x4(const float (&x)[4]) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+      "mov.b32 %0, {a, b};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  return r;
+}
+__device__ __forceinline__ uint32_t to_e2m1x4(const float (&x)[4]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, z;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "mov.b32 %0, {a, b, a, b};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  return r & 0xffffu;
+}
+
+// The E4M3 scale of a block of 16 elements, 4 of them in each of four neighbouring lanes,
+// and the codes of this lane's 4.  The quotient is a true division: with the product by a
+// reciprocal, values half-way between two codes (common: 16-bit values over a scale of 4
+// significant bits) would not always round to even.
+__device__ __forceinline__ void quantise(const float (&y)[4], uint32_t& scale, uint32_t& codes) {
+  float m = max_nan(max_nan(fabsf(y[0]), fabsf(y[1])), max_nan(fabsf(y[2]), fabsf(y[3])));
+  m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const float want[4] = {m / 6.f, 0.f, 0.f, 0.f};
+  scale = to_e4m3x4(want) & 0xffu;
+  const float s = dev::Elem<__half>::to_f2(dev::e4m3x2_to_f16x2(scale)).x;
+  const bool any = s > 0.f;  // false for a NaN scale too: the codes do not matter then
+  const float z[4] = {any ? y[0] / s : 0.f, any ? y[1] / s : 0.f, any ? y[2] / s : 0.f,
+                      any ? y[3] / s : 0.f};
+  codes = to_e2m1x4(z);
+}
+
+// Byte offset in a 4-bit V block of element e (a multiple of 4) of row r.
+template <int D>
+__device__ __forceinline__ int v_offset(int r, int e) {
+  const int g = e / (D / 8), swap = ((D == 128 ? g : g >> 1) & 1) << 2;
+  return g * D + (((r >> 1) ^ swap) * (D / 8)) + (r & 1) * (D / 16) + (e % (D / 8)) / 2;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack4(const uint2& raw, float (&f)[4]) {
+  const float2 a = dev::Elem<T>::to_f2(raw.x), b = dev::Elem<T>::to_f2(raw.y);
+  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+template <typename T>
+__device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
+  return make_uint2(dev::pack2<T>(f[0], f[1]), dev::pack2<T>(f[2], f[3]));
+}
+
+// One warp: one token, rows_per_warp of its Hq + 2 Hkv head rows (q, then k, then v), 256 / D
+// of them at a time.  The angles depend on the token alone: a lane computes the four of its
+// pairs once and uses them for all its rows.  Position x frequency is a 64-bit product of
+// turns that wraps where whole turns drop out, so no position is too far.
+template <typename T, int D, int KV>
+__global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int LPH = D / 8;        // lanes per head row
+  constexpr int HPW = 32 / LPH;     // head rows a warp handles at a time
+  constexpr int U = 2;              // of which it loads ahead
+  dev::pdl_launch_dependents();
+  dev::pdl_wait();
+  const int64_t wid = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
+  const int t = (int)(wid / p.splits), split = (int)(wid - (int64_t)t * p.splits);
+  if (t >= p.T) return;
+  const int lane = threadIdx.x & 31, l = lane & (LPH - 1), sub = lane / LPH;
+  const int b = find_sequence(p.m, t);
+  const int r = p.m.begin[b] + (t - p.m.cu[b]);
+  const int64_t row = p.k_cache != nullptr ? cache_row(p.m, b, r) : -1;
+
+  const int Hq = p.q != nullptr ? p.Hq : 0, Hk = p.k != nullptr ? p.m.Hkv : 0;
+  const int Hv = p.v != nullptr ? p.m.Hkv : 0;
+  const int lo = split * p.rows_per_warp, hi = min(lo + p.rows_per_warp, Hq + Hk + Hv);
+
+  // This lane's runs of 4 elements: the two halves of its pairs below rot, plain runs above.
+  const int half = p.rot >> 1, rl = p.rot >> 3;
+  const bool rotates = l < rl;
+  const int ea = rotates ? 4 * l : p.rot + 4 * (l - rl);
+  const int eb = rotates ? half + 4 * l : ((p.rot + D) >> 1) + 4 * (l - rl);
+  float c[4], s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { c[i] = 1.f; s[i] = 0.f; }
+  if (rotates && lo < Hq + Hk) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pair = p.interleaved ? (i < 2 ? 2 * l : (half >> 1) + 2 * l - 2) + i : 4 * l + i;
+      const int pos = p.positions != nullptr ? p.positions[p.axis[pair] * p.pos_stride + t] : r;
+      const uint64_t turns = (uint64_t)(int64_t)pos * p.freq[pair];
+      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s[i], &c[i]);
+      c[i] *= p.rope_scale;
+      s[i] *= p.rope_scale;
+    }
+  }
+
+  // Rows [first, last) of one kind, `out` in the q type, `kind` 0: q, 1: k, 2: v.
+  auto rows = [&](int kind, int first, int last, const void* in, const int64_t* stride,
+                  const void* weight, int norm, void* out, int H, void* cache, float mul) {
+    if (first >= last) return;
+    float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
+    if (norm && weight != nullptr) {
+      unpack4<T>(*reinterpret_cast<const uint2*>(reinterpret_cast<const T*>(weight) + ea), wa);
+      unpack4<T>(*reinterpret_cast<const uint2*>(reinterpret_cast<const T*>(weight) + eb), wb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { wa[i] += p.weight_offset; wb[i] += p.weight_offset; }
+    }
+    const T* src = reinterpret_cast<const T*>(in) + (int64_t)t * stride[0];
+    for (int h0 = first; h0 < last; h0 += U * HPW) {
+      uint2 ra[U], rb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = min(h0 + u * HPW + sub, last - 1);  // rows past the end repeat the last one
+        ra[u] = *reinterpret_cast<const uint2*>(src + (int64_t)h * stride[1] + ea);
+        rb[u] = *reinterpret_cast<const uint2*>(src + (int64_t)h * stride[1] + eb);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * HPW + sub;
+        const bool there = h < last;
+        float a[4], x[4];
+        unpack4<T>(ra[u], a);
+        unpack4<T>(rb[u], x);
+        if (norm) {
+          float ss = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ss = fmaf(a[i], a[i], fmaf(x[i], x[i], ss));
+#pragma unroll
+          for (int off = 1; off < LPH; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          const float n = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = a[i] * n * wa[i];
+            x[i] = x[i] * n * wb[i];
+          }
+        }
+        if (kind < 2 && rotates) {
+          if (p.interleaved) {
+            const float a0 = a[0], a2 = a[2], x0 = x[0], x2 = x[2];
+            a[0] = a0 * c[0] - a[1] * s[0];
+            a[1] = a0 * s[0] + a[1] * c[0];
+            a[2] = a2 * c[1] - a[3] * s[1];
+            a[3] = a2 * s[1] + a[3] * c[1];
+            x[0] = x0 * c[2] - x[1] * s[2];
+            x[1] = x0 * s[2] + x[1] * c[2];
+            x[2] = x2 * c[3] - x[3] * s[3];
+            x[3] = x2 * s[3] + x[3] * c[3];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a0 = a[i];
+              a[i] = a0 * c[i] - x[i] * s[i];
+              x[i] = a0 * s[i] + x[i] * c[i];
+            }
+          }
+        }
+        if (out != nullptr && there) {
+          T* dst = reinterpret_cast<T*>(out) + ((int64_t)t * H + h) * D;
+          *reinterpret_cast<uint2*>(dst + ea) = pack4<T>(a);
+          *reinterpret_cast<uint2*>(dst + eb) = pack4<T>(x);
+        }
+        if (kind == 0 || cache == nullptr) continue;
+        const bool store = there && row >= 0;
+        if constexpr (KV == kKv16) {
+          if (store) {
+            T* dst = reinterpret_cast<T*>(cache) + (row * H + h) * D;
+            *reinterpret_cast<uint2*>(dst + ea) = pack4<T>(a);
+            *reinterpret_cast<uint2*>(dst + eb) = pack4<T>(x);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) { a[i] *= mul; x[i] *= mul; }
+          if constexpr (KV == kKvE4m3) {
+            if (store) {
+              uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + (row * H + h) * D;
+              *reinterpret_cast<uint32_t*>(dst + ea) = to_e4m3x4(a);
+              *reinterpret_cast<uint32_t*>(dst + eb) = to_e4m3x4(x);
+            }
+          } else {
+            // Runs of four neighbouring lanes are whole blocks of 16 (rot is a multiple of 32).
+            uint32_t sa, sb, ca, cb;
+            quantise(a, sa, ca);
+            quantise(x, sb, cb);
+            if (store) {
+              uint8_t* blk = reinterpret_cast<uint8_t*>(cache) + ((row >> kBlockShift) * H + h) * (9 * D);
+              const int r16 = (int)(row & (kBlockTokens - 1));
+              const int oa = kind == 1 ? r16 * (D / 2) + ea / 2 : v_offset<D>(r16, ea);
+              const int ob = kind == 1 ? r16 * (D / 2) + eb / 2 : v_offset<D>(r16, eb);
+              *reinterpret_cast<uint16_t*>(blk + oa) = (uint16_t)ca;
+              *reinterpret_cast<uint16_t*>(blk + ob) = (uint16_t)cb;
+              if ((l & 3) == 0) {
+                const int ja = ea / 16, jb = eb / 16;
+                blk[8 * D + (kind == 1 ? r16 * (D / 16) + ja : 16 * ja + r16)] = (uint8_t)sa;
+                blk[8 * D + (kind == 1 ? r16 * (D / 16) + jb : 16 * jb + r16)] = (uint8_t)sb;
+              }
+            }
+          }
+        }
+      }
+    }
+  };
+  rows(0, lo, min(hi, Hq), p.q, p.q_stride, p.q_weight, p.q_norm, p.q_out, p.Hq, nullptr, 1.f);
+  rows(1, max(lo - Hq, 0), min(hi - Hq, Hk), p.k, p.k_stride, p.k_weight, p.k_norm, p.k_out, p.m.Hkv,
+       p.k_cache, p.k_mul);
+  rows(2, max(lo - Hq - Hk, 0), min(hi - Hq - Hk, Hv), p.v, p.v_stride, nullptr, 0, nullptr, p.m.Hkv,
+       p.v_cache, p.v_mul);
+}
+
+// One warp: 16 tokens of one KV head, K (even warps of the grid) or V.  Lanes as above; a
+// lane's 8 elements are neighbours.
+template <typename T, int D, int KV>
+__global__ void __launch_bounds__(kRowsThreads) fd_gather_kernel(const __grid_constant__ GatherParams p) {
+  constexpr int LPH = D / 8, HPW = 32 / LPH, TOK = 16;
+  dev::pdl_launch_dependents();
+  dev::pdl_wait();
+  const int64_t wid = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
+  const int H = p.m.Hkv;
+  const int64_t tile = wid / (2 * H);
+  const int w = (int)(wid - tile * (2 * H)), h = w >> 1, is_v = w & 1;
+  const int64_t t0 = tile * TOK;
+  if (t0 >= p.T) return;
+  const int lane = threadIdx.x & 31, l = lane & (LPH - 1), sub = lane / LPH;
+  // Lane i finds the cache row of token t0 + i.
+  int64_t my_row = -1;
+  if (lane < TOK && t0 + lane < p.T) {
+    const int t = (int)(t0 + lane), b = find_sequence(p.m, t);
+    my_row = cache_row(p.m, b, p.m.begin[b] + (t - p.m.cu[b]));
+  }
+  const uint8_t* cache = reinterpret_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
+  T* out = reinterpret_cast<T*>(is_v ? p.v_out : p.k_out);
+#pragma unroll
+  for (int i = 0; i < TOK / HPW; ++i) {
+    const int tok = i * HPW + sub;
+    const int64_t row = __shfl_sync(0xffffffffu, my_row, tok);
+    const int64_t t = t0 + tok;
+    if (t >= p.T) continue;
+    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= 0) {
+      if constexpr (KV == kKv16) {
+        y = *reinterpret_cast<const uint4*>(cache + ((row * H + h) * D + 8 * l) * 2);
+      } else if constexpr (KV == kKvE4m3) {
+        const uint2 x = *reinterpret_cast<const uint2*>(cache + (row * H + h) * D + 8 * l);
+        dev::e4m3x4_to_f16x4(x.x, y.x, y.y);
+        dev::e4m3x4_to_f16x4(x.y, y.z, y.w);
+      } else {
+        const uint8_t* blk = cache + ((row >> kBlockShift) * H + h) * (9 * D);
+        const int r16 = (int)(row & (kBlockTokens - 1));
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(
+            blk + (is_v ? v_offset<D>(r16, 8 * l) : r16 * (D / 2) + 4 * l));
+        const uint32_t z = dev::e4m3x2_to_f16x2(blk[8 * D + (is_v ? 16 * (l >> 1) + r16 : r16 * (D / 16) + (l >> 1))]);
+        const uint32_t s2 = __byte_perm(z, z, 0x1010);
+        uint32_t f[4];
+        dev::e2m1x8_to_f16x8(x, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[j] = dev::hmul2(f[j], s2);
+          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            const float2 v = dev::Elem<__half>::to_f2(f[j]);
+            f[j] = dev::pack2<T>(v.x, v.y);
+          }
+        }
+        y = make_uint4(f[0], f[1], f[2], f[3]);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + (t * H + h) * D + 8 * l) = y;
+  }
+}
+
+int kv_kind(int dtype) {
+  return dtype == FD_F16_E4M3KV                                  ? kKvE4m3
+         : dtype == FD_F16_E2M1KV || dtype == FD_BF16_E2M1KV ? kKvE2m1
+                                                               : kKv16;
+}
+bool is_bf16(int dtype) { return dtype == FD_BF16 || dtype == FD_BF16_E2M1KV; }
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int64_t row_bytes(const fd_rows_s* r) {
+  const int kind = kv_kind(r->dtype);
+  return kind == kKv16 ? 2 * r->d : kind == kKvE4m3 ? r->d : r->d * 9 / 16;
+}
+
+// Page-table checks shared by both calls, and the map of the rows.
+int make_map(const fd_rows_s* r, int num_pages, const int32_t* block_table, int bt_stride,
+             uint32_t* status, RowMap* m) {
+  m->page_shift = 0;
+  if (r->page_size) {
+    if (num_pages < 1 || block_table == nullptr || bt_stride < r->max_pages) return FD_ERR_INVALID;
+    if ((int64_t)num_pages * r->page_size >= (int64_t)1 << 31) return FD_ERR_UNSUPPORTED;
+    while ((1 << m->page_shift) < r->page_size) ++m->page_shift;
+  } else if (block_table != nullptr) {
+    return FD_ERR_INVALID;
+  }
+  if (!aligned(block_table, 4) || !aligned(status, 4)) return FD_ERR_ALIGN;
+  m->B = r->B;
+  m->Hkv = r->Hkv;
+  m->num_pages = num_pages;
+  m->bt_stride = bt_stride;
+  m->block_table = block_table;
+  m->status = status;
+  std::memcpy(m->cu, r->cu, sizeof(m->cu));
+  std::memcpy(m->begin, r->begin, sizeof(m->begin));
+  std::memcpy(m->base, r->base, sizeof(m->base));
+  return FD_OK;
+}
+
+int launch_rows(const void* fn, int64_t warps, void* params, cudaStream_t stream) {
+  const int64_t blocks = (warps + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
+  if (blocks >= (int64_t)1 << 31) return FD_ERR_UNSUPPORTED;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kRowsThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* args[] = {params};
+  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    cudaGetLastError();
+    return FD_ERR_CUDA;
+  }
+  return FD_OK;
+}
+
+template <template <typename, int, int> class K>
+const void* pick(int dtype, int d) {
+  const int kind = kv_kind(dtype);
+  if (is_bf16(dtype)) {
+    if (d == 64) return kind == kKv16 ? K<__nv_bfloat16, 64, kKv16>::fn() : K<__nv_bfloat16, 64, kKvE2m1>::fn();
+    return kind == kKv16 ? K<__nv_bfloat16, 128, kKv16>::fn() : K<__nv_bfloat16, 128, kKvE2m1>::fn();
+  }
+  if (d == 64)
+    return kind == kKv16 ? K<__half, 64, kKv16>::fn()
+           : kind == kKvE4m3 ? K<__half, 64, kKvE4m3>::fn() : K<__half, 64, kKvE2m1>::fn();
+  return kind == kKv16 ? K<__half, 128, kKv16>::fn()
+         : kind == kKvE4m3 ? K<__half, 128, kKvE4m3>::fn() : K<__half, 128, kKvE2m1>::fn();
+}
+template <typename T, int D, int KV>
+struct AppendFn {
+  static const void* fn() { return reinterpret_cast<const void*>(&fd_append_kernel<T, D, KV>); }
+};
+template <typename T, int D, int KV>
+struct GatherFn {
+  static const void* fn() { return reinterpret_cast<const void*>(&fd_gather_kernel<T, D, KV>); }
+};
+
+// Frequencies in units of 2^-64 turns per position (whole turns dropped), and their axes.
+int set_rope(const fd_rope* rope, int d, bool four_bit_cache, AppendParams* p) {
+  p->rot = 0;
+  p->rope_scale = 1.f;
+  if (rope == nullptr || rope->rot_dim == 0) return FD_OK;
+  if (rope->rot_dim < 0 || rope->rot_dim > d || rope->rot_dim % 2 || rope->inv_freq == nullptr ||
+      rope->num_axes < 1 || rope->num_axes > kMaxAxes || !std::isfinite(rope->scale) || rope->scale == 0.f)
+    return FD_ERR_INVALID;
+  if (rope->rot_dim % (four_bit_cache ? 32 : 16)) return FD_ERR_UNSUPPORTED;
+  if (rope->num_axes > 1 && (p->positions == nullptr || p->pos_stride < p->T)) return FD_ERR_INVALID;
+  for (int i = 0; i < rope->rot_dim / 2; ++i) {
+    const double f = rope->inv_freq[i];
+    if (!(std::fabs(f) <= kMaxFreq)) return FD_ERR_INVALID;  // NaN too
+    // Turns per position in twice double precision (product and its rounding error), then
+    // modulo 1 in 64 bits: the whole turns of the high part drop out exactly.
+    const double high = f * 0.15915494309189535;                        // 1 / (2 pi), high part
+    const double low = std::fma(f, 0.15915494309189535, -high) + f * -9.839338337591243e-18;
+    const double part = std::fabs(high - std::trunc(high));
+    const uint64_t units = (uint64_t)std::ldexp(part, 64);
+    p->freq[i] = (high < 0 ? 0 - units : units) + (uint64_t)std::llrint(std::ldexp(low, 64));
+    const int axis = rope->axis ? rope->axis[i] : 0;
+    if (axis >= rope->num_axes) return FD_ERR_INVALID;
+    p->axis[i] = (uint8_t)axis;
+  }
+  p->rot = rope->rot_dim;
+  p->interleaved = rope->interleaved != 0;
+  p->rope_scale = rope->scale;
+  return FD_OK;
+}
+
+// Bytes [p, p + n) of one tensor and those of an input with the given strides overlap.
+bool overlap(const void* out, int64_t out_bytes, const void* in, const int64_t* stride, int64_t T, int H, int d) {
+  if (out == nullptr || in == nullptr) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
+  const uintptr_t n = 2 * (uintptr_t)((T - 1) * stride[0] + (H - 1) * stride[1] + d);
+  return a < b + n && b < a + (uintptr_t)out_bytes;
+}
+bool in_place(const void* out, const void* in, const int64_t* stride, int64_t T, int H, int d) {
+  return out == in && (stride[1] == d || H == 1) && (stride[0] == (int64_t)H * d || T == 1);
+}
+
+}  // namespace
+}  // namespace fd
+
+extern "C" {
+
+int fd_rows_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32_t* begin,
+                 const int32_t* count, int page_size, int dtype, fd_rows_t* out_rows) {
+  if (!out_rows) return FD_ERR_INVALID;
+  *out_rows = nullptr;
+  if (!seqlens || !begin || !count) return FD_ERR_INVALID;
+  if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || page_size < 0 || Hq % Hkv != 0) return FD_ERR_INVALID;
+  if (dtype != FD_F16 && dtype != FD_BF16 && dtype != FD_F16_E4M3KV && dtype != FD_F16_E2M1KV &&
+      dtype != FD_BF16_E2M1KV)
+    return FD_ERR_INVALID;
+  if (page_size != 0 && (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))))
+    return FD_ERR_UNSUPPORTED;
+  if (B > FD_MAX_BATCH || (d != 64 && d != 128)) return FD_ERR_UNSUPPORTED;
+  const int64_t limit = (int64_t)1 << 31;
+  if ((int64_t)Hq + 2 * (int64_t)Hkv >= limit / FD_MAX_BATCH) return FD_ERR_UNSUPPORTED;
+  const bool four = fd::kv_kind(dtype) == fd::kKvE2m1;
+  int64_t T = 0, rows = 0;
+  int max_pages = 0;
+  for (int b = 0; b < B; ++b) {
+    if (seqlens[b] < 0 || begin[b] < 0 || count[b] < 0 ||
+        (int64_t)begin[b] + count[b] > (int64_t)seqlens[b])
+      return FD_ERR_INVALID;
+    T += count[b];
+    const int64_t L = seqlens[b];
+    rows += four ? (L + fd::kBlockTokens - 1) / fd::kBlockTokens * fd::kBlockTokens : L;
+    if (page_size) max_pages = (int)std::max<int64_t>(max_pages, (L + page_size - 1) / page_size);
+  }
+  if (rows >= limit) return FD_ERR_UNSUPPORTED;
+
+  fd_rows_s* r = new (std::nothrow) fd_rows_s();
+  if (!r) return FD_ERR_NOMEM;
+  r->B = B; r->Hq = Hq; r->Hkv = Hkv; r->d = d; r->dtype = dtype; r->page_size = page_size;
+  r->max_pages = max_pages;
+  r->T = T;
+  r->cache_bytes = (page_size ? page_size : rows) * Hkv * fd::row_bytes(r);
+  int32_t cu = 0, base = 0;
+  for (int b = 0; b < B; ++b) {
+    r->cu[b] = cu;
+    r->begin[b] = begin[b];
+    r->base[b] = base;
+    cu += count[b];
+    base += four ? (int32_t)(((int64_t)seqlens[b] + fd::kBlockTokens - 1) / fd::kBlockTokens * fd::kBlockTokens)
+                 : seqlens[b];
+  }
+  r->cu[B] = cu;
+  *out_rows = r;
+  return FD_OK;
+}
+
+int fd_rows_destroy(fd_rows_t rows) {
+  delete rows;
+  return FD_OK;
+}
+
+int fd_rows_get_info(fd_rows_t rows, fd_rows_info* info) {
+  if (!rows || !info) return FD_ERR_INVALID;
+  info->tokens = rows->T;
+  info->cache_bytes = rows->cache_bytes;
+  return FD_OK;
+}
+
+int fd_append(fd_rows_t rows, const fd_append_args* a, cudaStream_t stream) {
+  if (!rows || !a) return FD_ERR_INVALID;
+  const fd_rows_s* r = rows;
+  const int d = r->d, kind = fd::kv_kind(r->dtype);
+  if ((a->q != nullptr) != (a->q_out != nullptr) || (a->v != nullptr) != (a->v_cache != nullptr) ||
+      (a->k_cache != nullptr) != (a->v_cache != nullptr) ||
+      (a->k != nullptr) != (a->k_out != nullptr || a->k_cache != nullptr) || (!a->q && !a->k))
+    return FD_ERR_INVALID;
+  const int64_t* strides[3] = {a->q_stride, a->k_stride, a->v_stride};
+  const void* ins[3] = {a->q, a->k, a->v};
+  for (int i = 0; i < 3; ++i)
+    if (ins[i] && (strides[i][0] < 0 || strides[i][1] < 0)) return FD_ERR_INVALID;
+  if (a->k_cache) {
+    if (!std::isfinite(a->k_mul) || !std::isfinite(a->v_mul) || a->k_mul <= 0.f || a->v_mul <= 0.f)
+      return FD_ERR_INVALID;
+    if (kind == fd::kKv16 && (a->k_mul != 1.f || a->v_mul != 1.f)) return FD_ERR_INVALID;
+  }
+  if ((a->q_norm || a->k_norm) &&
+      (!std::isfinite(a->eps) || a->eps < 0.f || !std::isfinite(a->weight_offset)))
+    return FD_ERR_INVALID;
+  for (const void* p : {a->q, a->k, a->v, a->q_weight, a->k_weight, (const void*)a->q_out,
+                        (const void*)a->k_out, (const void*)a->k_cache, (const void*)a->v_cache})
+    if (!fd::aligned(p, 16)) return FD_ERR_ALIGN;
+  if (!fd::aligned(a->positions, 4)) return FD_ERR_ALIGN;
+  for (int i = 0; i < 3; ++i)
+    if (ins[i] && (strides[i][0] % 8 || strides[i][1] % 8)) return FD_ERR_ALIGN;
+
+  fd::AppendParams p;
+  p.T = (int32_t)r->T;
+  p.positions = a->positions;
+  p.pos_stride = a->pos_stride;
+  p.interleaved = 0;
+  int rc = fd::set_rope(a->rope, d, kind == fd::kKvE2m1 && a->k_cache, &p);
+  if (rc != FD_OK) return rc;
+  if (a->k_cache) {
+    rc = fd::make_map(r, a->num_pages, a->block_table, a->bt_stride, a->status, &p.m);
+    if (rc != FD_OK) return rc;
+  } else {
+    // Nothing is stored in a cache: the map only tells rows (default positions) from tokens.
+    fd_rows_s flat = *r;
+    flat.page_size = 0;
+    rc = fd::make_map(&flat, 0, nullptr, 0, nullptr, &p.m);
+    if (rc != FD_OK) return rc;
+  }
+  const int64_t T = r->T;
+  if (T == 0) return FD_OK;
+  const int heads[3] = {r->Hq, r->Hkv, r->Hkv};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t qb = 2 * T * r->Hq * d, kb = 2 * T * r->Hkv * d;
+    if (!(i == 0 && fd::in_place(a->q_out, a->q, a->q_stride, T, r->Hq, d)) &&
+        fd::overlap(a->q_out, qb, ins[i], strides[i], T, heads[i], d))
+      return FD_ERR_INVALID;
+    if (!(i == 1 && fd::in_place(a->k_out, a->k, a->k_stride, T, r->Hkv, d)) &&
+        fd::overlap(a->k_out, kb, ins[i], strides[i], T, heads[i], d))
+      return FD_ERR_INVALID;
+  }
+  p.q = a->q; p.k = a->k; p.v = a->v;
+  p.q_weight = a->q_weight; p.k_weight = a->k_weight;
+  std::memcpy(p.q_stride, a->q_stride, sizeof(p.q_stride));
+  std::memcpy(p.k_stride, a->k_stride, sizeof(p.k_stride));
+  std::memcpy(p.v_stride, a->v_stride, sizeof(p.v_stride));
+  p.q_out = a->q_out; p.k_out = a->k_out; p.k_cache = a->k_cache; p.v_cache = a->v_cache;
+  p.eps = a->eps;
+  p.weight_offset = a->weight_offset;
+  p.k_mul = a->k_mul; p.v_mul = a->v_mul;
+  p.q_norm = a->q_norm != 0; p.k_norm = a->k_norm != 0;
+  p.Hq = r->Hq;
+  // Head rows per warp: one load round (4 rows at d = 128) while tokens are few, so that a
+  // decode step fills the device; more as they grow, so that the angles of a token are
+  // computed less often.
+  const int rows_all = (a->q ? r->Hq : 0) + (a->k ? r->Hkv : 0) + (a->v ? r->Hkv : 0);
+  const int round = 2 * (256 / d);
+  int64_t per = (T * rows_all + fd::kAppendWarps - 1) / fd::kAppendWarps;
+  per = (per + round - 1) / round * round;
+  if (per > rows_all) per = rows_all;
+  p.rows_per_warp = (int32_t)per;
+  p.splits = (int32_t)((rows_all + per - 1) / per);
+  return fd::launch_rows(fd::pick<fd::AppendFn>(r->dtype, d), T * p.splits, &p, stream);
+}
+
+int fd_gather(fd_rows_t rows, const void* k_cache, const void* v_cache, int num_pages,
+              const int32_t* block_table, int bt_stride, void* k_out, void* v_out,
+              uint32_t* status, cudaStream_t stream) {
+  if (!rows || !k_cache || !v_cache || !k_out || !v_out) return FD_ERR_INVALID;
+  for (const void* p : {k_cache, v_cache, (const void*)k_out, (const void*)v_out})
+    if (!fd::aligned(p, 16)) return FD_ERR_ALIGN;
+  fd::GatherParams p;
+  int rc = fd::make_map(rows, num_pages, block_table, bt_stride, status, &p.m);
+  if (rc != FD_OK) return rc;
+  if (rows->T == 0) return FD_OK;
+  p.k_cache = k_cache; p.v_cache = v_cache;
+  p.k_out = k_out; p.v_out = v_out;
+  p.T = (int32_t)rows->T;
+  const int64_t tiles = (rows->T + 15) / 16;
+  return fd::launch_rows(fd::pick<fd::GatherFn>(rows->dtype, rows->d), tiles * 2 * rows->Hkv, &p, stream);
+}
+
+}  // extern "C"

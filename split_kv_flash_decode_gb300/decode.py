@@ -10,8 +10,19 @@ import torch
 from . import _binding as B
 
 # q / out type and K / V storage type of each plan dtype.
-_TORCH_DTYPE = {"f16": torch.float16, "bf16": torch.bfloat16, "f16_e4m3kv": torch.float16}
-_KV_DTYPE = {"f16": torch.float16, "bf16": torch.bfloat16, "f16_e4m3kv": torch.uint8}
+_TORCH_DTYPE = {"f16": torch.float16, "bf16": torch.bfloat16, "f16_e4m3kv": torch.float16,
+                "f16_e2m1kv": torch.float16, "bf16_e2m1kv": torch.bfloat16}
+_KV_DTYPE = {"f16": torch.float16, "bf16": torch.bfloat16, "f16_e4m3kv": torch.uint8,
+             "f16_e2m1kv": torch.uint8, "bf16_e2m1kv": torch.uint8}
+
+
+def cache_shape(dtype, Hkv, d, seqlens=None, num_pages=None, page_size=0):
+    """Shape of the K (and of the V) cache: of the contiguous cache of `seqlens`, or of a pool of
+    `num_pages` pages.  4-bit caches are made of blocks of 16 tokens (include/fd.h)."""
+    unit, last = (16, 9 * d) if dtype.endswith("e2m1kv") else (1, d)
+    if page_size:
+        return (num_pages, page_size // unit, Hkv, last)
+    return (sum((int(x) + unit - 1) // unit for x in seqlens), Hkv, last)
 
 
 class Decoder:
@@ -56,8 +67,9 @@ class Decoder:
 
     def __call__(self, q, k, v, out=None, lse=None, stream=None):
         self._check("q", q, (self.Bsz, self.Hq, self.d))
-        self._check("k", k, (self.n_tokens, self.Hkv, self.d))
-        self._check("v", v, (self.n_tokens, self.Hkv, self.d))
+        shape = cache_shape(self.dtype, self.Hkv, self.d, self.seqlens)
+        self._check("k", k, shape)
+        self._check("v", v, shape)
         if out is None:
             out = torch.empty_like(q)
         else:
@@ -71,13 +83,15 @@ class Decoder:
         return out, lse
 
     def decode_paged(self, q, k_pages, v_pages, block_table, out=None, lse=None, stream=None):
-        """Decode over a paged cache: pools [num_pages, page_size, Hkv, d], int32 block_table [B, stride]."""
+        """Decode over a paged cache: pools [num_pages, page_size, Hkv, d] (or as cache_shape says),
+        int32 block_table [B, stride]."""
         if not self.page_size:
             raise ValueError("this Decoder was planned for contiguous K/V")
         self._check("q", q, (self.Bsz, self.Hq, self.d))
         num_pages = k_pages.shape[0]
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-            self._check(name, t, (num_pages, self.page_size, self.Hkv, self.d))
+            self._check(name, t, cache_shape(self.dtype, self.Hkv, self.d, None, num_pages,
+                                             self.page_size))
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
                 block_table.shape[0] != self.Bsz or not block_table.is_contiguous() or \
                 block_table.device != self.device:
@@ -100,7 +114,7 @@ def flash_decode(q, k, v, seqlens, W, flags=0, chunks=0):
     """One-shot decode: plan, allocate, run.  Returns (out, lse)."""
     dtype = {torch.float16: "f16", torch.bfloat16: "bf16"}[q.dtype]
     if k.dtype == torch.uint8:
-        dtype = "f16_e4m3kv"
+        dtype = dtype + "_e2m1kv" if k.shape[2] == 9 * q.shape[2] else "f16_e4m3kv"
     dec = Decoder(q.shape[1], k.shape[1], q.shape[2], seqlens, W, dtype, flags, chunks,
                   device=q.device)
     return dec(q, k, v)
