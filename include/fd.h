@@ -78,6 +78,13 @@ enum fd_dtype {
  *               ceil(L_0 / 16) + ... + ceil(L_{b-1} / 16)
  *   paged       [num_pages, page_size / 16, Hkv, 9 d]
  * Bytes of tokens past a sequence's length may hold anything.
+ *
+ * Stream plans.  By default a 4-bit plan does not launch one CTA per partial: the 128-token
+ * tiles of all (sequence, KV head) pairs are cut into one equal run per resident CTA, and a pair that
+ * several CTAs share is combined by the last of them to arrive.  W then has no effect (the
+ * result does not depend on it).  Explicit chunks, or one of the flags LITERAL_W, TWO_LAUNCH,
+ * WAITS, CLUSTER, NO_CLUSTER, CLUSTER_COMBINE, COMBINERS_n and TEST_DROP_ARRIVAL, gives the
+ * W * C partials of the other dtypes.
  */
 
 enum fd_status {
@@ -460,7 +467,7 @@ typedef struct fd_plan_info {
   uint32_t flags;
   int32_t chunks;          /* C actually used */
   int32_t num_sms;         /* SM count the plan was sized for */
-  int32_t ctas;            /* CTAs fd_decode launches = Hkv * sum_b W_b * C */
+  int32_t ctas;            /* CTAs fd_decode launches = Hkv * sum_b W_b * C (stream: the resident ones) */
   int32_t max_partials;    /* max_b W_b * C */
   int64_t total_tokens;    /* N */
   int64_t total_partials;  /* P */
@@ -478,12 +485,13 @@ typedef struct fd_plan_info {
                               1 = the last arriver alone */
   int32_t ctas_per_sm;     /* resident CTAs per SM the split kernel is launched for:
                               2 (96 KB rings), 3 (64 KB rings) or 1 (tcgen05) */
+  int32_t stream;          /* 1: a stream plan (4-bit caches, see FD_F16_E2M1KV) */
 } fd_plan_info;
 
 int fd_plan_get_info(fd_plan_t plan, fd_plan_info* info);
 
 /* Token range [*begin, *end) (relative to the start of sequence b) covered by
- * partial `slot` (0 <= slot < W_b * C) of sequence b. */
+ * partial `slot` (0 <= slot < W_b * C) of sequence b.  FD_ERR_UNSUPPORTED for stream plans. */
 int fd_plan_get_range(fd_plan_t plan, int b, int slot, int32_t* begin, int32_t* end);
 
 /* Library version, e.g. 0x000100 for 0.1.0. */

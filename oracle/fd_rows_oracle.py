@@ -27,7 +27,7 @@ def nearest_code(a, grid):
 def quantise(x):
     """Codes [..., n] (sign in bit 3) and E4M3 scale bytes [..., n / 16] of x (finite)."""
     x = np.asarray(x, dtype=np.float64)
-    y = x.reshape(*x.shape[:-1], -1, 16)
+    y = x.reshape(*x.shape[:-1], x.shape[-1] // 16, 16)
     amax = np.abs(y).max(-1)
     # The scale is the E4M3 rounding of an fp32 quotient.
     scale = nearest_code((amax.astype(np.float32) / np.float32(6)).astype(np.float64), E4M3)
@@ -40,7 +40,7 @@ def quantise(x):
 def dequantise(codes, scales):
     """Values of codes and scale bytes (a NaN scale makes its 16 values NaN)."""
     mag = E2M1[codes & 7]
-    v = np.where(codes & 8, -mag, mag).reshape(*codes.shape[:-1], -1, 16)
+    v = np.where(codes & 8, -mag, mag).reshape(*codes.shape[:-1], codes.shape[-1] // 16, 16)
     return (v * widen(scales, "e4m3")[..., None]).reshape(codes.shape)
 
 

@@ -79,7 +79,7 @@ class PlanInfo(ctypes.Structure):
         ("workspace_bytes", ctypes.c_uint64), ("kv_bytes", ctypes.c_uint64),
         ("path", ctypes.c_int32), ("records_per_segment", ctypes.c_int32),
         ("combine_cluster", ctypes.c_int32), ("combiners", ctypes.c_int32),
-        ("ctas_per_sm", ctypes.c_int32),
+        ("ctas_per_sm", ctypes.c_int32), ("stream", ctypes.c_int32),
     ]
 
 

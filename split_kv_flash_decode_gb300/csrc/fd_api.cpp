@@ -234,6 +234,7 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
   pl->flags = flags; pl->C = C; pl->num_sms = num_sms;
   pl->path = path;
   pl->page_size = page_size;
+  pl->stream = false;
   pl->max_pages = 0;
   if (page_size)
     for (int b = 0; b < B; ++b)
@@ -313,6 +314,47 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
   p.cu[B] = cu;
   p.unit_base[B] = ub;
 
+  // 4-bit caches: unless the caller asks for a particular decomposition, the tiles of all
+  // (sequence, KV head) pairs are cut into one equal run per CTA, whatever W.  (64 sequences of 8K
+  // tokens, W = 16: see fd_kv4.cuh.)
+  constexpr uint32_t kFixed = FD_PLAN_LITERAL_W | FD_PLAN_TWO_LAUNCH | FD_PLAN_WAITS | FD_PLAN_CLUSTER |
+                              FD_PLAN_NO_CLUSTER | FD_PLAN_CLUSTER_COMBINE | FD_PLAN_COMBINERS_MASK |
+                              FD_PLAN_TEST_DROP_ARRIVAL;
+  if (kv4 && !(flags & kFixed) && chunks == 0) {
+    const int tile = fd::kStreamTile;
+    auto units_of = [&](int L) {
+      return fd::kPairUnits + std::max<int64_t>(1, ((int64_t)L + tile - 1) / tile);
+    };
+    int64_t units = 0, tiles = 0;
+    for (int b = 0; b < B; ++b) {
+      units += Hkv * units_of(seqlens[b]);
+      tiles += Hkv * (units_of(seqlens[b]) - fd::kPairUnits);
+    }
+    if (units < (int64_t)1 << 31) {
+      pl->stream = true;
+      const int n =
+          (int)std::min<int64_t>({tiles, (int64_t)num_sms * fd::stream_ctas(G), (int64_t)fd::kMaxStreamCtas});
+      p.run_len = (int32_t)(units / n);
+      p.run_extra = (int32_t)(units % n);
+      int32_t base = 0;
+      int64_t most = 0;
+      for (int b = 0; b < B; ++b) {
+        p.unit_base[b] = base;
+        base += (int32_t)(Hkv * units_of(seqlens[b]));
+        // A pair of u units meets at most (u - 2) / run_len + 2 runs.
+        most = std::max<int64_t>(most, std::min<int64_t>(n, (units_of(seqlens[b]) - 2) / p.run_len + 2));
+      }
+      p.unit_base[B] = base;
+      p.box_rows = page_size ? std::min(tile, page_size) : tile;
+      p.rps = C;
+      p.combiners = 1;
+      p.ctas_per_sm = fd::stream_ctas(G);
+      pl->ctas = n;
+      pl->max_partials = (int)most;
+      pl->total_partials = (int64_t)2 * n * std::max(G, 4);  // two records per CTA
+    }
+  }
+
   // Workspace: status | counters | flags | partial records [P][d + 4] (each 256-byte aligned).
   size_t off = kAlign;
   pl->off_counters = off;
@@ -364,11 +406,13 @@ int fd_plan_get_info(fd_plan_t pl, fd_plan_info* info) {
   info->combine_cluster = pl->params.pair_cluster;
   info->combiners = pl->params.combiners;
   info->ctas_per_sm = pl->params.ctas_per_sm;
+  info->stream = pl->stream;
   return FD_OK;
 }
 
 int fd_plan_get_range(fd_plan_t pl, int b, int slot, int32_t* begin, int32_t* end) {
   if (!pl || !begin || !end || b < 0 || b >= pl->B) return FD_ERR_INVALID;
+  if (pl->stream) return FD_ERR_UNSUPPORTED;
   const int wtot = pl->params.wseg[b] * pl->C;
   if (slot < 0 || slot >= wtot) return FD_ERR_INVALID;
   const int L = pl->params.cu[b + 1] - pl->params.cu[b];

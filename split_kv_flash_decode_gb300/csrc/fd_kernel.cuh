@@ -1069,6 +1069,14 @@ __device__ __forceinline__ void finish_cta(const Params& p, const Work& wk, floa
   if (merge_seg) cluster_wait();
 }
 
+}  // namespace dev
+}  // namespace fd
+
+#include "fd_kv4.cuh"
+
+namespace fd {
+namespace dev {
+
 // MODE 0: fused split + last-arriver combine.  MODE 1: split only (partials).
 // MODE 3: fused split + fine-grained waits.  MODE 4 / 5: MODE 0 / 1 with each
 // segment's chunk partials merged inside a thread-block cluster (rps == 1).
@@ -1710,83 +1718,12 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
     }
   } else if constexpr (PATH == kPathMmaKv4) {
     // ---------------- MMA consumers over a 4-bit (E2M1) cache ----------------
-    // The tile is 8 blocks of 16 tokens.  As on the E4M3 path, index permutations make
-    // each thread's fragment bytes contiguous: thread quad t covers elements
-    // t D/4 + 4 kk + {0, 1} (a0/a1/b0) and + {2, 3} (a2/a3/b1) in k-step kk of S = K q^T;
-    // row g / g + 8 of m-tile mi of O^T is dim g D/8 + 2 mi / + 1.  An element is E2M1 value
-    // x E4M3 scale, at most 6 significant bits and 2^-10 .. 2688 in size: exact in f16, so
-    // both products run on f16 mma whatever q's type.  bf16 q is brought to f16 range by a
-    // power of two per head (its 8 significant bits stay; elements below 2^-14 of the
-    // head's largest lose at most 2^-25 of it, the size of fp32's own rounding).
-    constexpr int KT = D / 16;              // k-steps of S, m-tiles of O^T
-    constexpr int NT = G >= 8 ? G / 8 : 1;  // N tiles of 8 query heads
-    constexpr int NW = D / 64;              // K words (of 8 elements) per thread and row, x 2
-    constexpr int BLK = 16 * ring_row_bytes(PATH, D);  // bytes between blocks in the ring
-    static_assert(BLK % 128 == 0, "every block can be the destination of a TMA box");
-    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    const int g = lane >> 2, t = lane & 3, qcol = 2 * t;
-    uint32_t qb[NT][KT][2];
-    float scA[NT], scB[NT];  // log2-domain logit scales of this thread's two heads
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int head = nt * 8 + g;
-      const uint2* qh = reinterpret_cast<const uint2*>(
-          reinterpret_cast<const T*>(p.q) + ((int64_t)wk.b * p.Hq + wk.kvh * G + (head < G ? head : 0)) * D +
-          t * (D / 4));
-      float scale = p.scale_log2;
-      if constexpr (kBf16) {
-        float2 f[KT][2];
-        float mx = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-          const uint2 x = head < G ? qh[kk] : make_uint2(0u, 0u);
-          f[kk][0] = Elem<T>::to_f2(x.x);
-          f[kk][1] = Elem<T>::to_f2(x.y);
-          mx = fmaxf(mx, fmaxf(fmaxf(fabsf(f[kk][0].x), fabsf(f[kk][0].y)),
-                               fmaxf(fabsf(f[kk][1].x), fabsf(f[kk][1].y))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // Exponent of the largest |q|, kept where 2^e and 2^-e are normal; infinite q: 0.
-        int e = (int)(__float_as_uint(mx) >> 23) - 127;
-        e = e == 128 ? 0 : max(-126, min(126, e));
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-          qb[nt][kk][0] = pack2<__half>(f[kk][0].x * down, f[kk][0].y * down);
-          qb[nt][kk][1] = pack2<__half>(f[kk][1].x * down, f[kk][1].y * down);
-        }
-        scale *= __uint_as_float((uint32_t)(127 + e) << 23);
-      } else {
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-          const uint2 x = head < G ? qh[kk] : make_uint2(0u, 0u);
-          qb[nt][kk][0] = x.x;
-          qb[nt][kk][1] = x.y;
-        }
-      }
-      scA[nt] = __shfl_sync(0xffffffffu, scale, 4 * qcol);
-      scB[nt] = __shfl_sync(0xffffffffu, scale, 4 * qcol + 4);
-    }
-    float o[NT][KT][4];
-    // l: sums of the fp32 weights (for lse); lr: of the f16 weights P.V uses (for out).
-    float mA[NT], mB[NT], lA[NT], lB[NT], lrA[NT], lrB[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int mi = 0; mi < KT; ++mi) o[nt][mi][0] = o[nt][mi][1] = o[nt][mi][2] = o[nt][mi][3] = 0.f;
-      mA[nt] = mB[nt] = -INFINITY;
-      lA[nt] = lB[nt] = lrA[nt] = lrB[nt] = 0.f;
-    }
-    constexpr int SUB = TILE / (kConsumerWarps * 16);  // blocks of 16 tokens per warp and tile
+    // The tile is 8 blocks of 16 tokens; each warp takes SUB neighbouring ones.
+    constexpr int SUB = TILE / (kConsumerWarps * 16);
     static_assert(SUB * kConsumerWarps * 16 == TILE, "the tile splits into 16-token blocks");
+    Kv4Warp<T, D, G> w;
+    w.load_q(p, wk.b, wk.kvh);
     const int tok0 = warp * 16 * SUB;
-    // This thread's byte offsets in a block (fd.h, "4-bit blocks").
-    const int k_at = g * (D / 2) + t * (D / 8), ks_at = 8 * D + g * (D / 16) + t * (D / 64);
-    const int vg = g * D, vswap = ((D == 128 ? g : g >> 1) & 1) << 2;
-    const int v_at0 = vg + (t ^ vswap) * (D / 8), v_at1 = vg + ((t + 4) ^ vswap) * (D / 8);
-    const int vs_at = 8 * D + (D == 128 ? g : g >> 1) * 16 + 2 * t;
-
     for (int kt = 0; kt < ntiles; ++kt) {
       const int s = kt % NSLOT;
       const bool ok = mbar_wait(full_bar(s), (kt / NSLOT) & 1);
@@ -1797,192 +1734,17 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
         }
         break;
       }
-      const int ntok = min(TILE, wk.t1 - (wk.t0 + kt * TILE));
-      if (tok0 < ntok) {
-        const uint8_t* kblk = smem + (size_t)s * kSlotBytes + warp * SUB * BLK;
-        const uint8_t* vblk = kblk + kRowsBytes;
-        float sc[SUB][NT][4];
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          // K: rows g and g + 8 of block u; kw words of 8 elements, ks the scales as pairs.
-          uint32_t kw[2][2 * NW], ks[2][NW];
-#pragma unroll
-          for (int rh = 0; rh < 2; ++rh) {
-            const uint8_t* row = kblk + u * BLK + rh * (4 * D) + k_at;
-            const uint8_t* srow = kblk + u * BLK + rh * (D / 2) + ks_at;
-            if constexpr (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(row);
-              kw[rh][0] = x.x; kw[rh][1] = x.y; kw[rh][2] = x.z; kw[rh][3] = x.w;
-              const uint32_t z = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(srow));
-              ks[rh][0] = __byte_perm(z, z, 0x1010);
-              ks[rh][1] = __byte_perm(z, z, 0x3232);
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(row);
-              kw[rh][0] = x.x; kw[rh][1] = x.y;
-              const uint32_t z = e4m3x2_to_f16x2(*srow);
-              ks[rh][0] = __byte_perm(z, z, 0x1010);
-            }
-          }
-          // Two accumulators (even and odd words) halve the chains of dependent mma.
-          float sd[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[u][nt][i] = sd[nt][i] = 0.f;
-#pragma unroll
-          for (int wi = 0; wi < 2 * NW; ++wi) {  // a word: k-steps 2 wi and 2 wi + 1
-            uint32_t x0[4], x1[4];
-            e2m1x8_to_f16x8(kw[0][wi], x0);
-            e2m1x8_to_f16x8(kw[1][wi], x1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t a[4] = {hmul2(x0[2 * h], ks[0][wi >> 1]), hmul2(x1[2 * h], ks[1][wi >> 1]),
-                                     hmul2(x0[2 * h + 1], ks[0][wi >> 1]), hmul2(x1[2 * h + 1], ks[1][wi >> 1])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<__half>(h ? sd[nt] : sc[u][nt], a, qb[nt][2 * wi + h][0], qb[nt][2 * wi + h][1]);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[u][nt][i] += sd[nt][i];
-        }
-        uint32_t pb0[SUB][NT], pb1[SUB][NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float sA0[SUB], sB0[SUB], sA1[SUB], sB1[SUB];
-          float xA = -INFINITY, xB = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < SUB; ++u) {
-            // Tokens past the end are selected away: their bytes may be anything.
-            const bool v0 = tok0 + 16 * u + g < ntok, v1 = tok0 + 16 * u + g + 8 < ntok;
-            sA0[u] = v0 ? sc[u][nt][0] * scA[nt] : -INFINITY;
-            sB0[u] = v0 ? sc[u][nt][1] * scB[nt] : -INFINITY;
-            sA1[u] = v1 ? sc[u][nt][2] * scA[nt] : -INFINITY;
-            sB1[u] = v1 ? sc[u][nt][3] * scB[nt] : -INFINITY;
-            xA = fmaxf(xA, fmaxf(sA0[u], sA1[u]));
-            xB = fmaxf(xB, fmaxf(sB0[u], sB1[u]));
-          }
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) {
-            xA = fmaxf(xA, __shfl_xor_sync(0xffffffffu, xA, off));
-            xB = fmaxf(xB, __shfl_xor_sync(0xffffffffu, xB, off));
-          }
-          if (xA > mA[nt] + kRescaleThreshold) {
-            const float corr = ex2(mA[nt] - xA);
-            lA[nt] *= corr;
-            lrA[nt] *= corr;
-#pragma unroll
-            for (int mi = 0; mi < KT; ++mi) { o[nt][mi][0] *= corr; o[nt][mi][2] *= corr; }
-            mA[nt] = xA;
-          }
-          if (xB > mB[nt] + kRescaleThreshold) {
-            const float corr = ex2(mB[nt] - xB);
-            lB[nt] *= corr;
-            lrB[nt] *= corr;
-#pragma unroll
-            for (int mi = 0; mi < KT; ++mi) { o[nt][mi][1] *= corr; o[nt][mi][3] *= corr; }
-            mB[nt] = xB;
-          }
-          // Row tok0 is valid, so the column maxima (and mA, mB) are finite here.
-#pragma unroll
-          for (int u = 0; u < SUB; ++u) {
-            const float pA0 = ex2(sA0[u] - mA[nt]), pB0 = ex2(sB0[u] - mB[nt]);
-            const float pA1 = ex2(sA1[u] - mA[nt]), pB1 = ex2(sB1[u] - mB[nt]);
-            lA[nt] += pA0 + pA1;
-            lB[nt] += pB0 + pB1;
-            const uint32_t r0 = pack2<__half>(pA0, pB0), r1 = pack2<__half>(pA1, pB1);
-            // lr sums the same f16 weights that P.V multiplies.
-            const float2 w0 = Elem<__half>::to_f2(r0), w1 = Elem<__half>::to_f2(r1);
-            lrA[nt] += w0.x + w1.x;
-            lrB[nt] += w0.y + w1.y;
-            pb0[u][nt] = movmatrix_trans(r0);
-            pb1[u][nt] = movmatrix_trans(r1);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          // V^T: tokens 2t, 2t + 1 (words e[0], scales vs[0]) and 2t + 8, 2t + 9 (e[1], vs[1]).
-          uint32_t ve[2][NW], vo[2][NW], vs[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint8_t* at = vblk + u * BLK + (i ? v_at1 : v_at0);
-            if constexpr (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(at);
-              ve[i][0] = x.x; ve[i][1] = x.y; vo[i][0] = x.z; vo[i][1] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(at);
-              ve[i][0] = x.x; vo[i][0] = x.y;
-            }
-            vs[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(vblk + u * BLK + vs_at + 8 * i));
-            const int left = ntok - (tok0 + 16 * u + 8 * i + 2 * t);  // valid tokens of the pair
-            // A weight of 0 times a NaN scale would be NaN: scales past the end become 0.
-            if (left < 2) vs[i] = left < 1 ? 0u : vs[i] & 0xffffu;
-          }
-#pragma unroll
-          for (int wi = 0; wi < NW; ++wi) {
-            // Half-bytes of the two tokens of a pair side by side: even dims in x, odd in y.
-            uint32_t f[2][2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t a = ve[i][wi], b = vo[i][wi];
-              e2m1x8_to_f16x8((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), f[i][0]);
-              e2m1x8_to_f16x8(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), f[i][1]);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t a[4] = {hmul2(f[0][0][j], vs[0]), hmul2(f[0][1][j], vs[0]),
-                                     hmul2(f[1][0][j], vs[1]), hmul2(f[1][1][j], vs[1])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<__half>(o[nt][4 * wi + j], a, pb0[u][nt], pb1[u][nt]);
-            }
-          }
-        }
+      const int ntok = min(TILE, wk.t1 - (wk.t0 + kt * TILE)) - tok0;
+      if (ntok > 0) {
+        const uint8_t* kblk = smem + (size_t)s * kSlotBytes + warp * SUB * Kv4Warp<T, D, G>::BLK;
+        w.template blocks<SUB>(kblk, kblk + kRowsBytes, ntok);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(s));
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        lA[nt] += __shfl_xor_sync(0xffffffffu, lA[nt], off);
-        lB[nt] += __shfl_xor_sync(0xffffffffu, lB[nt], off);
-        lrA[nt] += __shfl_xor_sync(0xffffffffu, lrA[nt], off);
-        lrB[nt] += __shfl_xor_sync(0xffffffffu, lrB[nt], off);
-      }
-    }
+    w.finish();
     __syncthreads();  // ring drained: reuse it for the per-warp states
-    if (*(volatile int*)&sm_abort == 0) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int hA = nt * 8 + qcol;
-        if (hA < G) {
-          float* accA = sm_acc + (warp * G + hA) * D + g * (D / 8);
-#pragma unroll
-          for (int mi = 0; mi < KT; ++mi) {
-            accA[2 * mi] = o[nt][mi][0];
-            accA[2 * mi + 1] = o[nt][mi][2];
-            if (G > 1) {
-              accA[D + 2 * mi] = o[nt][mi][1];
-              accA[D + 2 * mi + 1] = o[nt][mi][3];
-            }
-          }
-          if (g == 0) {
-            sm_m[warp * G + hA] = mA[nt];
-            sm_l[warp * G + hA] = lA[nt];
-            sm_lr[warp * G + hA] = lrA[nt];
-            if (G > 1) {
-              sm_m[warp * G + hA + 1] = mB[nt];
-              sm_l[warp * G + hA + 1] = lB[nt];
-              sm_lr[warp * G + hA + 1] = lrB[nt];
-            }
-          }
-        }
-      }
-    }
+    if (*(volatile int*)&sm_abort == 0) w.store(sm_acc + warp * G * D, sm_m + warp * G, sm_l + warp * G, sm_lr + warp * G);
   } else if constexpr (PATH == kPathMma) {
     // ---------------- MMA consumers ----------------
     constexpr int KT = D / 16;            // k-steps of S = K Q^T, m-tiles of O^T
@@ -2435,12 +2197,43 @@ cudaError_t launch_typed_mma(const Params& p, int d, int G, int path, int mode, 
   return cudaErrorInvalidValue;
 }
 
+// The stream kernel over a 4-bit cache (host mode 8).
+template <typename T, int D, int G>
+cudaError_t launch_kv4_stream(const Params& p, bool pdl, int grid, cudaStream_t stream) {
+  using S = dev::Kv4Stream<D, G>;
+  const void* fn = reinterpret_cast<const void*>(&dev::fd_kv4_stream_kernel<T, D, G>);
+  int dev_id = 0;
+  cudaError_t err = cudaGetDevice(&dev_id);
+  if (err != cudaSuccess) return err;
+  static uint64_t done_mask = 0;  // devices whose shared-memory limit is set for this kernel
+  const uint64_t bit = 1ull << (dev_id & 63);
+  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
+    err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmemBytes);
+    if (err != cudaSuccess) return err;
+    __atomic_fetch_or(&done_mask, bit, __ATOMIC_RELEASE);
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* args[] = {const_cast<Params*>(&p)};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
 // The consumers over a 4-bit cache; their own translation units.
 template <typename T>
 cudaError_t launch_typed_kv4(const Params& p, int d, int G, int mode, bool pdl, int grid,
                              cudaStream_t s) {
-#define FD_CASE(DD, GG) \
-  if (d == DD && G == GG) return launch_dgp<T, DD, GG, kPathMmaKv4>(p, mode, pdl, grid, s);
+#define FD_CASE(DD, GG)                                                            \
+  if (d == DD && G == GG)                                                          \
+    return mode == kModeStream ? launch_kv4_stream<T, DD, GG>(p, pdl, grid, s)     \
+                               : launch_dgp<T, DD, GG, kPathMmaKv4>(p, mode, pdl, grid, s);
   FD_CASE(64, 1) FD_CASE(64, 2) FD_CASE(64, 4) FD_CASE(64, 8) FD_CASE(64, 16)
   FD_CASE(128, 1) FD_CASE(128, 2) FD_CASE(128, 4) FD_CASE(128, 8) FD_CASE(128, 16)
 #undef FD_CASE

@@ -8,6 +8,7 @@ struct fd_plan_s {
   uint32_t flags;
   int C;
   int path;       // fd::kPathFfma, kPathMma, kPathMmaKv8, kPathUmma or kPathMmaKv4
+  bool stream;    // 4-bit caches: equal runs of tiles per CTA instead of W * C partials
   int page_size;  // 0: contiguous K/V; else tokens per page of a paged cache
   int max_pages;  // max_b ceil(L_b / page_size) (paged plans)
   int num_sms;
@@ -36,7 +37,7 @@ namespace fd {
 // Kernel mode of a one-launch decode: fine-grained waits (3), every partial of a pair
 // in one cluster (6), or the last-arriver combine (0).
 inline int fused_mode(const fd_plan_s* pl) {
-  return (pl->flags & FD_PLAN_WAITS) ? 3 : (pl->flags & FD_PLAN_CLUSTER_COMBINE) ? 6 : 0;
+  return pl->stream ? kModeStream : (pl->flags & FD_PLAN_WAITS) ? 3 : (pl->flags & FD_PLAN_CLUSTER_COMBINE) ? 6 : 0;
 }
 // fd_status of a failed launch: a grid that cannot be co-resident (cooperative
 // launch) or a cluster the device cannot place is unsupported; anything else is a

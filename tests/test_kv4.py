@@ -226,17 +226,38 @@ def test_batch_of_256(fd):
     c.check(*c.run(c.decoder()))
 
 
-def test_pipeline_wait_timeout_is_reported(fd):
-    """A tile that is never loaded (test hook): the bounded wait gives up, the status says so."""
+@pytest.mark.parametrize("stream", [True, False])
+def test_pipeline_wait_timeout_is_reported(fd, stream):
+    """A tile that is never loaded (test hook): the bounded wait gives up, the status says so, every
+    counter returns to zero, and the next decode on the workspace is right."""
     import torch
-    c = Case(fd, "f16_e2m1kv", 128, 4, 2, [6000, 300], [4, 2], seed=16)
-    dec = c.decoder(flags=fd.FD_PLAN_TEST_SKIP_TILE)
-    lo, hi = dec.plan.range(0, 0)
-    assert hi - lo > 128
-    dec(c.q, c.k, c.v)
+    c = Case(fd, "f16_e2m1kv", 128, 4, 2, [20000, 300], [4, 2], seed=16)
+    chunks = 0 if stream else 1
+    dec = c.decoder(flags=fd.FD_PLAN_TEST_SKIP_TILE, chunks=chunks, num_sms=8)
+    assert dec.info["stream"] == stream
+    out, lse = dec(c.q, c.k, c.v)
     assert dec.status() == fd.FD_ERR_TIMEOUT
-    clean = fd.fd_plan(2, 8, 2, 128, c.seqlens, c.W, c.dtype)
+    assert not dec.workspace[256:256 + 4 * 2 * 2].any()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    clean = fd.fd_plan(2, 8, 2, 128, c.seqlens, c.W, c.dtype, chunks=chunks, num_sms=8)
     out, lse = torch.empty_like(c.q), torch.empty((2, 8), dtype=torch.float32, device="cuda")
     fd.fd_decode(clean, c.q, c.k, c.v, out, lse, dec.workspace)
     assert fd.fd_workspace_status(clean, dec.workspace) == fd.FD_OK
     c.check(f64(out), f64(lse))
+
+
+def test_stream_runs_cut_anywhere(fd):
+    """Runs of half tiles that start and end inside pairs, cover whole pairs, or hold one half tile;
+    empty sequences between them.  The counters are at rest after each decode."""
+    for i, (lens, Hkv, sms) in enumerate([
+            ([3000, 0, 0, 5, 700], 3, 7), ([0, 0, 64, 65, 63, 0], 2, 2), ([0], 4, 152), ([10000], 1, 152),
+            ([1] * 100 + [4000], 1, 5), ([200, 9000], 5, 1), ([0, 0, 0], 1, 152)]):
+        for G, dtype in ((2, "f16_e2m1kv"), (8, "bf16_e2m1kv"), (16, "f16_e2m1kv")):
+            c = Case(fd, dtype, 64 if G == 2 else 128, G, Hkv, lens, [1] * len(lens), seed=i)
+            dec = c.decoder(num_sms=sms)
+            assert dec.info["stream"] == 1
+            first = c.run(dec)
+            c.check(*first)
+            again = c.run(dec)
+            assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+            assert not dec.workspace[256:256 + 4 * len(lens) * Hkv].any()

@@ -201,8 +201,17 @@ def test_four_bit_plan(dtype, d, G):
     lens, W = [5000, 0, 1, 33, 1031], [3, 1, 2, 4, 8]
     p = fd.fd_plan(5, 8 * G, 8, d, lens, W, dtype, num_sms=152)
     assert p.info["path"] == 4 and p.info["kv_bytes"] == sum(lens) * 8 * 2 * 9 * d // 16
-    paged = fd.fd_plan_paged(5, 8 * G, 8, d, lens, W, 64, dtype, num_sms=152)
+    # By default the resident CTAs take equal runs of half tiles; W * C partials on request.
+    assert p.info["stream"] == 1 and p.info["ctas"] == 152 * p.info["ctas_per_sm"]
+    with pytest.raises(fd.FdError) as e:
+        p.range(0, 0)
+    assert e.value.status == fd.FD_ERR_UNSUPPORTED
+    for flags in (fd.FD_PLAN_LITERAL_W, fd.FD_PLAN_TWO_LAUNCH, fd.FD_PLAN_WAITS, fd.FD_PLAN_NO_CLUSTER):
+        assert fd.fd_plan(5, 8 * G, 8, d, lens, W, dtype, flags=flags, num_sms=152).info["stream"] == 0
+    p = fd.fd_plan(5, 8 * G, 8, d, lens, W, dtype, chunks=3, num_sms=152)
+    paged = fd.fd_plan_paged(5, 8 * G, 8, d, lens, W, 64, dtype, chunks=2, num_sms=152)
     for plan, unit in ((p, 16), (paged, 128)):
+        assert plan.info["stream"] == 0
         C = plan.info["chunks"]
         for b, L in enumerate(lens):
             at = 0
