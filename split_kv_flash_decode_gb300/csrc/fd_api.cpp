@@ -80,7 +80,10 @@ int fd::encode_kv_map(CUtensorMap* map, const void* base, int64_t rows, int box_
   const CUtensorMapSwizzle swz =
       fd::is_mma(pl->path) && !kv4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
   CUresult r = enc(map, ty, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                   // 4-bit blocks start at multiples of 128 bytes only: 256-byte sectors would
+                   // fetch beyond them (the loads of 604 MB alone: 94 against 90 us).
+                   kv4 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FD_OK : FD_ERR_CUDA;
 }
@@ -345,7 +348,7 @@ int plan_impl(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32
         most = std::max<int64_t>(most, std::min<int64_t>(n, (units_of(seqlens[b]) - 2) / p.run_len + 2));
       }
       p.unit_base[B] = base;
-      p.box_rows = page_size ? std::min(tile, page_size) : tile;
+      p.box_rows = page_size ? std::min(fd::kStreamSlotTokens, page_size) : fd::kStreamSlotTokens;
       p.rps = C;
       p.combiners = 1;
       p.ctas_per_sm = fd::stream_ctas(G);

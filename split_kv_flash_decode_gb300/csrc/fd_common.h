@@ -62,7 +62,8 @@ FD_HD constexpr int row_tokens(int path) { return path == kPathMmaKv4 ? kBlockTo
 // The 4-bit stream kernel: warps per CTA and CTAs per SM, by the registers a group of heads takes.
 FD_HD constexpr int stream_warps(int G) { return G <= 8 ? KV4_WARPS : 12; }
 FD_HD constexpr int stream_ctas(int G) { return G <= 8 ? KV4_SCTAS : 1; }
-constexpr int kStreamTile = 128;  // tokens per ring slot
+constexpr int kStreamTile = 128;  // tokens that four warps take together
+constexpr int kStreamSlotTokens = 32;
 #ifndef KV4_UNITS
 #define KV4_UNITS 4
 #endif
