@@ -49,7 +49,8 @@ struct Kv4Warp {
   // l: sums of the fp32 weights (for lse); lr: of the weights P.V uses (for out).
   float mA[NT], mB[NT], lA[NT], lB[NT], lrA[NT], lrB[NT];
 
-  __device__ __forceinline__ void load_q(const Params& p, int b, int kvh) {
+  // q of (sequence, KV head) as it is stored: issues the loads.
+  __device__ __forceinline__ void fetch_q(const Params& p, int b, int kvh) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -65,6 +66,10 @@ struct Kv4Warp {
         qb[nt][kk][1] = x.y;
       }
     }
+  }
+  // Makes the fetched q the B operand, and starts from the empty state.
+  __device__ __forceinline__ void start(const Params& p) {
+    const int t = threadIdx.x & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float scale = p.scale_log2;
@@ -95,6 +100,11 @@ struct Kv4Warp {
       mA[nt] = mB[nt] = -INFINITY;
       lA[nt] = lB[nt] = lrA[nt] = lrB[nt] = 0.f;
     }
+  }
+
+  __device__ __forceinline__ void load_q(const Params& p, int b, int kvh) {
+    fetch_q(p, b, kvh);
+    start(p);
   }
 
   // SUB blocks of 16 tokens, BLK bytes apart, of which `ntok` (at least one) tokens are valid.
@@ -648,22 +658,28 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
   };
   __syncwarp();
   pdl_wait();  // q, K, V, the workspace and out may come from earlier kernels
+  // q ahead of K and V: behind them it would wait for the whole ring (3 us when all CTAs start).
+  W w;
+  w.fetch_q(p, sp.b, sp.kvh);
 #pragma unroll 1
   for (int s = 0; s < NSLOT; ++s) load_next(s);
   __syncthreads();
 
-  W w;
   bool gave_up = false;
   int turn = quad;     // tiles of the run until the quad's next one
   int slot = 0;        // the warp's next slot, and the parity of its barrier
   uint32_t parity = 0;
+  // Pairs that other CTAs share: the arrival's answer, read at the end of the run.
+  uint32_t arrived0 = 0, arrived1 = 0;  // thread 0's
+  StreamPair shared0 = sp, shared1 = sp;
+  int n_shared = 0;
 #pragma unroll 1
-  for (int i = i0; i < i1; sp.next(p)) {
+  for (int i = i0; i < i1;) {
     const int end = min(i1, sp.at + sp.units);
     const int ta = sp.first_tile(i), nt = sp.first_tile(end) - ta;
     i = end;
-    if (nt <= 0) continue;  // the run ends before the pair's first tile
-    w.load_q(p, sp.b, sp.kvh);
+    if (nt <= 0) break;  // the run ends before the pair's first tile
+    w.start(p);
     if (sp.len > 0) {
       int ntok = sp.len - (ta + turn) * kTile - first_token;
 #pragma unroll 1
@@ -686,17 +702,21 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
       }
       turn -= nt;
     }
+    const StreamPair done = sp;
+    sp.next(p);
+    // The next piece's q, on its way while the states are merged.
+    if (i < i1) w.fetch_q(p, sp.b, sp.kvh);
     // Merge the warps' states: common maxima first, then plain sums.
     w.template put_max<NW>(st_m, warp);
     __syncthreads();
     w.template put_state<NW>(st_frag + warp * S::kItems, st_m, st_l, st_lr, warp);
     __syncthreads();
     const bool aborted = words[0] != 0;  // a CTA that gave up contributes empty partials
-    const bool whole = ta == 0 && nt == sp.units - kPairUnits;
-    T* out = reinterpret_cast<T*>(p.out) + ((int64_t)sp.b * p.Hq + sp.kvh * G) * D;
-    float* lse = p.lse == nullptr ? nullptr : p.lse + (int64_t)sp.b * p.Hq + sp.kvh * G;
+    const bool whole = ta == 0 && nt == done.units - kPairUnits;
+    T* out = reinterpret_cast<T*>(p.out) + ((int64_t)done.b * p.Hq + done.kvh * G) * D;
+    float* lse = p.lse == nullptr ? nullptr : p.lse + (int64_t)done.b * p.Hq + done.kvh * G;
     // Record 0 of a CTA: of a piece whose pair begins no later than its run; record 1: of its last.
-    float* rec = p.part + ((int64_t)c * 2 + (i0 >= sp.at ? 0 : 1)) * S::kRecord;
+    float* rec = p.part + ((int64_t)c * 2 + (i0 >= done.at ? 0 : 1)) * S::kRecord;
     for (int v = tid; v < S::kItems; v += S::kThreads) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       if (!aborted) {
@@ -726,86 +746,107 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
         __stcg(reinterpret_cast<float4*>(rec + H * D) + tid, make_float4(M, l, lr, 0.f));
       }
     }
+    __syncthreads();  // the next piece overwrites the states
     if (!whole) {
       // Arrival, as in finish_cta: the barrier orders the CTA's stores before thread 0's release.
-      const int c_first = stream_cta(p, sp.at + kPairUnits), nrec = stream_cta(p, sp.at + sp.units - 1) - c_first + 1;
-      __syncthreads();
+      // Whether this CTA was the last of the pair is asked at the end of its run.
       if (tid == 0) {
-        uint32_t* cnt = p.counters + (int64_t)sp.b * p.Hkv + sp.kvh;
-        const uint32_t old = atom_add_acq_rel_gpu(cnt, 1u);
-        if (old >= (uint32_t)nrec) atomicOr(p.status, kStatusCounter);
-        const bool last = old == (uint32_t)(nrec - 1);
-        if (last) *cnt = 0u;  // every CTA of the pair has arrived
-        words[1] = last;
+        const uint32_t old = atom_add_acq_rel_gpu(p.counters + (int64_t)done.b * p.Hkv + done.kvh, 1u);
+        if (n_shared == 0) arrived0 = old; else arrived1 = old;
       }
-      __syncthreads();
-      if (words[1]) {
-        // Combine the pair's records, in CTA order.  Only its first CTA can have begun before it.
-        float4* sums = st_frag;                                                    // [kSplit][kItems]
-        float* coef = reinterpret_cast<float*>(st_frag + S::kSplit * S::kItems);   // [H][nrec]
-        const float* rec1 = p.part + (int64_t)c_first * 2 * S::kRecord;
-        const float* rec0 = rec1 + (stream_begin(p, c_first) >= sp.at ? 0 : S::kRecord);
-        auto record = [&](int r) { return r == 0 ? rec0 : rec1 + (int64_t)r * 2 * S::kRecord; };
-        for (int g = warp; g < H; g += NW) {
-          float M = -INFINITY, l = 0.f, lr = 0.f;
-          for (int r = lane; r < nrec; r += 32) {
-            const float4 ml = __ldcg(reinterpret_cast<const float4*>(record(r) + H * D) + g);
-            coef[g * nrec + r] = ml.x;
-            stream_merge(M, l, lr, ml.x, ml.y, ml.z);
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, M, off);
-            const float l2 = __shfl_xor_sync(0xffffffffu, l, off);
-            const float lr2 = __shfl_xor_sync(0xffffffffu, lr, off);
-            stream_merge(M, l, lr, m2, l2, lr2);
-          }
-          for (int r = lane; r < nrec; r += 32)
-            coef[g * nrec + r] = M == -INFINITY ? 0.f : ex2(coef[g * nrec + r] - M);
-          if (lane == 0) {
-            st_lr[g] = lr;
-            if (lse != nullptr && g < G) lse[g] = l != 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
-          }
-        }
-        __syncthreads();
-        for (int v = tid; v < S::kItems * S::kSplit; v += S::kThreads) {
-          const int q = v / S::kItems, it = v - q * S::kItems, h = W::frag_head(it >> 5, lane);
-          const float *cA = coef + h * nrec, *cB = cA + nrec;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (n_shared == 0) shared0 = done; else shared1 = done;
+      ++n_shared;
+    }
+  }
+
+  // The pairs that this CTA shares with others and was the last to arrive at: combine their
+  // records, in CTA order.  Only a pair's first CTA can have begun before it.
 #pragma unroll 1
-          for (int r = q; r < nrec; r += 8 * S::kSplit) {
-            float4 x[8];
+  for (int k = 0; k < n_shared; ++k) {
+    const StreamPair pr = k == 0 ? shared0 : shared1;
+    const int c_first = stream_cta(p, pr.at + kPairUnits), nrec = stream_cta(p, pr.at + pr.units - 1) - c_first + 1;
+    if (tid == 0) {
+      const uint32_t old = k == 0 ? arrived0 : arrived1;
+      if (old >= (uint32_t)nrec) atomicOr(p.status, kStatusCounter);
+      const bool last = old == (uint32_t)(nrec - 1);
+      if (last) p.counters[(int64_t)pr.b * p.Hkv + pr.kvh] = 0u;  // every CTA of the pair has arrived
+      words[1] = last;
+    }
+    __syncthreads();
+    const bool last = words[1] != 0;
+    __syncthreads();
+    if (!last) continue;
+    T* out = reinterpret_cast<T*>(p.out) + ((int64_t)pr.b * p.Hq + pr.kvh * G) * D;
+    float* lse = p.lse == nullptr ? nullptr : p.lse + (int64_t)pr.b * p.Hq + pr.kvh * G;
+    float4* sums = st_frag;                                                    // [kSplit][kItems]
+    float* coef = reinterpret_cast<float*>(st_frag + S::kSplit * S::kItems);   // [H][nrec]
+    const float* rec1 = p.part + (int64_t)c_first * 2 * S::kRecord;
+    const float* rec0 = rec1 + (stream_begin(p, c_first) >= pr.at ? 0 : S::kRecord);
+    auto record = [&](int r) { return r == 0 ? rec0 : rec1 + (int64_t)r * 2 * S::kRecord; };
+    // Thread v: fragment v mod kItems of every kSplit-th record, eight at a time; the first eight
+    // are on their way while the coefficients are computed.
+    float4 x[8];
+    auto fetch = [&](int it, int r) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              if (r + u * S::kSplit < nrec)
-                x[u] = __ldcg(reinterpret_cast<const float4*>(record(r + u * S::kSplit)) + it);
+      for (int u = 0; u < 8; ++u)
+        if (r + u * S::kSplit < nrec) x[u] = __ldcg(reinterpret_cast<const float4*>(record(r + u * S::kSplit)) + it);
+    };
+    if (tid < S::kItems * S::kSplit) fetch(tid % S::kItems, tid / S::kItems);
+    for (int g = warp; g < H; g += NW) {
+      float M = -INFINITY, l = 0.f, lr = 0.f;
+      for (int r = lane; r < nrec; r += 32) {
+        const float4 ml = __ldcg(reinterpret_cast<const float4*>(record(r) + H * D) + g);
+        coef[g * nrec + r] = ml.x;
+        stream_merge(M, l, lr, ml.x, ml.y, ml.z);
+      }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              if (r + u * S::kSplit < nrec) {
-                const float fA = cA[r + u * S::kSplit], fB = cB[r + u * S::kSplit];
-                a.x = fmaf(x[u].x, fA, a.x);
-                a.y = fmaf(x[u].y, fB, a.y);
-                a.z = fmaf(x[u].z, fA, a.z);
-                a.w = fmaf(x[u].w, fB, a.w);
-              }
-            }
-          }
-          sums[v] = a;
-        }
-        __syncthreads();
-        for (int v = tid; v < S::kItems; v += S::kThreads) {
-          float4 a = sums[v];
-          if constexpr (S::kSplit == 2) {
-            const float4 x = sums[S::kItems + v];
-            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-          }
-          const int h = W::frag_head(v >> 5, lane);
-          const float lA = st_lr[h], lB = st_lr[h + 1];
-          W::put_out(out, v >> 5, lane, a, lA != 0.f ? 1.f / lA : 0.f, lB != 0.f ? 1.f / lB : 0.f);
-        }
+      for (int off = 16; off > 0; off >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, M, off);
+        const float l2 = __shfl_xor_sync(0xffffffffu, l, off);
+        const float lr2 = __shfl_xor_sync(0xffffffffu, lr, off);
+        stream_merge(M, l, lr, m2, l2, lr2);
+      }
+      for (int r = lane; r < nrec; r += 32)
+        coef[g * nrec + r] = M == -INFINITY ? 0.f : ex2(coef[g * nrec + r] - M);
+      if (lane == 0) {
+        st_lr[g] = lr;
+        if (lse != nullptr && g < G) lse[g] = l != 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
       }
     }
-    __syncthreads();  // the next piece overwrites the states
+    __syncthreads();
+#pragma unroll 1
+    for (int v = tid; v < S::kItems * S::kSplit; v += S::kThreads) {
+      const int q = v / S::kItems, it = v - q * S::kItems, h = W::frag_head(it >> 5, lane);
+      const float *cA = coef + h * nrec, *cB = cA + nrec;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int r = q; r < nrec; r += 8 * S::kSplit) {
+        if (v != tid || r != q) fetch(it, r);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (r + u * S::kSplit < nrec) {
+            const float fA = cA[r + u * S::kSplit], fB = cB[r + u * S::kSplit];
+            a.x = fmaf(x[u].x, fA, a.x);
+            a.y = fmaf(x[u].y, fB, a.y);
+            a.z = fmaf(x[u].z, fA, a.z);
+            a.w = fmaf(x[u].w, fB, a.w);
+          }
+        }
+      }
+      sums[v] = a;
+    }
+    __syncthreads();
+    for (int v = tid; v < S::kItems; v += S::kThreads) {
+      float4 a = sums[v];
+      if constexpr (S::kSplit == 2) {
+        const float4 y = sums[S::kItems + v];
+        a.x += y.x; a.y += y.y; a.z += y.z; a.w += y.w;
+      }
+      const int h = W::frag_head(v >> 5, lane);
+      const float lA = st_lr[h], lB = st_lr[h + 1];
+      W::put_out(out, v >> 5, lane, a, lA != 0.f ? 1.f / lA : 0.f, lB != 0.f ? 1.f / lB : 0.f);
+    }
+    __syncthreads();  // the next pair overwrites the sums
   }
   // A warp that gave up leaves loads behind: they must land before shared memory is released.
   if (gave_up && lane == 0)
