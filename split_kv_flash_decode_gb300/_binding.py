@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libfd_gb300.so")
@@ -114,6 +115,12 @@ class AppendArgs(ctypes.Structure):
     ]
 
 
+# AppendArgs as one struct.pack call (null pointers are 0): a tenth of the time that setting the
+# fields one by one takes.
+APPEND_ARGS = struct.Struct("@3P6q2i2P2f2Pq4P2f2i2P")
+assert APPEND_ARGS.size == ctypes.sizeof(AppendArgs)
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -173,7 +180,7 @@ def lib() -> ctypes.CDLL:
             L.fd_rows_destroy.restype = ctypes.c_int
             L.fd_rows_get_info.argtypes = [vp, ctypes.POINTER(RowsInfo)]
             L.fd_rows_get_info.restype = ctypes.c_int
-            L.fd_append.argtypes = [vp, ctypes.POINTER(AppendArgs), vp]
+            L.fd_append.argtypes = [vp, vp, vp]  # byref(AppendArgs), or its bytes (APPEND_ARGS)
             L.fd_append.restype = ctypes.c_int
             L.fd_gather.argtypes = [vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, vp]
             L.fd_gather.restype = ctypes.c_int
@@ -216,6 +223,23 @@ def _stream(stream) -> int:
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
+
+
+def on_device(index: int, call, *args) -> int:
+    """call(*args) with CUDA device `index` current."""
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
+
+
+def stream_on(index: int, stream) -> int:
+    """Address of `stream`, or of torch's current stream of device `index`."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return _stream(stream)
 
 
 class Plan:

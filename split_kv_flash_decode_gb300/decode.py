@@ -40,6 +40,7 @@ class Decoder:
         self.Hq, self.Hkv, self.d, self.dtype = int(Hq), int(Hkv), int(d), dtype
         self.n_tokens = sum(self.seqlens)
         self.page_size = int(page_size)
+        self._q_shape = (self.Bsz, self.Hq, self.d)
         with torch.cuda.device(self.device):
             if self.page_size:
                 self.plan = B.fd_plan_paged(self.Bsz, Hq, Hkv, d, self.seqlens, W, self.page_size,
@@ -49,37 +50,47 @@ class Decoder:
                                       num_sms)
             self.workspace = torch.zeros(max(1, self.plan.workspace_bytes), dtype=torch.uint8,
                                          device=self.device)
+        self._workspace_ptr = self.workspace.data_ptr()
+        if self.page_size:
+            self._page_shape = cache_shape(dtype, self.Hkv, self.d, None, 0, self.page_size)[1:]
+        else:
+            self._kv_shape = cache_shape(dtype, self.Hkv, self.d, self.seqlens)
 
     @property
     def info(self) -> dict:
         return self.plan.info
 
-    def _check(self, name, t, shape):
+    def _check(self, name, t, shape, dtype):
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        want = (_KV_DTYPE if name in ("k", "v", "k_pages", "v_pages") else _TORCH_DTYPE)[self.dtype]
-        if t.dtype != want:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {want}")
-        if tuple(t.shape) != tuple(shape):
+        if t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
 
-    def __call__(self, q, k, v, out=None, lse=None, stream=None):
-        self._check("q", q, (self.Bsz, self.Hq, self.d))
-        shape = cache_shape(self.dtype, self.Hkv, self.d, self.seqlens)
-        self._check("k", k, shape)
-        self._check("v", v, shape)
+    def _outputs(self, q, out, lse):
+        """Addresses of q, out and lse, the latter two allocated where missing."""
+        t16 = _TORCH_DTYPE[self.dtype]
+        q_ptr = self._check("q", q, self._q_shape, t16)
         if out is None:
             out = torch.empty_like(q)
-        else:
-            self._check("out", out, (self.Bsz, self.Hq, self.d))
         if lse is None:
-            lse = torch.empty((self.Bsz, self.Hq), dtype=torch.float32, device=self.device)
-        elif lse.dtype != torch.float32 or tuple(lse.shape) != (self.Bsz, self.Hq):
-            raise ValueError("lse must be float32 [B, Hq]")
-        with torch.cuda.device(self.device):
-            B.fd_decode(self.plan, q, k, v, out, lse, self.workspace, stream)
+            lse = torch.empty(self._q_shape[:2], dtype=torch.float32, device=self.device)
+        return (out, lse, q_ptr, self._check("out", out, self._q_shape, t16),
+                self._check("lse", lse, self._q_shape[:2], torch.float32))
+
+    def __call__(self, q, k, v, out=None, lse=None, stream=None):
+        out, lse, q_ptr, out_ptr, lse_ptr = self._outputs(q, out, lse)
+        kv = _KV_DTYPE[self.dtype]
+        k_ptr, v_ptr = self._check("k", k, self._kv_shape, kv), self._check("v", v, self._kv_shape, kv)
+        index = self.device.index
+        rc = B.on_device(index, B.lib().fd_decode, self.plan.handle, q_ptr, k_ptr, v_ptr, out_ptr, lse_ptr,
+                         self._workspace_ptr, B.stream_on(index, stream))
+        if rc != B.FD_OK:
+            raise B.FdError(rc, "fd_decode")
         return out, lse
 
     def decode_paged(self, q, k_pages, v_pages, block_table, out=None, lse=None, stream=None):
@@ -87,22 +98,20 @@ class Decoder:
         int32 block_table [B, stride]."""
         if not self.page_size:
             raise ValueError("this Decoder was planned for contiguous K/V")
-        self._check("q", q, (self.Bsz, self.Hq, self.d))
-        num_pages = k_pages.shape[0]
-        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-            self._check(name, t, cache_shape(self.dtype, self.Hkv, self.d, None, num_pages,
-                                             self.page_size))
+        out, lse, q_ptr, out_ptr, lse_ptr = self._outputs(q, out, lse)
+        kv, num_pages = _KV_DTYPE[self.dtype], k_pages.shape[0]
+        shape = (num_pages, *self._page_shape)
+        k_ptr, v_ptr = self._check("k_pages", k_pages, shape, kv), self._check("v_pages", v_pages, shape, kv)
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
                 block_table.shape[0] != self.Bsz or not block_table.is_contiguous() or \
                 block_table.device != self.device:
             raise ValueError("block_table must be a contiguous int32 [B, stride] tensor on the device")
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((self.Bsz, self.Hq), dtype=torch.float32, device=self.device)
-        with torch.cuda.device(self.device):
-            B.fd_decode_paged(self.plan, q, k_pages, v_pages, num_pages, block_table,
-                              block_table.shape[1], out, lse, self.workspace, stream)
+        index = self.device.index
+        rc = B.on_device(index, B.lib().fd_decode_paged, self.plan.handle, q_ptr, k_ptr, v_ptr, num_pages,
+                         block_table.data_ptr(), block_table.shape[1], out_ptr, lse_ptr,
+                         self._workspace_ptr, B.stream_on(index, stream))
+        if rc != B.FD_OK:
+            raise B.FdError(rc, "fd_decode_paged")
         return out, lse
 
     def status(self, stream=None) -> int:

@@ -38,6 +38,7 @@ class Rope:
                                inv_freq=ctypes.addressof(self._freq),
                                axis=ctypes.addressof(self._axis) if self._axis else None,
                                num_axes=self.num_axes, scale=float(scale))
+        self.address = ctypes.addressof(self.args)
 
 
 class KVRows:
@@ -64,45 +65,48 @@ class KVRows:
         self.rows = B.fd_rows_plan(self.Bsz, self.Hq, self.Hkv, self.d, self.seqlens, begin, count,
                                    self.page_size, dtype)
         self.tokens = self.rows.tokens
-        self._cache_shape = None if self.page_size else cache_shape(dtype, self.Hkv, self.d, self.seqlens)
+        self._t16, self._kv = _TORCH_DTYPE[dtype], _KV_DTYPE[dtype]
+        self._q_shape = (self.tokens, self.Hq, self.d)
+        self._k_shape = (self.tokens, self.Hkv, self.d)
+        self._cache_shape = cache_shape(dtype, self.Hkv, self.d, self.seqlens, 0, self.page_size)
 
     def _tensor(self, name, t, shape, dtype):
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape:
+        if t.dtype != dtype or t.device != self.device or t.shape != shape:
             raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected "
-                             f"{dtype} {shape} on {self.device}")
-        return t
+                             f"{dtype} {tuple(shape)} on {self.device}")
 
     def _whole(self, name, t, shape, dtype):
-        if not self._tensor(name, t, shape, dtype).is_contiguous():
+        """Address of a contiguous tensor."""
+        self._tensor(name, t, shape, dtype)
+        if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
-    def _input(self, name, t, heads):
-        self._tensor(name, t, (self.tokens, heads, self.d), _TORCH_DTYPE[self.dtype])
+    def _input(self, name, t, shape):
+        """Address and strides of q, k or v (0 for a dimension of size 1: it is never stepped along)."""
+        self._tensor(name, t, shape, self._t16)
         a, b, c = t.stride()
-        if c != 1 and t.numel() > 0:
+        if c != 1 and self.tokens > 0:
             raise ValueError(f"the elements of a head of {name} must be contiguous")
-        # A dimension of size 1 is never stepped along, whatever stride it reports.
-        return t.data_ptr(), (a if self.tokens > 1 else 0, b if heads > 1 else 0)
+        return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
 
     def _caches(self, k_cache, v_cache, block_table):
-        num_pages, stride, table = 0, 0, None
-        shape = self._cache_shape
+        """(k, v, num_pages, block table, its stride)."""
+        num_pages, stride, table, shape = 0, 0, 0, self._cache_shape
         if self.page_size:
             if block_table is None:
                 raise ValueError("a paged cache needs its block_table")
             num_pages = k_cache.shape[0]
-            shape = cache_shape(self.dtype, self.Hkv, self.d, None, num_pages, self.page_size)
-            stride = block_table.shape[1] if block_table.dim() == 2 else -1
+            shape = (num_pages, *shape[1:])
+            stride = block_table.shape[-1] if block_table.dim() == 2 else -1
             table = self._whole("block_table", block_table, (self.Bsz, stride), torch.int32)
         elif block_table is not None:
             raise ValueError("these rows are of a contiguous cache")
-        kv = _KV_DTYPE[self.dtype]
-        return (self._whole("k_cache", k_cache, shape, kv), self._whole("v_cache", v_cache, shape, kv),
+        return (self._whole("k_cache", k_cache, shape, self._kv), self._whole("v_cache", v_cache, shape, self._kv),
                 num_pages, table, stride)
 
     def _status(self, status):
-        return None if status is None else self._whole("status", status, (1,), torch.int32)
+        return 0 if status is None else self._whole("status", status, (1,), torch.int32)
 
     def append(self, q=None, k=None, v=None, k_cache=None, v_cache=None, *, q_norm=None, k_norm=None,
                q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, rope=None, positions=None,
@@ -115,66 +119,67 @@ class KVRows:
         positions: int32 [T], or [axes, T]; default: each token's row.  q_out and k_out
         [T, heads, d] contiguous (or q and k themselves); q_out is allocated if missing.
         """
-        a = B.AppendArgs()
-        t16 = _TORCH_DTYPE[self.dtype]
+        q_in = k_in = v_in = (0, 0, 0)
+        q_to = k_to = q_w = k_w = rope_ptr = pos = pos_stride = 0
+        cache = (0, 0, 0, 0, 0)
         if q is not None:
-            a.q, a.q_stride[:] = self._input("q", q, self.Hq)
+            q_in = self._input("q", q, self._q_shape)
             if q_out is None:
-                q_out = torch.empty((self.tokens, self.Hq, self.d), dtype=t16, device=self.device)
-            a.q_out = self._whole("q_out", q_out, (self.tokens, self.Hq, self.d), t16)
+                q_out = torch.empty(self._q_shape, dtype=self._t16, device=self.device)
+            q_to = self._whole("q_out", q_out, self._q_shape, self._t16)
         elif q_out is not None:
             raise ValueError("q_out without q")
         if k is not None:
-            a.k, a.k_stride[:] = self._input("k", k, self.Hkv)
+            k_in = self._input("k", k, self._k_shape)
         if v is not None:
-            a.v, a.v_stride[:] = self._input("v", v, self.Hkv)
+            v_in = self._input("v", v, self._k_shape)
         if k_out is not None:
-            a.k_out = self._whole("k_out", k_out, (self.tokens, self.Hkv, self.d), t16)
+            k_to = self._whole("k_out", k_out, self._k_shape, self._t16)
         if (k_cache is None) != (v_cache is None):
             raise ValueError("k_cache and v_cache come together")
         if k_cache is not None:
-            a.k_cache, a.v_cache, a.num_pages, a.block_table, a.bt_stride = \
-                self._caches(k_cache, v_cache, block_table)
-        for name, w, heads in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
-            if w is not None:
-                if heads is None:
-                    raise ValueError(f"{name} without its input")
-                setattr(a, name, self._whole(name, w, (self.d,), t16))
-        a.q_norm = int(q_weight is not None if q_norm is None else q_norm)
-        a.k_norm = int(k_weight is not None if k_norm is None else k_norm)
-        a.eps, a.weight_offset = eps, weight_offset
-        a.k_mul, a.v_mul = k_mul, v_mul
+            cache = self._caches(k_cache, v_cache, block_table)
+        if q_weight is not None:
+            if q is None:
+                raise ValueError("q_weight without q")
+            q_w = self._whole("q_weight", q_weight, (self.d,), self._t16)
+        if k_weight is not None:
+            if k is None:
+                raise ValueError("k_weight without k")
+            k_w = self._whole("k_weight", k_weight, (self.d,), self._t16)
         if rope is not None:
-            a.rope = ctypes.addressof(rope.args)
+            rope_ptr = rope.address
             if positions is not None:
-                if positions.dim() == 1 and rope.num_axes == 1:
-                    shape, a.pos_stride = (self.tokens,), self.tokens
-                else:
-                    shape, a.pos_stride = (rope.num_axes, self.tokens), self.tokens
-                a.positions = self._whole("positions", positions, shape, torch.int32)
+                shape = (self.tokens,) if positions.dim() == 1 and rope.num_axes == 1 else (rope.num_axes, self.tokens)
+                pos, pos_stride = self._whole("positions", positions, shape, torch.int32), self.tokens
         elif positions is not None:
             raise ValueError("positions without rope")
-        a.status = self._status(status)
+        args = B.APPEND_ARGS.pack(
+            q_in[0], k_in[0], v_in[0], q_in[1], q_in[2], k_in[1], k_in[2], v_in[1], v_in[2],
+            q_w != 0 if q_norm is None else bool(q_norm), k_w != 0 if k_norm is None else bool(k_norm),
+            q_w, k_w, eps, weight_offset, rope_ptr, pos, pos_stride, q_to, k_to, cache[0], cache[1],
+            k_mul, v_mul, cache[2], cache[4], cache[3], self._status(status))
         if self.tokens:  # no rows: empty tensors have null addresses
-            self._on_device(B.fd_append, self.rows, a, stream)
+            index = self.device.index
+            rc = B.on_device(index, B.lib().fd_append, self.rows.handle, args, B.stream_on(index, stream))
+            if rc != B.FD_OK:
+                raise B.FdError(rc, "fd_append")
         return q_out
 
     def gather(self, k_cache, v_cache, *, block_table=None, k_out=None, v_out=None, status=None,
                stream=None):
         """The rows of K and V back in 16 bits: (k, v), each [T, Hkv, d]."""
-        k_ptr, v_ptr, num_pages, table, stride = self._caches(k_cache, v_cache, block_table)
-        shape, t16 = (self.tokens, self.Hkv, self.d), _TORCH_DTYPE[self.dtype]
-        k_out = torch.empty(shape, dtype=t16, device=self.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=t16, device=self.device) if v_out is None else v_out
-        k_to, v_to = self._whole("k_out", k_out, shape, t16), self._whole("v_out", v_out, shape, t16)
+        cache = self._caches(k_cache, v_cache, block_table)
+        if k_out is None:
+            k_out = torch.empty(self._k_shape, dtype=self._t16, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(self._k_shape, dtype=self._t16, device=self.device)
+        k_to = self._whole("k_out", k_out, self._k_shape, self._t16)
+        v_to = self._whole("v_out", v_out, self._k_shape, self._t16)
         if self.tokens:
-            self._on_device(B.fd_gather, self.rows, k_ptr, v_ptr, num_pages, table, stride, k_to, v_to,
-                            self._status(status), stream)
+            index = self.device.index
+            rc = B.on_device(index, B.lib().fd_gather, self.rows.handle, *cache, k_to, v_to, self._status(status),
+                             B.stream_on(index, stream))
+            if rc != B.FD_OK:
+                raise B.FdError(rc, "fd_gather")
         return k_out, v_out
-
-    def _on_device(self, call, *args):
-        if torch.cuda.current_device() == self.device.index:
-            call(*args)
-        else:
-            with torch.cuda.device(self.device):
-                call(*args)
