@@ -1,9 +1,7 @@
 // Cache rows: fd_append (norm, rotation and store of new tokens) and fd_gather (rows of a
 // cache back in 16 bits).  See fd.h for the contract.
 //
-// Both are bound by the bytes they move.  A head row of d elements is handled by d / 8
-// lanes with 8 elements each, so that a rotation pair never leaves its lane: a lane's two
-// runs of 4 elements are the two halves of its pairs.
+// Both are bound by the bytes they move.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -90,46 +88,52 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// Four values rounded to E4M3 (saturating) or E2M1, first value in the low bits.
-__device__ __forceinline__ uint32_t to_e4m3x4(const float (&x)[4]) {
+// Eight values rounded to E4M3 or E2M1 (saturating), first value in the low bits.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
   uint32_t r;
   asm("{\n\t.reg .b16 a, b;\n\t"
       "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
       "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
       "mov.b32 %0, {a, b};\n\t}"
       : "=r"(r)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+      : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
-__device__ __forceinline__ uint32_t to_e2m1x4(const float (&x)[4]) {
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8]) {
+  return make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
+}
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 a, b, z;\n\t"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "mov.b32 %0, {a, b, a, b};\n\t}"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
-  return r & 0xffffu;
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
 }
 
-// The E4M3 scale of a block of 16 elements, 4 of them in each of four neighbouring lanes,
-// and the codes of this lane's 4.  The quotient is a true division: with the product by a
-// reciprocal, values half-way between two codes (common: 16-bit values over a scale of 4
-// significant bits) would not always round to even.
-__device__ __forceinline__ void quantise(const float (&y)[4], uint32_t& scale, uint32_t& codes) {
-  float m = max_nan(max_nan(fabsf(y[0]), fabsf(y[1])), max_nan(fabsf(y[2]), fabsf(y[3])));
+// The E4M3 scale of a block of 16 elements, 8 of them in each of two neighbouring lanes, and the
+// codes of this lane's 8.  The quotient is a true division: with the product by a reciprocal,
+// values half-way between two codes (common: 16-bit values over a scale of 4 significant bits)
+// would not always round to even.
+__device__ __forceinline__ void quantise(const float (&y)[8], uint32_t& scale, uint32_t& codes) {
+  float m = fabsf(y[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
   m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const float want[4] = {m / 6.f, 0.f, 0.f, 0.f};
-  scale = to_e4m3x4(want) & 0xffu;
+  scale = to_e4m3x4(m / 6.f, 0.f, 0.f, 0.f) & 0xffu;
   const float s = dev::Elem<__half>::to_f2(dev::e4m3x2_to_f16x2(scale)).x;
   const bool any = s > 0.f;  // false for a NaN scale too: the codes do not matter then
-  const float z[4] = {any ? y[0] / s : 0.f, any ? y[1] / s : 0.f, any ? y[2] / s : 0.f,
-                      any ? y[3] / s : 0.f};
-  codes = to_e2m1x4(z);
+  float z[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = any ? y[i] / s : 0.f;
+  codes = to_e2m1x8(z);
 }
 
-// Byte offset in a 4-bit V block of element e (a multiple of 4) of row r.
+// Byte offset in a 4-bit V block of element e (a multiple of 8) of row r.
 template <int D>
 __device__ __forceinline__ int v_offset(int r, int e) {
   const int g = e / (D / 8), swap = ((D == 128 ? g : g >> 1) & 1) << 2;
@@ -137,24 +141,24 @@ __device__ __forceinline__ int v_offset(int r, int e) {
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack4(const uint2& raw, float (&f)[4]) {
-  const float2 a = dev::Elem<T>::to_f2(raw.x), b = dev::Elem<T>::to_f2(raw.y);
-  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
-}
-template <typename T>
-__device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
-  return make_uint2(dev::pack2<T>(f[0], f[1]), dev::pack2<T>(f[2], f[3]));
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(dev::pack2<T>(f[0], f[1]), dev::pack2<T>(f[2], f[3]), dev::pack2<T>(f[4], f[5]),
+                    dev::pack2<T>(f[6], f[7]));
 }
 
-// One warp: one token, rows_per_warp of its Hq + 2 Hkv head rows (q, then k, then v), 256 / D
-// of them at a time.  The angles depend on the token alone: a lane computes the four of its
-// pairs once and uses them for all its rows.  Position x frequency is a 64-bit product of
-// turns that wraps where whole turns drop out, so no position is too far.
+// A head row of D elements takes D / 16 lanes.  A lane has two runs of 8 elements: the two halves
+// of its rotation pairs (below rot), or plain runs (above), so that a pair never leaves its lane
+// and every load and store is 16 bytes wide.  One warp: one token, rows_per_warp of its Hq + 2 Hkv
+// head rows (q, then k, then v), 512 / D of them at a time.  The angles depend on the token alone:
+// each lane computes 8 / (512 / D) of the eight it needs, the lanes of the warp's other rows the
+// rest.  Position x frequency is a 64-bit product of turns that wraps where whole turns drop out,
+// so no position is too far.
 template <typename T, int D, int KV>
 __global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int LPH = D / 8;        // lanes per head row
+  constexpr int LPH = D / 16;       // lanes per head row
   constexpr int HPW = 32 / LPH;     // head rows a warp handles at a time
   constexpr int U = 2;              // of which it loads ahead
+  constexpr int OWN = 8 / HPW;      // angles a lane computes
   dev::pdl_launch_dependents();
   dev::pdl_wait();
   const int64_t wid = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
@@ -169,23 +173,32 @@ __global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_co
   const int Hv = p.v != nullptr ? p.m.Hkv : 0;
   const int lo = split * p.rows_per_warp, hi = min(lo + p.rows_per_warp, Hq + Hk + Hv);
 
-  // This lane's runs of 4 elements: the two halves of its pairs below rot, plain runs above.
-  const int half = p.rot >> 1, rl = p.rot >> 3;
+  const int half = p.rot >> 1, rl = p.rot >> 4;
   const bool rotates = l < rl;
-  const int ea = rotates ? 4 * l : p.rot + 4 * (l - rl);
-  const int eb = rotates ? half + 4 * l : ((p.rot + D) >> 1) + 4 * (l - rl);
-  float c[4], s[4];
+  const int ea = rotates ? 8 * l : p.rot + 8 * (l - rl);
+  const int eb = rotates ? half + 8 * l : ((p.rot + D) >> 1) + 8 * (l - rl);
+  // Pair i of a lane: (ea + i, eb + i), or, interleaved, neighbours of run a (i < 4) or run b.
+  float c[8], s[8];
+  if (p.rot > 0 && lo < Hq + Hk) {
+    float co[OWN], so[OWN];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) { c[i] = 1.f; s[i] = 0.f; }
-  if (rotates && lo < Hq + Hk) {
+    for (int k = 0; k < OWN; ++k) {
+      const int i = sub * OWN + k;
+      co[k] = 1.f;
+      so[k] = 0.f;
+      if (rotates) {
+        const int pair = p.interleaved ? (i < 4 ? 4 * l : (half >> 1) + 4 * l - 4) + i : 8 * l + i;
+        const int pos = p.positions != nullptr ? p.positions[p.axis[pair] * p.pos_stride + t] : r;
+        const uint64_t turns = (uint64_t)(int64_t)pos * p.freq[pair];
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &so[k], &co[k]);
+        co[k] *= p.rope_scale;
+        so[k] *= p.rope_scale;
+      }
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int pair = p.interleaved ? (i < 2 ? 2 * l : (half >> 1) + 2 * l - 2) + i : 4 * l + i;
-      const int pos = p.positions != nullptr ? p.positions[p.axis[pair] * p.pos_stride + t] : r;
-      const uint64_t turns = (uint64_t)(int64_t)pos * p.freq[pair];
-      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s[i], &c[i]);
-      c[i] *= p.rope_scale;
-      s[i] *= p.rope_scale;
+    for (int i = 0; i < 8; ++i) {
+      c[i] = __shfl_sync(0xffffffffu, co[i % OWN], i / OWN * LPH + l);
+      s[i] = __shfl_sync(0xffffffffu, so[i % OWN], i / OWN * LPH + l);
     }
   }
 
@@ -193,56 +206,62 @@ __global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_co
   auto rows = [&](int kind, int first, int last, const void* in, const int64_t* stride,
                   const void* weight, int norm, void* out, int H, void* cache, float mul) {
     if (first >= last) return;
-    float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
-    if (norm && weight != nullptr) {
-      unpack4<T>(*reinterpret_cast<const uint2*>(reinterpret_cast<const T*>(weight) + ea), wa);
-      unpack4<T>(*reinterpret_cast<const uint2*>(reinterpret_cast<const T*>(weight) + eb), wb);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { wa[i] += p.weight_offset; wb[i] += p.weight_offset; }
-    }
     const T* src = reinterpret_cast<const T*>(in) + (int64_t)t * stride[0];
+    const uint4* wa = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + ea);
+    const uint4* wb = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + eb);
+#pragma unroll 1
     for (int h0 = first; h0 < last; h0 += U * HPW) {
-      uint2 ra[U], rb[U];
+      uint4 ra[U], rb[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = min(h0 + u * HPW + sub, last - 1);  // rows past the end repeat the last one
-        ra[u] = *reinterpret_cast<const uint2*>(src + (int64_t)h * stride[1] + ea);
-        rb[u] = *reinterpret_cast<const uint2*>(src + (int64_t)h * stride[1] + eb);
+        ra[u] = *reinterpret_cast<const uint4*>(src + (int64_t)h * stride[1] + ea);
+        rb[u] = *reinterpret_cast<const uint4*>(src + (int64_t)h * stride[1] + eb);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (u > 0 && h0 + u * HPW >= last) break;
         const int h = h0 + u * HPW + sub;
         const bool there = h < last;
-        float a[4], x[4];
-        unpack4<T>(ra[u], a);
-        unpack4<T>(rb[u], x);
-        if (norm) {
+        float a[8], x[8];
+        dev::unpack8<T>(ra[u], a);
+        dev::unpack8<T>(rb[u], x);
+        if (kind < 2 && norm) {
           float ss = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) ss = fmaf(a[i], a[i], fmaf(x[i], x[i], ss));
+          for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(x[i], x[i], ss));
 #pragma unroll
           for (int off = 1; off < LPH; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
           const float n = rsqrtf(ss * (1.f / D) + p.eps);
+          if (weight != nullptr) {
+            float w[8];
+            dev::unpack8<T>(*wa, w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a[i] = a[i] * n * wa[i];
-            x[i] = x[i] * n * wb[i];
+            for (int i = 0; i < 8; ++i) a[i] = a[i] * n * (w[i] + p.weight_offset);
+            dev::unpack8<T>(*wb, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * n * (w[i] + p.weight_offset);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              a[i] *= n;
+              x[i] *= n;
+            }
           }
         }
         if (kind < 2 && rotates) {
           if (p.interleaved) {
-            const float a0 = a[0], a2 = a[2], x0 = x[0], x2 = x[2];
-            a[0] = a0 * c[0] - a[1] * s[0];
-            a[1] = a0 * s[0] + a[1] * c[0];
-            a[2] = a2 * c[1] - a[3] * s[1];
-            a[3] = a2 * s[1] + a[3] * c[1];
-            x[0] = x0 * c[2] - x[1] * s[2];
-            x[1] = x0 * s[2] + x[1] * c[2];
-            x[2] = x2 * c[3] - x[3] * s[3];
-            x[3] = x2 * s[3] + x[3] * c[3];
-          } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+              const float a0 = a[2 * i], x0 = x[2 * i];
+              a[2 * i] = a0 * c[i] - a[2 * i + 1] * s[i];
+              a[2 * i + 1] = a0 * s[i] + a[2 * i + 1] * c[i];
+              x[2 * i] = x0 * c[4 + i] - x[2 * i + 1] * s[4 + i];
+              x[2 * i + 1] = x0 * s[4 + i] + x[2 * i + 1] * c[4 + i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
               const float a0 = a[i];
               a[i] = a0 * c[i] - x[i] * s[i];
               x[i] = a0 * s[i] + x[i] * c[i];
@@ -251,39 +270,37 @@ __global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_co
         }
         if (out != nullptr && there) {
           T* dst = reinterpret_cast<T*>(out) + ((int64_t)t * H + h) * D;
-          *reinterpret_cast<uint2*>(dst + ea) = pack4<T>(a);
-          *reinterpret_cast<uint2*>(dst + eb) = pack4<T>(x);
+          *reinterpret_cast<uint4*>(dst + ea) = pack8<T>(a);
+          *reinterpret_cast<uint4*>(dst + eb) = pack8<T>(x);
         }
         if (kind == 0 || cache == nullptr) continue;
         const bool store = there && row >= 0;
         if constexpr (KV == kKv16) {
           if (store) {
             T* dst = reinterpret_cast<T*>(cache) + (row * H + h) * D;
-            *reinterpret_cast<uint2*>(dst + ea) = pack4<T>(a);
-            *reinterpret_cast<uint2*>(dst + eb) = pack4<T>(x);
+            *reinterpret_cast<uint4*>(dst + ea) = pack8<T>(a);
+            *reinterpret_cast<uint4*>(dst + eb) = pack8<T>(x);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) { a[i] *= mul; x[i] *= mul; }
+          for (int i = 0; i < 8; ++i) { a[i] *= mul; x[i] *= mul; }
           if constexpr (KV == kKvE4m3) {
             if (store) {
               uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + (row * H + h) * D;
-              *reinterpret_cast<uint32_t*>(dst + ea) = to_e4m3x4(a);
-              *reinterpret_cast<uint32_t*>(dst + eb) = to_e4m3x4(x);
+              *reinterpret_cast<uint2*>(dst + ea) = to_e4m3x8(a);
+              *reinterpret_cast<uint2*>(dst + eb) = to_e4m3x8(x);
             }
           } else {
-            // Runs of four neighbouring lanes are whole blocks of 16 (rot is a multiple of 32).
+            // The runs of two neighbouring lanes are whole blocks of 16 (rot is a multiple of 32).
             uint32_t sa, sb, ca, cb;
             quantise(a, sa, ca);
             quantise(x, sb, cb);
             if (store) {
               uint8_t* blk = reinterpret_cast<uint8_t*>(cache) + ((row >> kBlockShift) * H + h) * (9 * D);
               const int r16 = (int)(row & (kBlockTokens - 1));
-              const int oa = kind == 1 ? r16 * (D / 2) + ea / 2 : v_offset<D>(r16, ea);
-              const int ob = kind == 1 ? r16 * (D / 2) + eb / 2 : v_offset<D>(r16, eb);
-              *reinterpret_cast<uint16_t*>(blk + oa) = (uint16_t)ca;
-              *reinterpret_cast<uint16_t*>(blk + ob) = (uint16_t)cb;
-              if ((l & 3) == 0) {
+              *reinterpret_cast<uint32_t*>(blk + (kind == 1 ? r16 * (D / 2) + ea / 2 : v_offset<D>(r16, ea))) = ca;
+              *reinterpret_cast<uint32_t*>(blk + (kind == 1 ? r16 * (D / 2) + eb / 2 : v_offset<D>(r16, eb))) = cb;
+              if ((l & 1) == 0) {
                 const int ja = ea / 16, jb = eb / 16;
                 blk[8 * D + (kind == 1 ? r16 * (D / 16) + ja : 16 * ja + r16)] = (uint8_t)sa;
                 blk[8 * D + (kind == 1 ? r16 * (D / 16) + jb : 16 * jb + r16)] = (uint8_t)sb;
@@ -301,11 +318,11 @@ __global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_co
        p.v_cache, p.v_mul);
 }
 
-// One warp: 16 tokens of one KV head, K (even warps of the grid) or V.  Lanes as above; a
-// lane's 8 elements are neighbours.
+// One warp: 16 tokens of one KV head, K (even warps of the grid) or V.  A row takes D / 16 lanes,
+// a lane the 8 elements at 8 l and those at D / 2 + 8 l.
 template <typename T, int D, int KV>
 __global__ void __launch_bounds__(kRowsThreads) fd_gather_kernel(const __grid_constant__ GatherParams p) {
-  constexpr int LPH = D / 8, HPW = 32 / LPH, TOK = 16;
+  constexpr int LPH = D / 16, HPW = 32 / LPH, TOK = 16;
   dev::pdl_launch_dependents();
   dev::pdl_wait();
   const int64_t wid = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
@@ -322,42 +339,48 @@ __global__ void __launch_bounds__(kRowsThreads) fd_gather_kernel(const __grid_co
     my_row = cache_row(p.m, b, p.m.begin[b] + (t - p.m.cu[b]));
   }
   const uint8_t* cache = reinterpret_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
-  T* out = reinterpret_cast<T*>(is_v ? p.v_out : p.k_out);
+  T* out = reinterpret_cast<T*>(is_v ? p.v_out : p.k_out) + (t0 * H + h) * D + 8 * l;
+  const int n = (int)min((int64_t)TOK, p.T - t0);
 #pragma unroll
   for (int i = 0; i < TOK / HPW; ++i) {
     const int tok = i * HPW + sub;
     const int64_t row = __shfl_sync(0xffffffffu, my_row, tok);
-    const int64_t t = t0 + tok;
-    if (t >= p.T) continue;
-    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+    if (tok >= n) continue;
+    uint4 y[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
     if (row >= 0) {
-      if constexpr (KV == kKv16) {
-        y = *reinterpret_cast<const uint4*>(cache + ((row * H + h) * D + 8 * l) * 2);
-      } else if constexpr (KV == kKvE4m3) {
-        const uint2 x = *reinterpret_cast<const uint2*>(cache + (row * H + h) * D + 8 * l);
-        dev::e4m3x4_to_f16x4(x.x, y.x, y.y);
-        dev::e4m3x4_to_f16x4(x.y, y.z, y.w);
-      } else {
-        const uint8_t* blk = cache + ((row >> kBlockShift) * H + h) * (9 * D);
-        const int r16 = (int)(row & (kBlockTokens - 1));
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(
-            blk + (is_v ? v_offset<D>(r16, 8 * l) : r16 * (D / 2) + 4 * l));
-        const uint32_t z = dev::e4m3x2_to_f16x2(blk[8 * D + (is_v ? 16 * (l >> 1) + r16 : r16 * (D / 16) + (l >> 1))]);
-        const uint32_t s2 = __byte_perm(z, z, 0x1010);
-        uint32_t f[4];
-        dev::e2m1x8_to_f16x8(x, f);
+      const uint8_t* blk = cache + (KV == kKv16     ? (row * H + h) * (2 * D)
+                                    : KV == kKvE4m3 ? (row * H + h) * D
+                                                    : ((row >> kBlockShift) * H + h) * (9 * D));
+      const int r16 = (int)row & (kBlockTokens - 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[j] = dev::hmul2(f[j], s2);
-          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-            const float2 v = dev::Elem<__half>::to_f2(f[j]);
-            f[j] = dev::pack2<T>(v.x, v.y);
+      for (int k = 0; k < 2; ++k) {
+        const int e = k * (D / 2) + 8 * l;
+        if constexpr (KV == kKv16) {
+          y[k] = *reinterpret_cast<const uint4*>(blk + 2 * e);
+        } else if constexpr (KV == kKvE4m3) {
+          const uint2 x = *reinterpret_cast<const uint2*>(blk + e);
+          dev::e4m3x4_to_f16x4(x.x, y[k].x, y[k].y);
+          dev::e4m3x4_to_f16x4(x.y, y[k].z, y[k].w);
+        } else {
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(blk + (is_v ? v_offset<D>(r16, e) : r16 * (D / 2) + e / 2));
+          const uint32_t z = dev::e4m3x2_to_f16x2(blk[8 * D + (is_v ? 16 * (e / 16) + r16 : r16 * (D / 16) + e / 16)]);
+          const uint32_t s2 = __byte_perm(z, z, 0x1010);
+          uint32_t f[4];
+          dev::e2m1x8_to_f16x8(x, f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[j] = dev::hmul2(f[j], s2);
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+              const float2 v = dev::Elem<__half>::to_f2(f[j]);
+              f[j] = dev::pack2<T>(v.x, v.y);
+            }
           }
+          y[k] = make_uint4(f[0], f[1], f[2], f[3]);
         }
-        y = make_uint4(f[0], f[1], f[2], f[3]);
       }
     }
-    *reinterpret_cast<uint4*>(out + (t * H + h) * D + 8 * l) = y;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(out + (int64_t)tok * H * D + k * (D / 2)) = y[k];
   }
 }
 
@@ -614,11 +637,10 @@ int fd_append(fd_rows_t rows, const fd_append_args* a, cudaStream_t stream) {
   p.k_mul = a->k_mul; p.v_mul = a->v_mul;
   p.q_norm = a->q_norm != 0; p.k_norm = a->k_norm != 0;
   p.Hq = r->Hq;
-  // Head rows per warp: one load round (4 rows at d = 128) while tokens are few, so that a
-  // decode step fills the device; more as they grow, so that the angles of a token are
-  // computed less often.
+  // Head rows per warp: one round (4 rows at d = 128) while tokens are few, so that a decode step
+  // fills the device; more as they grow, so that the angles of a token are computed less often.
   const int rows_all = (a->q ? r->Hq : 0) + (a->k ? r->Hkv : 0) + (a->v ? r->Hkv : 0);
-  const int round = 2 * (256 / d);
+  const int round = 512 / d;
   int64_t per = (T * rows_all + fd::kAppendWarps - 1) / fd::kAppendWarps;
   per = (per + round - 1) / round * round;
   if (per > rows_all) per = rows_all;

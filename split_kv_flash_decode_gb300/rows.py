@@ -70,23 +70,22 @@ class KVRows:
         self._k_shape = (self.tokens, self.Hkv, self.d)
         self._cache_shape = cache_shape(dtype, self.Hkv, self.d, self.seqlens, 0, self.page_size)
 
-    def _tensor(self, name, t, shape, dtype):
-        if t.dtype != dtype or t.device != self.device or t.shape != shape:
-            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected "
-                             f"{dtype} {tuple(shape)} on {self.device}")
+    def _refuse(self, name, t, shape, dtype):
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}, expected "
+                         f"a contiguous {dtype} {tuple(shape)} on {self.device}")
 
     def _whole(self, name, t, shape, dtype):
         """Address of a contiguous tensor."""
-        self._tensor(name, t, shape, dtype)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            self._refuse(name, t, shape, dtype)
         return t.data_ptr()
 
     def _input(self, name, t, shape):
         """Address and strides of q, k or v (0 for a dimension of size 1: it is never stepped along)."""
-        self._tensor(name, t, shape, self._t16)
+        if t.dtype != self._t16 or t.shape != shape or t.device != self.device:
+            self._refuse(name, t, shape, self._t16)
         a, b, c = t.stride()
-        if c != 1 and self.tokens > 0:
+        if c != 1 and shape[0] > 0:
             raise ValueError(f"the elements of a head of {name} must be contiguous")
         return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
 
