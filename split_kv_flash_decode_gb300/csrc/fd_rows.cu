@@ -25,8 +25,14 @@ constexpr int kRowsThreads = 128;
 constexpr int kMaxAxes = 4;
 constexpr int kMaxPairs = 64;
 constexpr double kMaxFreq = 1 << 20;
-// Warps that an append is split into while it has enough head rows: 32 on each of 152 SMs.
-constexpr int64_t kAppendWarps = 32 * 152;
+// Warps that an append is split into while it has enough head rows: 16 on each of 152 SMs.  (2090
+// tokens of 40 head rows: 11.9 us with 16, 13.1 with 32, 14.0 with 64: a token's angles are computed
+// once per warp.)
+constexpr int64_t kAppendWarps = 16 * 152;
+
+// Tokens of one gather warp: two rounds of its lanes.  (32K tokens of a 4-bit cache, 172 MB: 27.2 us;
+// with one round 34.0, three 27.6, four 28.5 us.)
+FD_HD constexpr int gather_tokens(int d) { return 2 * (512 / d); }
 
 enum KvKind { kKv16 = 0, kKvE4m3 = 1, kKvE2m1 = 2 };
 
@@ -153,11 +159,14 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // each lane computes 8 / (512 / D) of the eight it needs, the lanes of the warp's other rows the
 // rest.  Position x frequency is a 64-bit product of turns that wraps where whole turns drop out,
 // so no position is too far.
+//
+// Bound by HBM: 805 MB (32K tokens of 48 head rows) in 125 us, 6.4 TB/s.  It takes many warps to
+// keep enough loads in flight: with the registers of 5 blocks per SM (92) the same took 145 us, of
+// 8 (64) 125 us; 4-bit caches, whose quantisation needs the registers, are faster with 4.
 template <typename T, int D, int KV>
-__global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kRowsThreads, KV == kKvE2m1 ? 4 : 8) fd_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPH = D / 16;       // lanes per head row
   constexpr int HPW = 32 / LPH;     // head rows a warp handles at a time
-  constexpr int U = 2;              // of which it loads ahead
   constexpr int OWN = 8 / HPW;      // angles a lane computes
   dev::pdl_launch_dependents();
   dev::pdl_wait();
@@ -177,6 +186,21 @@ __global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_co
   const bool rotates = l < rl;
   const int ea = rotates ? 8 * l : p.rot + 8 * (l - rl);
   const int eb = rotates ? half + 8 * l : ((p.rot + D) >> 1) + 8 * (l - rl);
+  // The warp's first rows, on their way while the angles are computed.
+  const int first_kind = lo < Hq ? 0 : lo < Hq + Hk ? 1 : 2;
+  uint4 na, nb;
+  auto load = [&](const T* src, int64_t stride, int h, int last) {
+    const T* at = src + (int64_t)min(h + sub, last - 1) * stride;  // rows past the end repeat the last one
+    na = *reinterpret_cast<const uint4*>(at + ea);
+    nb = *reinterpret_cast<const uint4*>(at + eb);
+  };
+  {
+    const int64_t* stride = first_kind == 0 ? p.q_stride : first_kind == 1 ? p.k_stride : p.v_stride;
+    const void* in = first_kind == 0 ? p.q : first_kind == 1 ? p.k : p.v;
+    const int before = first_kind == 0 ? 0 : first_kind == 1 ? Hq : Hq + Hk;
+    load(reinterpret_cast<const T*>(in) + (int64_t)t * stride[0], stride[1], lo - before,
+         min(hi - before, first_kind == 0 ? Hq : p.m.Hkv));
+  }
   // Pair i of a lane: (ea + i, eb + i), or, interleaved, neighbours of run a (i < 4) or run b.
   float c[8], s[8];
   if (p.rot > 0 && lo < Hq + Hk) {
@@ -209,23 +233,16 @@ __global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_co
     const T* src = reinterpret_cast<const T*>(in) + (int64_t)t * stride[0];
     const uint4* wa = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + ea);
     const uint4* wb = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + eb);
+    if (kind != first_kind) load(src, stride[1], first, last);
 #pragma unroll 1
-    for (int h0 = first; h0 < last; h0 += U * HPW) {
-      uint4 ra[U], rb[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = min(h0 + u * HPW + sub, last - 1);  // rows past the end repeat the last one
-        ra[u] = *reinterpret_cast<const uint4*>(src + (int64_t)h * stride[1] + ea);
-        rb[u] = *reinterpret_cast<const uint4*>(src + (int64_t)h * stride[1] + eb);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u > 0 && h0 + u * HPW >= last) break;
-        const int h = h0 + u * HPW + sub;
+    for (int h0 = first; h0 < last; h0 += HPW) {
+      {
+        const int h = h0 + sub;
         const bool there = h < last;
         float a[8], x[8];
-        dev::unpack8<T>(ra[u], a);
-        dev::unpack8<T>(rb[u], x);
+        dev::unpack8<T>(na, a);
+        dev::unpack8<T>(nb, x);
+        if (h0 + HPW < last) load(src, stride[1], h0 + HPW, last);
         if (kind < 2 && norm) {
           float ss = 0.f;
 #pragma unroll
@@ -318,11 +335,13 @@ __global__ void __launch_bounds__(kRowsThreads) fd_append_kernel(const __grid_co
        p.v_cache, p.v_mul);
 }
 
-// One warp: 16 tokens of one KV head, K (even warps of the grid) or V.  A row takes D / 16 lanes,
-// a lane the 8 elements at 8 l and those at D / 2 + 8 l.
+// One warp: gather_tokens(D) tokens of one KV head, K (even warps of the grid) or V.  A row takes
+// D / 16 lanes, a lane the 8 elements at 8 l and those at D / 2 + 8 l.  Bound by HBM: 172 MB at 6.3
+// TB/s (32K tokens from 4 bits), 35 MB in 5.7 us (from E4M3).  Many small warps: each finds its rows
+// (a chain of a binary search and a page-table load) while others load.
 template <typename T, int D, int KV>
 __global__ void __launch_bounds__(kRowsThreads) fd_gather_kernel(const __grid_constant__ GatherParams p) {
-  constexpr int LPH = D / 16, HPW = 32 / LPH, TOK = 16;
+  constexpr int LPH = D / 16, HPW = 32 / LPH, TOK = gather_tokens(D);
   dev::pdl_launch_dependents();
   dev::pdl_wait();
   const int64_t wid = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
@@ -338,9 +357,9 @@ __global__ void __launch_bounds__(kRowsThreads) fd_gather_kernel(const __grid_co
     const int t = (int)(t0 + lane), b = find_sequence(p.m, t);
     my_row = cache_row(p.m, b, p.m.begin[b] + (t - p.m.cu[b]));
   }
+  const int n = (int)min((int64_t)TOK, p.T - t0);
   const uint8_t* cache = reinterpret_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
   T* out = reinterpret_cast<T*>(is_v ? p.v_out : p.k_out) + (t0 * H + h) * D + 8 * l;
-  const int n = (int)min((int64_t)TOK, p.T - t0);
 #pragma unroll
   for (int i = 0; i < TOK / HPW; ++i) {
     const int tok = i * HPW + sub;
@@ -662,7 +681,7 @@ int fd_gather(fd_rows_t rows, const void* k_cache, const void* v_cache, int num_
   p.k_cache = k_cache; p.v_cache = v_cache;
   p.k_out = k_out; p.v_out = v_out;
   p.T = (int32_t)rows->T;
-  const int64_t tiles = (rows->T + 15) / 16;
+  const int64_t tok = fd::gather_tokens(rows->d), tiles = (rows->T + tok - 1) / tok;
   return fd::launch_rows(fd::pick<fd::GatherFn>(rows->dtype, rows->d), tiles * 2 * rows->Hkv, &p, stream);
 }
 
