@@ -2198,10 +2198,10 @@ cudaError_t launch_typed_mma(const Params& p, int d, int G, int path, int mode, 
 }
 
 // The stream kernel over a 4-bit cache (host mode 8).
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool PAGED>
 cudaError_t launch_kv4_stream(const Params& p, bool pdl, int grid, cudaStream_t stream) {
   using S = dev::Kv4Stream<D, G>;
-  const void* fn = reinterpret_cast<const void*>(&dev::fd_kv4_stream_kernel<T, D, G>);
+  const void* fn = reinterpret_cast<const void*>(&dev::fd_kv4_stream_kernel<T, D, G, PAGED>);
   int dev_id = 0;
   cudaError_t err = cudaGetDevice(&dev_id);
   if (err != cudaSuccess) return err;
@@ -2230,10 +2230,11 @@ cudaError_t launch_kv4_stream(const Params& p, bool pdl, int grid, cudaStream_t 
 template <typename T>
 cudaError_t launch_typed_kv4(const Params& p, int d, int G, int mode, bool pdl, int grid,
                              cudaStream_t s) {
-#define FD_CASE(DD, GG)                                                            \
-  if (d == DD && G == GG)                                                          \
-    return mode == kModeStream ? launch_kv4_stream<T, DD, GG>(p, pdl, grid, s)     \
-                               : launch_dgp<T, DD, GG, kPathMmaKv4>(p, mode, pdl, grid, s);
+#define FD_CASE(DD, GG)                                                                      \
+  if (d == DD && G == GG)                                                                    \
+    return mode != kModeStream          ? launch_dgp<T, DD, GG, kPathMmaKv4>(p, mode, pdl, grid, s) \
+           : p.block_table != nullptr ? launch_kv4_stream<T, DD, GG, true>(p, pdl, grid, s)  \
+                                        : launch_kv4_stream<T, DD, GG, false>(p, pdl, grid, s);
   FD_CASE(64, 1) FD_CASE(64, 2) FD_CASE(64, 4) FD_CASE(64, 8) FD_CASE(64, 16)
   FD_CASE(128, 1) FD_CASE(128, 2) FD_CASE(128, 4) FD_CASE(128, 8) FD_CASE(128, 16)
 #undef FD_CASE

@@ -67,6 +67,15 @@ struct Kv4Warp {
       }
     }
   }
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mi = 0; mi < KT; ++mi) o[nt][mi][0] = o[nt][mi][1] = o[nt][mi][2] = o[nt][mi][3] = 0.f;
+      mA[nt] = mB[nt] = -INFINITY;
+      lA[nt] = lB[nt] = lrA[nt] = lrB[nt] = 0.f;
+    }
+  }
   // Makes the fetched q the B operand, and starts from the empty state.
   __device__ __forceinline__ void start(const Params& p) {
     const int t = threadIdx.x & 3;
@@ -95,13 +104,9 @@ struct Kv4Warp {
       }
       scA[nt] = __shfl_sync(0xffffffffu, scale, 8 * t);      // column 2t is lane group g = 2t
       scB[nt] = __shfl_sync(0xffffffffu, scale, 8 * t + 4);
-#pragma unroll
-      for (int mi = 0; mi < KT; ++mi) o[nt][mi][0] = o[nt][mi][1] = o[nt][mi][2] = o[nt][mi][3] = 0.f;
-      mA[nt] = mB[nt] = -INFINITY;
-      lA[nt] = lB[nt] = lrA[nt] = lrB[nt] = 0.f;
     }
+    reset();
   }
-
   __device__ __forceinline__ void load_q(const Params& p, int b, int kvh) {
     fetch_q(p, b, kvh);
     start(p);
@@ -526,9 +531,11 @@ struct StreamPair {
 // What a warp loads next: its 32 tokens of tiles i, i + kQuads, .. of pair sp, `left` more of
 // them, then those of the following pairs; `row` is the next load's TMA row (its first token where
 // the cache is paged).  Every lane holds the same values, so that they can live in uniform registers.
+template <bool PAGED>
 struct StreamCursor {
   StreamPair sp;
   int i, left, row;
+  int page[2];  // paged caches: TMA rows of the next load's 16-token halves, read one load ahead
   // On by n tiles that hold tokens; i >= end when the run has fewer.
   __device__ __forceinline__ void seek(const Params& p, int n, int end) {
     while (i < end) {
@@ -551,21 +558,33 @@ struct StreamCursor {
       const int tiles = min((sp.len - first_token + kStreamTile - 1) / kStreamTile, end - sp.at - kPairUnits);
       if (sp.len > first_token && tile < tiles) {
         const int token = tile * kStreamTile + first_token;
-        row = p.block_table == nullptr ? p.blk[sp.b] + token / kBlockTokens : token;
+        row = PAGED ? token : p.blk[sp.b] + token / kBlockTokens;
         left = (tiles - tile - 1) / quads + 1;
         return;
       }
     }
   }
+  // Page-table entries of the next load; pages past the end of the sequence: its last one.
+  __device__ __forceinline__ void read_pages(const Params& p) {
+    if (!PAGED || left == 0) return;
+    const int32_t* bt = p.block_table + (int64_t)sp.b * p.bt_stride;
+    const int last_pg = (sp.len - 1) >> p.page_shift;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int a = row + k * kBlockTokens, pg = min(a >> p.page_shift, last_pg);
+      page[k] = (__ldg(bt + pg) * (1 << p.page_shift) + (a & ((1 << p.page_shift) - 1))) >> kBlockShift;
+    }
+  }
   // Past one load.
   __device__ __forceinline__ void step(const Params& p, int quads, int first_token, int end) {
-    row += quads * (p.block_table == nullptr ? kStreamTile / kBlockTokens : kStreamTile);
+    row += quads * (PAGED ? kStreamTile : kStreamTile / kBlockTokens);
     i += quads;
     if (--left == 0) {
       i -= quads;
       seek(p, quads, end);
       batch(p, quads, first_token, end);
     }
+    read_pages(p);
   }
 };
 
@@ -580,31 +599,26 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // K and V of one slot (32 tokens of a KV head) to dst.
-template <int D, int G>
-__device__ __forceinline__ void stream_load(const Params& p, const StreamCursor& cur, uint32_t dst, uint32_t bar,
+template <int D, int G, bool PAGED>
+__device__ __forceinline__ void stream_load(const Params& p, const StreamCursor<PAGED>& cur, uint32_t dst, uint32_t bar,
                                             uint64_t policy) {
   using S = Kv4Stream<D, G>;
   const int kvh = cur.sp.kvh, row = cur.row;
   mbar_arrive_expect_tx(bar, S::kSlotBytes);
-  if (p.block_table == nullptr) {
+  if constexpr (!PAGED) {
     tma_load_3d(dst, &p.tm_k, 0, kvh, row, bar, policy);
     tma_load_3d(dst + S::kRowsBytes, &p.tm_v, 0, kvh, row, bar, policy);
     return;
   }
-  // One box per page piece; pieces past the end of the sequence reload its last page.
-  const int32_t* bt = p.block_table + (int64_t)cur.sp.b * p.bt_stride;
-  const int last_pg = (cur.sp.len - 1) >> p.page_shift;
-#pragma unroll 1
-  for (int r = 0; r < S::kSub * 16; r += p.box_rows) {
-    const int a = row + r, pg = min(a >> p.page_shift, last_pg);
-    const int at = __ldg(bt + pg) * (1 << p.page_shift) + (a & ((1 << p.page_shift) - 1));
-    const uint32_t to = dst + r * ring_row_bytes(kPathMmaKv4, D);
-    tma_load_3d(to, &p.tm_k, 0, kvh, at >> kBlockShift, bar, policy);
-    tma_load_3d(to + S::kRowsBytes, &p.tm_v, 0, kvh, at >> kBlockShift, bar, policy);
+  // Pages of 16 tokens: a box for each half of the slot; larger pages hold all of it.
+  for (int k = 0; k * p.box_rows < S::kSub * 16; ++k) {
+    const uint32_t to = dst + k * 16 * ring_row_bytes(kPathMmaKv4, D);
+    tma_load_3d(to, &p.tm_k, 0, kvh, cur.page[k], bar, policy);
+    tma_load_3d(to + S::kRowsBytes, &p.tm_v, 0, kvh, cur.page[k], bar, policy);
   }
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool PAGED>
 __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>::kCtas))
     fd_kv4_stream_kernel(const __grid_constant__ Params p) {
   using S = Kv4Stream<D, G>;
@@ -637,13 +651,13 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
     prefetch_tensormap(&p.tm_v);
   }
   // The warp's loads, one slot after the other.
-  StreamCursor cur;
+  StreamCursor<PAGED> cur;
   cur.sp = sp;
   cur.i = i0;
   cur.seek(p, quad, i1);
   cur.batch(p, S::kQuads, first_token, i1);
   // The first slot into L2 while the previous kernel drains (see fd_split_kernel).
-  if (p.block_table == nullptr && cur.left > 0 && lane == 0) {
+  if (!PAGED && cur.left > 0 && lane == 0) {
     tma_prefetch_l2_3d(&p.tm_k, 0, cur.sp.kvh, cur.row);
     tma_prefetch_l2_3d(&p.tm_v, 0, cur.sp.kvh, cur.row);
   }
@@ -651,13 +665,14 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
   auto load_next = [&](int slot) {
     if (cur.left == 0) return;
     if (elect_one())
-      stream_load<D, G>(p, cur, ring + slot * S::kSlotBytes, bar + 8 * slot, policy);
+      stream_load<D, G, PAGED>(p, cur, ring + slot * S::kSlotBytes, bar + 8 * slot, policy);
     __syncwarp();
     cur.step(p, S::kQuads, first_token, i1);
     ++loads;
   };
   __syncwarp();
   pdl_wait();  // q, K, V, the workspace and out may come from earlier kernels
+  cur.read_pages(p);
   // q ahead of K and V: behind them it would wait for the whole ring (3 us when all CTAs start).
   W w;
   w.fetch_q(p, sp.b, sp.kvh);
@@ -783,12 +798,13 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
     const float* rec1 = p.part + (int64_t)c_first * 2 * S::kRecord;
     const float* rec0 = rec1 + (stream_begin(p, c_first) >= pr.at ? 0 : S::kRecord);
     auto record = [&](int r) { return r == 0 ? rec0 : rec1 + (int64_t)r * 2 * S::kRecord; };
-    // Thread v: fragment v mod kItems of every kSplit-th record, eight at a time; the first eight
+    // Thread v: fragment v mod kItems of every kSplit-th record, sixteen at a time; the first sixteen
     // are on their way while the coefficients are computed.
-    float4 x[8];
+    constexpr int kAhead = 16;
+    float4 x[kAhead];
     auto fetch = [&](int it, int r) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int u = 0; u < kAhead; ++u)
         if (r + u * S::kSplit < nrec) x[u] = __ldcg(reinterpret_cast<const float4*>(record(r + u * S::kSplit)) + it);
     };
     if (tid < S::kItems * S::kSplit) fetch(tid % S::kItems, tid / S::kItems);
@@ -820,10 +836,10 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
       const float *cA = coef + h * nrec, *cB = cA + nrec;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int r = q; r < nrec; r += 8 * S::kSplit) {
+      for (int r = q; r < nrec; r += kAhead * S::kSplit) {
         if (v != tid || r != q) fetch(it, r);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
           if (r + u * S::kSplit < nrec) {
             const float fA = cA[r + u * S::kSplit], fB = cB[r + u * S::kSplit];
             a.x = fmaf(x[u].x, fA, a.x);
@@ -833,18 +849,22 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
           }
         }
       }
-      sums[v] = a;
-    }
-    __syncthreads();
-    for (int v = tid; v < S::kItems; v += S::kThreads) {
-      float4 a = sums[v];
-      if constexpr (S::kSplit == 2) {
-        const float4 y = sums[S::kItems + v];
-        a.x += y.x; a.y += y.y; a.z += y.z; a.w += y.w;
+      if constexpr (S::kSplit == 1) {
+        const float lA = st_lr[h], lB = st_lr[h + 1];
+        W::put_out(out, it >> 5, lane, a, lA != 0.f ? 1.f / lA : 0.f, lB != 0.f ? 1.f / lB : 0.f);
+      } else {
+        sums[v] = a;
       }
-      const int h = W::frag_head(v >> 5, lane);
-      const float lA = st_lr[h], lB = st_lr[h + 1];
-      W::put_out(out, v >> 5, lane, a, lA != 0.f ? 1.f / lA : 0.f, lB != 0.f ? 1.f / lB : 0.f);
+    }
+    if constexpr (S::kSplit == 2) {
+      __syncthreads();
+      for (int v = tid; v < S::kItems; v += S::kThreads) {
+        const float4 a = sums[v], y = sums[S::kItems + v];
+        const int h = W::frag_head(v >> 5, lane);
+        const float lA = st_lr[h], lB = st_lr[h + 1];
+        W::put_out(out, v >> 5, lane, make_float4(a.x + y.x, a.y + y.y, a.z + y.z, a.w + y.w),
+                   lA != 0.f ? 1.f / lA : 0.f, lB != 0.f ? 1.f / lB : 0.f);
+      }
     }
     __syncthreads();  // the next pair overwrites the sums
   }
