@@ -432,12 +432,18 @@ typedef struct fd_append_args {
  *             scale, and so all 16 values, NaN
  *
  * q and q_out come together, v and v_cache, k_cache and v_cache too; k with k_out or k_cache.
- * The pages of a call's rows must differ from each other (two rows that share a place in the
- * pool leave either's bytes there).  A row whose page index lies outside [0, num_pages) is not
+ * Two rows of a call that the block table sends to one place of the pool leave either's values
+ * there, in pieces of 4 bytes or more.  A row whose page index lies outside [0, num_pages) is not
  * stored in the cache (q_out and k_out are).  T = 0 launches nothing.
  *
- * FD_ERR_INVALID: a missing pointer, a negative stride, an output that overlaps an input (but
- * for the in-place case), bt_stride < ceil(L_b / page_size), a bad rope or factor.
+ * Before a cache's first decode: fd_decode over a 16-bit or E4M3 cache also reads the rows behind
+ * a sequence's last token up to the end of its 32-, 64- or 128-token tile, and multiplies their
+ * values by a weight of 0; a new pool is cleared once (cudaMemset), so that they are finite.  Over a
+ * 4-bit cache they may hold anything.
+ *
+ * FD_ERR_INVALID: a missing pointer, a negative stride, an output (caches included) that overlaps
+ * an input or another output (but for the in-place case), bt_stride < ceil(L_b / page_size), a bad
+ * rope or factor.
  * FD_ERR_ALIGN: a device pointer not 16-byte aligned (positions, block_table, status: 4) or a
  * stride not a multiple of 8.  FD_ERR_UNSUPPORTED: rot_dim, num_pages * page_size >= 2^31.
  * Asynchronous; launched with programmatic dependent launch like fd_decode.
@@ -450,7 +456,8 @@ int fd_append(fd_rows_t rows, const fd_append_args* args, cudaStream_t stream);
  * the q type.
  *
  *   k_cache, v_cache, num_pages, block_table, bt_stride, status   as for fd_append
- *   k_out, v_out   device [T, Hkv, d] in the q type, contiguous, not overlapping the caches
+ *   k_out, v_out   device [T, Hkv, d] in the q type, contiguous, overlapping neither each other
+ *                  nor the caches (FD_ERR_INVALID)
  *
  * A row whose page index lies outside [0, num_pages) reads zeros.  Errors as for fd_append.
  */

@@ -50,31 +50,26 @@ FD_HD constexpr int kv_row_bytes(int path, int d) {
 // Tokens per row of the TMA view: a 4-bit cache is made of blocks of 16 tokens.
 constexpr int kBlockTokens = 16, kBlockShift = 4;
 FD_HD constexpr int row_tokens(int path) { return path == kPathMmaKv4 ? kBlockTokens : 1; }
-#ifndef KV4_TILE
-#define KV4_TILE 128
-#define KV4_CPS 2
-#define KV4_RING (96 * 1024)
-#endif
-#ifndef KV4_WARPS
-#define KV4_WARPS 8
-#define KV4_SCTAS 2
-#endif
-// The 4-bit stream kernel: warps per CTA and CTAs per SM, by the registers a group of heads takes.
-FD_HD constexpr int stream_warps(int G) { return G <= 8 ? KV4_WARPS : 12; }
-FD_HD constexpr int stream_ctas(int G) { return G <= 8 ? KV4_SCTAS : 1; }
-constexpr int kStreamTile = 128;  // tokens that four warps take together
-constexpr int kStreamSlotTokens = 32;
-#ifndef KV4_UNITS
-#define KV4_UNITS 4
-#endif
-constexpr int kPairUnits = KV4_UNITS;   // what a pair costs a run beyond its tiles, in tiles
+// The 4-bit stream kernel (fd_kv4.cuh): warps per CTA and CTAs per SM, by the registers that a
+// group of heads takes (at most 128 for G <= 8, 168 for G = 16).  One CTA of 16 warps instead of
+// two of 8: 103.5 against 99.7 us on 64 sequences of 8K tokens (their merges stop the whole SM).
+FD_HD constexpr int stream_warps(int G) { return G <= 8 ? 8 : 12; }
+FD_HD constexpr int stream_ctas(int G) { return G <= 8 ? 2 : 1; }
+constexpr int kStreamTile = 128;       // tokens that four warps take together
+constexpr int kStreamSlotTokens = 32;  // tokens of a ring slot, and of a warp's share of a tile
+// What a (sequence, KV head) pair costs a run beyond its tiles, in tiles.  (A ragged batch of 17, G =
+// 16: 39 us with 0, 19.4 with 2, 18.9 with 4, 17.4 with 6; 64 sequences of 8K: 99.7, 99.7, 100.3
+// with 2, 4, 6.)
+constexpr int kPairUnits = 6;
 // Host mode of the 4-bit stream kernel, and its largest grid.
 constexpr int kModeStream = 8;
 constexpr int kMaxStreamCtas = 320;
 // Tokens per pipeline stage.
 // (FP8: 128-token tiles, two 16-token groups per consumer warp per stage.)
 FD_HD constexpr int tile_for(int path) {
-  return (path == kPathUmma || path == kPathMmaKv8) ? 128 : path == kPathMmaKv4 ? KV4_TILE : is_mma(path) ? 64 : 32;
+  return (path == kPathUmma || path == kPathMmaKv8 || path == kPathMmaKv4) ? 128
+         : is_mma(path)                                                    ? 64
+                                                                           : 32;
 }
 // Bytes of that row in the ring.  A TMA box has to start on a multiple of 128 bytes of shared
 // memory, and with pages of 16 tokens every 4-bit block is a box of its own: a d = 64 block of
@@ -110,7 +105,7 @@ constexpr int kRingBytes = 96 * 1024;
 // A kernel that uses tcgen05 instructions is resident one CTA per SM (the occupancy
 // calculator reports 1 for any such kernel, whatever its shared memory), so that
 // path gets the bytes in flight of two CTAs of the other paths: a 192 KB ring.
-FD_HD constexpr int ctas_per_sm_for(int path) { return path == kPathUmma ? 1 : path == kPathMmaKv4 ? KV4_CPS : 2; }
+FD_HD constexpr int ctas_per_sm_for(int path) { return path == kPathUmma ? 1 : 2; }
 // Plans of many short CTAs on the mma.sync path run three CTAs per SM with 64 KB
 // rings instead (kShallowCtasPerSm): one CTA's ramp and tail then leave two others
 // streaming.  (Measured on 64 sequences of 8K tokens: 512-token CTAs 305.2 against
@@ -122,7 +117,7 @@ constexpr int kShallowRingBytes = 64 * 1024;
 // the registers of two, though only one is resident.)
 FD_HD constexpr int build_ctas_for(int path) { return path == kPathUmma ? 2 : ctas_per_sm_for(path); }
 FD_HD constexpr int ring_target_bytes(int path, int cps) {
-  return path == kPathMmaKv4 ? KV4_RING : path == kPathUmma ? 2 * kRingBytes : cps == kShallowCtasPerSm ? kShallowRingBytes : kRingBytes;
+  return path == kPathUmma ? 2 * kRingBytes : cps == kShallowCtasPerSm ? kShallowRingBytes : kRingBytes;
 }
 FD_HD constexpr int slot_bytes_for(int path, int d) {
   return (2 / loads_per_tile(path)) * tile_for(path) * ring_row_bytes(path, d);

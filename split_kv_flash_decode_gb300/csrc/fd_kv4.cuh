@@ -443,9 +443,15 @@ struct Kv4Warp {
 // CTA is written at once, else the CTA publishes a record and the last one to arrive at the pair's
 // counter combines them, in order.  No CTA waits for another.
 //
-// Measured on 64 sequences of 8K tokens (604 MB): the loads alone 90 us, the arithmetic alone 55 us.
-// Rings shared by a quad, refilled by its last warp to finish, ran 118 us: the hand-over took 93
-// of 325 instructions per block and warp.
+// What bounds it: HBM for long sequences (64 sequences of 8K tokens, 604 MB, G = 4: 100 us, 6.05 TB/s
+// of the 6.8 TB/s that a copy reaches; 128K tokens, G = 8: 32.1 us for 151 MB).  The loads alone
+// take 90 us there and the arithmetic alone 55 us (238 instructions per block and warp, 104 of
+// them on the half-rate ALU pipe), so a slot must not be held for longer than the loads of the
+// others take: a warp is done with its 32 tokens in about 2100 cycles; held for 3000, the loads alone
+// would take 115 us.  Rings shared by four warps and refilled by the last of them to finish ran at
+// 118 us, one CTA per partial (8192 short CTAs) at 212 us.  Short inputs are bound by latencies: one
+// 32K-token sequence (G = 4) takes 13.1 us for 38 MB, of which the first loads 2 us, the merge and the
+// arrival 2 us and the combine of 15 records 3 us.
 template <int D, int G>
 struct Kv4Stream {
   static constexpr int kTile = kStreamTile;
@@ -471,7 +477,7 @@ struct Kv4Stream {
   // The combine keeps its partial sums and the coefficients [kHeads][records] where the states were.
   static_assert((kWarps - kSplit) * D >= kMaxStreamCtas, "coefficients of the longest pair");
   static_assert(kSlots >= 2 && kWarps * kSlots * 8 + 16 <= 1024, "ring");
-  static_assert(kTile == 4 * 16 * kSub, "a quad covers a tile");
+  static_assert(kTile == 4 * 16 * kSub && kStreamSlotTokens == 16 * kSub, "a quad covers a tile");
   static_assert(kWarps % 4 == 0 && kStateBytes % 16 == 0, "float4 rows");
 };
 
@@ -572,7 +578,10 @@ struct StreamCursor {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int a = row + k * kBlockTokens, pg = min(a >> p.page_shift, last_pg);
-      page[k] = (__ldg(bt + pg) * (1 << p.page_shift) + (a & ((1 << p.page_shift) - 1))) >> kBlockShift;
+      // An index that no pool has goes to a row outside every pool (TMA reads zeros there).
+      const int entry = __ldg(bt + pg);
+      const bool possible = (uint32_t)entry <= (0x7fffffffu >> p.page_shift);
+      page[k] = possible ? ((entry << p.page_shift) + (a & ((1 << p.page_shift) - 1))) >> kBlockShift : -kBlockTokens;
     }
   }
   // Past one load.
@@ -603,18 +612,18 @@ template <int D, int G, bool PAGED>
 __device__ __forceinline__ void stream_load(const Params& p, const StreamCursor<PAGED>& cur, uint32_t dst, uint32_t bar,
                                             uint64_t policy) {
   using S = Kv4Stream<D, G>;
-  const int kvh = cur.sp.kvh, row = cur.row;
+  const int kvh = cur.sp.kvh;
   mbar_arrive_expect_tx(bar, S::kSlotBytes);
   if constexpr (!PAGED) {
-    tma_load_3d(dst, &p.tm_k, 0, kvh, row, bar, policy);
-    tma_load_3d(dst + S::kRowsBytes, &p.tm_v, 0, kvh, row, bar, policy);
-    return;
-  }
-  // Pages of 16 tokens: a box for each half of the slot; larger pages hold all of it.
-  for (int k = 0; k * p.box_rows < S::kSub * 16; ++k) {
-    const uint32_t to = dst + k * 16 * ring_row_bytes(kPathMmaKv4, D);
-    tma_load_3d(to, &p.tm_k, 0, kvh, cur.page[k], bar, policy);
-    tma_load_3d(to + S::kRowsBytes, &p.tm_v, 0, kvh, cur.page[k], bar, policy);
+    tma_load_3d(dst, &p.tm_k, 0, kvh, cur.row, bar, policy);
+    tma_load_3d(dst + S::kRowsBytes, &p.tm_v, 0, kvh, cur.row, bar, policy);
+  } else {
+    // Pages of 16 tokens: a box for each half of the slot; larger pages hold all of it.
+    for (int k = 0; k * p.box_rows < kStreamSlotTokens; ++k) {
+      const uint32_t to = dst + k * kBlockTokens * ring_row_bytes(kPathMmaKv4, D);
+      tma_load_3d(to, &p.tm_k, 0, kvh, cur.page[k], bar, policy);
+      tma_load_3d(to + S::kRowsBytes, &p.tm_v, 0, kvh, cur.page[k], bar, policy);
+    }
   }
 }
 

@@ -513,12 +513,19 @@ int set_rope(const fd_rope* rope, int d, bool four_bit_cache, AppendParams* p) {
   return FD_OK;
 }
 
-// Bytes [p, p + n) of one tensor and those of an input with the given strides overlap.
-bool overlap(const void* out, int64_t out_bytes, const void* in, const int64_t* stride, int64_t T, int H, int d) {
-  if (out == nullptr || in == nullptr) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
-  const uintptr_t n = 2 * (uintptr_t)((T - 1) * stride[0] + (H - 1) * stride[1] + d);
-  return a < b + n && b < a + (uintptr_t)out_bytes;
+// A range of bytes.
+struct Span {
+  uintptr_t at;
+  uint64_t n;
+};
+Span span(const void* p, int64_t n) { return {reinterpret_cast<uintptr_t>(p), p == nullptr ? 0 : (uint64_t)n}; }
+Span input_span(const void* p, const int64_t* stride, int64_t T, int H, int d) {
+  return span(p, 2 * ((T - 1) * stride[0] + (H - 1) * stride[1] + d));
+}
+bool overlap(const Span& a, const Span& b) { return a.n > 0 && b.n > 0 && a.at < b.at + b.n && b.at < a.at + a.n; }
+// Bytes of one cache.
+int64_t cache_span(const fd_rows_s* r, int num_pages) {
+  return r->page_size ? (int64_t)num_pages * r->cache_bytes : r->cache_bytes;
 }
 bool in_place(const void* out, const void* in, const int64_t* stride, int64_t T, int H, int d) {
   return out == in && (stride[1] == d || H == 1) && (stride[0] == (int64_t)H * d || T == 1);
@@ -636,14 +643,17 @@ int fd_append(fd_rows_t rows, const fd_append_args* a, cudaStream_t stream) {
   const int64_t T = r->T;
   if (T == 0) return FD_OK;
   const int heads[3] = {r->Hq, r->Hkv, r->Hkv};
-  for (int i = 0; i < 3; ++i) {
-    const int64_t qb = 2 * T * r->Hq * d, kb = 2 * T * r->Hkv * d;
-    if (!(i == 0 && fd::in_place(a->q_out, a->q, a->q_stride, T, r->Hq, d)) &&
-        fd::overlap(a->q_out, qb, ins[i], strides[i], T, heads[i], d))
-      return FD_ERR_INVALID;
-    if (!(i == 1 && fd::in_place(a->k_out, a->k, a->k_stride, T, r->Hkv, d)) &&
-        fd::overlap(a->k_out, kb, ins[i], strides[i], T, heads[i], d))
-      return FD_ERR_INVALID;
+  const int64_t cache = a->k_cache ? fd::cache_span(r, a->num_pages) : 0;
+  const fd::Span outs[4] = {fd::span(a->q_out, 2 * T * r->Hq * d), fd::span(a->k_out, 2 * T * r->Hkv * d),
+                            fd::span(a->k_cache, cache), fd::span(a->v_cache, cache)};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      // q_out may be q and k_out k, element for element.
+      if (o == i && o < 2 && fd::in_place(o ? a->k_out : a->q_out, ins[i], strides[i], T, heads[i], d)) continue;
+      if (ins[i] && fd::overlap(outs[o], fd::input_span(ins[i], strides[i], T, heads[i], d))) return FD_ERR_INVALID;
+    }
+    for (int k = 0; k < o; ++k)
+      if (fd::overlap(outs[o], outs[k])) return FD_ERR_INVALID;
   }
   p.q = a->q; p.k = a->k; p.v = a->v;
   p.q_weight = a->q_weight; p.k_weight = a->k_weight;
@@ -678,6 +688,11 @@ int fd_gather(fd_rows_t rows, const void* k_cache, const void* v_cache, int num_
   int rc = fd::make_map(rows, num_pages, block_table, bt_stride, status, &p.m);
   if (rc != FD_OK) return rc;
   if (rows->T == 0) return FD_OK;
+  const int64_t cache = fd::cache_span(rows, num_pages), bytes = 2 * rows->T * rows->Hkv * rows->d;
+  const fd::Span outs[2] = {fd::span(k_out, bytes), fd::span(v_out, bytes)};
+  for (const fd::Span& o : outs)
+    if (fd::overlap(o, fd::span(k_cache, cache)) || fd::overlap(o, fd::span(v_cache, cache))) return FD_ERR_INVALID;
+  if (fd::overlap(outs[0], outs[1])) return FD_ERR_INVALID;
   p.k_cache = k_cache; p.v_cache = v_cache;
   p.k_out = k_out; p.v_out = v_out;
   p.T = (int32_t)rows->T;

@@ -205,6 +205,18 @@ def test_append(fd, dtype, form):
         assert np.array_equal(oracle.dequantise(codes, scales), vv[0])
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 16), (64, 48), (128, 16), (128, 48), (128, 80), (128, 112)])
+def test_partial_rotations_that_cut_blocks(fd, d, rot, inter):
+    """Rotated parts that are no multiple of 32 (16-bit and E4M3 caches only)."""
+    for dtype in ("bf16", "f16_e4m3kv"):
+        test_append(fd, dtype, (d, 3, 3, rot, inter, 1, rot == 48, 0))
+    s = Setup(fd, "f16_e2m1kv", d, 3, 3, [4], [0], [4])
+    with pytest.raises(fd.FdError) as e:
+        s.append(rope=fd.Rope([1.0] * (rot // 2)))
+    assert e.value.status == fd.FD_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("d,page", [(64, 0), (128, 0), (64, 16), (128, 64)])
 def test_gather_returns_what_is_stored(fd, dtype, d, page):

@@ -114,6 +114,10 @@ def test_append_refusals():
         (dict(q_out=P + 256), fd.FD_ERR_INVALID),                          # overlaps q, shifted
         (dict(q_out=P, q_stride=(2048, 128)), fd.FD_ERR_INVALID),          # in place, not contiguous
         (dict(k_out=3 * P + 16), fd.FD_ERR_INVALID),                       # overlaps v
+        (dict(k_out=4 * P + 512), fd.FD_ERR_INVALID),                      # overlaps q_out
+        (dict(v_cache=6 * P + 4096), fd.FD_ERR_INVALID),                   # overlaps k_cache
+        (dict(v_cache=5 * P - 16), fd.FD_ERR_INVALID),                     # overlaps k_out
+        (dict(k_cache=2 * P + 256), fd.FD_ERR_INVALID),                    # overlaps k
         (dict(q=P + 8), fd.FD_ERR_ALIGN), (dict(k_cache=6 * P + 4), fd.FD_ERR_ALIGN),
         (dict(q_weight=P + 2), fd.FD_ERR_ALIGN), (dict(positions=P + 2), fd.FD_ERR_ALIGN),
         (dict(k_stride=(256, 130)), fd.FD_ERR_ALIGN), (dict(status=P + 2), fd.FD_ERR_ALIGN),
@@ -182,6 +186,8 @@ def test_gather_refusals():
     assert L.fd_gather(r.handle, P + 8, P, 0, None, 0, P, P, None, None) == fd.FD_ERR_ALIGN
     assert L.fd_gather(r.handle, P, P, 0, None, 0, P, P, P + 1, None) == fd.FD_ERR_ALIGN
     assert L.fd_gather(r.handle, P, P, 1, P, 7, P, P, None, None) == fd.FD_ERR_INVALID
+    assert L.fd_gather(r.handle, P, 2 * P, 0, None, 0, 3 * P, 3 * P + 512, None, None) == fd.FD_ERR_INVALID
+    assert L.fd_gather(r.handle, P, 2 * P, 0, None, 0, 3 * P, 2 * P - 512, None, None) == fd.FD_ERR_INVALID
 
 
 def test_no_tokens_launch_nothing():
