@@ -128,7 +128,9 @@ enum fd_status {
  * reports FD_ERR_TIMEOUT and the out/lse of (sequence 0, KV head 0) lack that
  * partial.  Needs L_0 large enough for slot 0 to span two tiles (128 tokens with
  * FD_PLAN_TCGEN05 or an E4M3 cache, 64 on the other tensor-core paths, 32 on CUDA
- * cores); otherwise nothing is skipped.  Not with FD_PLAN_TEST_DROP_FLAG. */
+ * cores); otherwise nothing is skipped.  In a stream plan, one warp of the first CTA
+ * never loads its tiles (the second one of that CTA is the first of them), and that CTA
+ * contributes nothing to the pairs that end after it gives up.  Not with FD_PLAN_TEST_DROP_FLAG. */
 #define FD_PLAN_TEST_SKIP_TILE 0x200u
 /* Test hook for the shared combine's bounded wait: partial slot 1 of (sequence 0, KV
  * head 0) publishes its partial but never arrives.  The combiners of that pair wait
@@ -484,7 +486,7 @@ typedef struct fd_plan_info {
                               2: tensor-core over an E4M3 cache, 3: tcgen05 tensor cores,
                               4: tensor-core over a 4-bit cache */
   int32_t records_per_segment; /* partial records per segment: 1 (chunks merged in a
-                                  cluster) or chunks */
+                                  cluster) or chunks; 0: a stream plan ("Stream plans") */
   int32_t combine_cluster; /* CTAs per cluster that combine a pair's partials in shared
                               memory (FD_PLAN_CLUSTER_COMBINE: W * chunks), else 0 */
   int32_t combiners;       /* CTAs that share the combine of one pair: a power of two
@@ -492,7 +494,6 @@ typedef struct fd_plan_info {
                               1 = the last arriver alone */
   int32_t ctas_per_sm;     /* resident CTAs per SM the split kernel is launched for:
                               2 (96 KB rings), 3 (64 KB rings) or 1 (tcgen05) */
-  int32_t stream;          /* 1: a stream plan (4-bit caches, see FD_F16_E2M1KV) */
 } fd_plan_info;
 
 int fd_plan_get_info(fd_plan_t plan, fd_plan_info* info);

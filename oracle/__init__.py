@@ -4,7 +4,7 @@ Only ``tests/``, ``__graft_entry__.smoke()`` and ``bench.py``'s cpu-baseline and
 reference legs may import this package.  The CUDA library never imports, links
 or calls it, and it imports nothing from the CUDA library.
 
-Every function is pinned by ``tests/test_oracle.py`` (``-m "not gpu"``) against
+Every function is pinned by ``tests/test_oracle.py`` or ``tests/test_oracle_rows.py`` (``-m "not gpu"``) against
 brute force, closed forms, invariants and library routines; no function here is
 "parity unpinned".
 """

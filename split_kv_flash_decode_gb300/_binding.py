@@ -80,7 +80,7 @@ class PlanInfo(ctypes.Structure):
         ("workspace_bytes", ctypes.c_uint64), ("kv_bytes", ctypes.c_uint64),
         ("path", ctypes.c_int32), ("records_per_segment", ctypes.c_int32),
         ("combine_cluster", ctypes.c_int32), ("combiners", ctypes.c_int32),
-        ("ctas_per_sm", ctypes.c_int32), ("stream", ctypes.c_int32),
+        ("ctas_per_sm", ctypes.c_int32),
     ]
 
 
@@ -250,6 +250,7 @@ class Plan:
         info = PlanInfo()
         _check(lib().fd_plan_get_info(handle, ctypes.byref(info)), "fd_plan_get_info")
         self.info = {name: getattr(info, name) for name, _ in PlanInfo._fields_}
+        self.info["stream"] = int(info.records_per_segment == 0)
 
     @property
     def workspace_bytes(self) -> int:

@@ -405,11 +405,10 @@ int fd_plan_get_info(fd_plan_t pl, fd_plan_info* info) {
   info->workspace_bytes = pl->ws_bytes;
   info->kv_bytes = (uint64_t)pl->n_tokens * pl->Hkv * 2 * fd::kv_row_bytes(pl->path, pl->d);
   info->path = pl->path;
-  info->records_per_segment = pl->params.rps;
+  info->records_per_segment = pl->stream ? 0 : pl->params.rps;
   info->combine_cluster = pl->params.pair_cluster;
   info->combiners = pl->params.combiners;
   info->ctas_per_sm = pl->params.ctas_per_sm;
-  info->stream = pl->stream;
   return FD_OK;
 }
 

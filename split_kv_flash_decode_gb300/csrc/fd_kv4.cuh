@@ -656,8 +656,6 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
     for (int s = 0; s < NSLOT; ++s) mbar_init(bar + 8 * s, 1);
     fence_mbar_init();
     if (tid == 0) words[0] = 0;
-    prefetch_tensormap(&p.tm_k);
-    prefetch_tensormap(&p.tm_v);
   }
   // The warp's loads, one slot after the other.
   StreamCursor<PAGED> cur;
@@ -666,9 +664,13 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
   cur.seek(p, quad, i1);
   cur.batch(p, S::kQuads, first_token, i1);
   // The first slot into L2 while the previous kernel drains (see fd_split_kernel).
-  if (!PAGED && cur.left > 0 && lane == 0) {
-    tma_prefetch_l2_3d(&p.tm_k, 0, cur.sp.kvh, cur.row);
-    tma_prefetch_l2_3d(&p.tm_v, 0, cur.sp.kvh, cur.row);
+  if (cur.left > 0 && lane == 0) {
+    prefetch_tensormap(&p.tm_k);
+    prefetch_tensormap(&p.tm_v);
+    if (!PAGED) {
+      tma_prefetch_l2_3d(&p.tm_k, 0, cur.sp.kvh, cur.row);
+      tma_prefetch_l2_3d(&p.tm_v, 0, cur.sp.kvh, cur.row);
+    }
   }
   if (p.test_hook == kHookSkipTile && c == 0 && warp == 4) cur.left = 0;  // test hook: loads nothing
   auto load_next = [&](int slot) {

@@ -19,7 +19,7 @@ _KV_DTYPE = {"f16": torch.float16, "bf16": torch.bfloat16, "f16_e4m3kv": torch.u
 def cache_shape(dtype, Hkv, d, seqlens=None, num_pages=None, page_size=0):
     """Shape of the K (and of the V) cache: of the contiguous cache of `seqlens`, or of a pool of
     `num_pages` pages.  4-bit caches are made of blocks of 16 tokens (include/fd.h)."""
-    unit, last = (16, 9 * d) if dtype.endswith("e2m1kv") else (1, d)
+    unit, last = (16, 9 * d) if str(dtype).endswith("e2m1kv") else (1, d)
     if page_size:
         return (num_pages, page_size // unit, Hkv, last)
     return (sum((int(x) + unit - 1) // unit for x in seqlens), Hkv, last)
@@ -50,69 +50,67 @@ class Decoder:
                                       num_sms)
             self.workspace = torch.zeros(max(1, self.plan.workspace_bytes), dtype=torch.uint8,
                                          device=self.device)
-        self._workspace_ptr = self.workspace.data_ptr()
-        if self.page_size:
-            self._page_shape = cache_shape(dtype, self.Hkv, self.d, None, 0, self.page_size)[1:]
-        else:
-            self._kv_shape = cache_shape(dtype, self.Hkv, self.d, self.seqlens)
+        self._lse_shape = (self.Bsz, self.Hq)
+        self._t16, self._kv = _TORCH_DTYPE.get(dtype), _KV_DTYPE.get(dtype)
+        self._decode, self._decode_paged = B.lib().fd_decode, B.lib().fd_decode_paged
+        self._kv_shape = cache_shape(dtype, self.Hkv, self.d, self.seqlens)
+        self._page_shape = cache_shape(dtype, self.Hkv, self.d, None, 0, self.page_size or 16)[1:]
 
     @property
     def info(self) -> dict:
         return self.plan.info
 
-    def _check(self, name, t, shape, dtype):
+    def _refuse(self, name, t, shape, dtype):
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, expected {self.device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} must be contiguous")
+
+    def _check(self, name, t, shape, dtype):
+        """Address of a contiguous tensor of this shape and type on the device."""
+        if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
+            self._refuse(name, t, shape, dtype)
         return t.data_ptr()
 
-    def _outputs(self, q, out, lse):
-        """Addresses of q, out and lse, the latter two allocated where missing."""
-        t16 = _TORCH_DTYPE[self.dtype]
-        q_ptr = self._check("q", q, self._q_shape, t16)
+    def _run(self, call, name, q, kv, out, lse, stream):
+        """call(plan, q, *kv, out, lse, workspace, stream), out and lse allocated where missing."""
+        q_ptr = self._check("q", q, self._q_shape, self._t16)
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty(self._q_shape[:2], dtype=torch.float32, device=self.device)
-        return (out, lse, q_ptr, self._check("out", out, self._q_shape, t16),
-                self._check("lse", lse, self._q_shape[:2], torch.float32))
+            lse = torch.empty(self._lse_shape, dtype=torch.float32, device=self.device)
+        index = self.device.index
+        rc = B.on_device(index, call, self.plan.handle, q_ptr, *kv, B._ptr(out), B._ptr(lse),
+                         self.workspace.data_ptr(), B.stream_on(index, stream))
+        if rc != B.FD_OK:
+            raise B.FdError(rc, name)
+        return out, lse
 
     def __call__(self, q, k, v, out=None, lse=None, stream=None):
-        out, lse, q_ptr, out_ptr, lse_ptr = self._outputs(q, out, lse)
-        kv = _KV_DTYPE[self.dtype]
-        k_ptr, v_ptr = self._check("k", k, self._kv_shape, kv), self._check("v", v, self._kv_shape, kv)
-        index = self.device.index
-        rc = B.on_device(index, B.lib().fd_decode, self.plan.handle, q_ptr, k_ptr, v_ptr, out_ptr, lse_ptr,
-                         self._workspace_ptr, B.stream_on(index, stream))
-        if rc != B.FD_OK:
-            raise B.FdError(rc, "fd_decode")
-        return out, lse
+        if out is not None:
+            self._check("out", out, self._q_shape, self._t16)
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != self._lse_shape):
+            raise ValueError("lse must be float32 [B, Hq]")
+        kv = (self._check("k", k, self._kv_shape, self._kv), self._check("v", v, self._kv_shape, self._kv))
+        return self._run(self._decode, "fd_decode", q, kv, out, lse, stream)
 
     def decode_paged(self, q, k_pages, v_pages, block_table, out=None, lse=None, stream=None):
         """Decode over a paged cache: pools [num_pages, page_size, Hkv, d] (or as cache_shape says),
         int32 block_table [B, stride]."""
         if not self.page_size:
             raise ValueError("this Decoder was planned for contiguous K/V")
-        out, lse, q_ptr, out_ptr, lse_ptr = self._outputs(q, out, lse)
-        kv, num_pages = _KV_DTYPE[self.dtype], k_pages.shape[0]
+        num_pages = k_pages.shape[0]
         shape = (num_pages, *self._page_shape)
-        k_ptr, v_ptr = self._check("k_pages", k_pages, shape, kv), self._check("v_pages", v_pages, shape, kv)
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
                 block_table.shape[0] != self.Bsz or not block_table.is_contiguous() or \
                 block_table.device != self.device:
             raise ValueError("block_table must be a contiguous int32 [B, stride] tensor on the device")
-        index = self.device.index
-        rc = B.on_device(index, B.lib().fd_decode_paged, self.plan.handle, q_ptr, k_ptr, v_ptr, num_pages,
-                         block_table.data_ptr(), block_table.shape[1], out_ptr, lse_ptr,
-                         self._workspace_ptr, B.stream_on(index, stream))
-        if rc != B.FD_OK:
-            raise B.FdError(rc, "fd_decode_paged")
-        return out, lse
+        kv = (self._check("k_pages", k_pages, shape, self._kv), self._check("v_pages", v_pages, shape, self._kv),
+              num_pages, block_table.data_ptr(), block_table.shape[1])
+        return self._run(self._decode_paged, "fd_decode_paged", q, kv, out, lse, stream)
 
     def status(self, stream=None) -> int:
         with torch.cuda.device(self.device):

@@ -66,6 +66,7 @@ class KVRows:
                                    self.page_size, dtype)
         self.tokens = self.rows.tokens
         self._t16, self._kv = _TORCH_DTYPE[dtype], _KV_DTYPE[dtype]
+        self._append, self._gather = B.lib().fd_append, B.lib().fd_gather
         self._q_shape = (self.tokens, self.Hq, self.d)
         self._k_shape = (self.tokens, self.Hkv, self.d)
         self._cache_shape = cache_shape(dtype, self.Hkv, self.d, self.seqlens, 0, self.page_size)
@@ -125,7 +126,9 @@ class KVRows:
             q_in = self._input("q", q, self._q_shape)
             if q_out is None:
                 q_out = torch.empty(self._q_shape, dtype=self._t16, device=self.device)
-            q_to = self._whole("q_out", q_out, self._q_shape, self._t16)
+                q_to = q_out.data_ptr()
+            else:
+                q_to = self._whole("q_out", q_out, self._q_shape, self._t16)
         elif q_out is not None:
             raise ValueError("q_out without q")
         if k is not None:
@@ -160,7 +163,7 @@ class KVRows:
             k_mul, v_mul, cache[2], cache[4], cache[3], self._status(status))
         if self.tokens:  # no rows: empty tensors have null addresses
             index = self.device.index
-            rc = B.on_device(index, B.lib().fd_append, self.rows.handle, args, B.stream_on(index, stream))
+            rc = B.on_device(index, self._append, self.rows.handle, args, B.stream_on(index, stream))
             if rc != B.FD_OK:
                 raise B.FdError(rc, "fd_append")
         return q_out
@@ -171,13 +174,17 @@ class KVRows:
         cache = self._caches(k_cache, v_cache, block_table)
         if k_out is None:
             k_out = torch.empty(self._k_shape, dtype=self._t16, device=self.device)
+            k_to = k_out.data_ptr()
+        else:
+            k_to = self._whole("k_out", k_out, self._k_shape, self._t16)
         if v_out is None:
             v_out = torch.empty(self._k_shape, dtype=self._t16, device=self.device)
-        k_to = self._whole("k_out", k_out, self._k_shape, self._t16)
-        v_to = self._whole("v_out", v_out, self._k_shape, self._t16)
+            v_to = v_out.data_ptr()
+        else:
+            v_to = self._whole("v_out", v_out, self._k_shape, self._t16)
         if self.tokens:
             index = self.device.index
-            rc = B.on_device(index, B.lib().fd_gather, self.rows.handle, *cache, k_to, v_to, self._status(status),
+            rc = B.on_device(index, self._gather, self.rows.handle, *cache, k_to, v_to, self._status(status),
                              B.stream_on(index, stream))
             if rc != B.FD_OK:
                 raise B.FdError(rc, "fd_gather")
