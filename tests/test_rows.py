@@ -344,6 +344,36 @@ def test_strides_and_in_place(fd):
         rows.append(q2, k2, k_out=q2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16_e4m3kv", "f16_e2m1kv"])
+def test_subsets_of_outputs(fd, dtype):
+    """q alone, k alone, k in place while it is stored, and all together: the same values."""
+    import torch
+    s = Setup(fd, dtype, 64, 4, 2, [50, 7], [20, 0], [30, 7], page_size=32, seed=17)
+    w = s.weights
+    norm = dict(q_weight=w[0], k_weight=w[1], rope=fd.Rope(10000.0 ** (-np.arange(32) / 32)))
+    k_out = torch.empty((37, 2, 64), dtype=q_type(dtype), device="cuda")
+    q = s.append(k_out=k_out, **norm)
+    kept = [x.clone() for x in (s.k_cache, s.v_cache)]
+    s.stored()
+    only = {n: x for n, x in norm.items() if n != "k_weight"}
+    assert torch.equal(s.rows.append(s.q, **only), q)
+    only = {n: x for n, x in norm.items() if n != "q_weight"}
+    k2 = torch.empty_like(k_out)
+    assert s.rows.append(None, s.k, k_out=k2, **only) is None
+    assert torch.equal(k2, k_out)
+    s.k_cache.zero_(), s.v_cache.zero_()
+    k3 = s.k.contiguous()
+    s.rows.append(None, k3, s.v, s.k_cache, s.v_cache, block_table=s.table, k_out=k3, **only)
+    assert torch.equal(k3, k_out)
+    got = s.rows.gather(s.k_cache, s.v_cache, block_table=s.table)
+    want = s.rows.gather(*kept, block_table=s.table)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # Without a cache a 4-bit handle rotates any multiple of 16.
+    y = s.rows.append(s.q, rope=fd.Rope([0.5] * 8))
+    ref, before = oracle.norm_rotate(f64(s.q), inv_freq=[0.5] * 8, positions=s.pos[None])
+    close(f64(y), ref, pair_size(before, 8, False), q_name(dtype))
+
+
 def test_bad_pages_are_reported_not_written(fd):
     import torch
     for dtype in DTYPES:
