@@ -225,23 +225,6 @@ def _stream(stream) -> int:
     return int(stream.cuda_stream)
 
 
-def on_device(index: int, call, *args) -> int:
-    """call(*args) with CUDA device `index` current."""
-    import torch
-    if torch._C._cuda_getDevice() == index:
-        return call(*args)
-    with torch.cuda.device(index):
-        return call(*args)
-
-
-def stream_on(index: int, stream) -> int:
-    """Address of `stream`, or of torch's current stream of device `index`."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index)
-    return _stream(stream)
-
-
 class Plan:
     """Owns one fd_plan_t handle (fd_plan_destroy on close / garbage collection)."""
 
