@@ -2,6 +2,8 @@
 // default.  Included by fd_kernel.cuh, which provides the primitives.
 #pragma once
 
+#include <cfloat>
+
 namespace fd {
 namespace dev {
 
@@ -67,12 +69,14 @@ struct Kv4Warp {
       }
     }
   }
+  // The empty state.  Its maximum is the lowest finite value: -inf logits (products that overflow)
+  // then have the weight 0 also where a warp has met no other, while -inf - -inf would be NaN.
   __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int mi = 0; mi < KT; ++mi) o[nt][mi][0] = o[nt][mi][1] = o[nt][mi][2] = o[nt][mi][3] = 0.f;
-      mA[nt] = mB[nt] = -INFINITY;
+      mA[nt] = mB[nt] = -FLT_MAX;
       lA[nt] = lB[nt] = lrA[nt] = lrB[nt] = 0.f;
     }
   }
@@ -215,7 +219,6 @@ struct Kv4Warp {
           mB[nt] = xB;
         }
       }
-      // The first token is valid, so mA and mB are finite here (unless its logit is NaN).
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
         const float pA0 = ex2(sc[u][nt][0] - mA[nt]), pB0 = ex2(sc[u][nt][1] - mB[nt]);
@@ -334,7 +337,7 @@ struct Kv4Warp {
     for (int nt = 0; nt < NT; ++nt) {
       const int hA = kTwice ? 2 * (t & 1) : nt * 8 + 2 * t;
       const float MA = head_max<NWARP>(m, hA), MB = head_max<NWARP>(m, hA + 1);
-      const float fA = MA == -INFINITY ? 0.f : ex2(mA[nt] - MA), fB = MB == -INFINITY ? 0.f : ex2(mB[nt] - MB);
+      const float fA = ex2(mA[nt] - MA), fB = ex2(mB[nt] - MB);
       if constexpr (kTwice) {
 #pragma unroll
         for (int f = 0; f < kFrags; ++f) {
@@ -481,7 +484,7 @@ struct Kv4Stream {
   static_assert(kWarps % 4 == 0 && kStateBytes % 16 == 0, "float4 rows");
 };
 
-// Merge of (max, sum, sum) triples; a -inf max comes with sums that are 0, or NaN if a score was.
+// Merge of (max, sum, sum) triples; a -inf max (a CTA that gave up) comes with sums of 0.
 __device__ __forceinline__ void stream_merge(float& M, float& l, float& lr, float m2, float l2, float lr2) {
   if (m2 > M) {
     const float c = ex2(M - m2);
@@ -756,8 +759,9 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
         const int h = W::frag_head(v >> 5, lane);
         const float lA = aborted ? 0.f : W::template head_sum<NW>(st_lr, h);
         const float lB = aborted ? 0.f : W::template head_sum<NW>(st_lr, h + 1);
-        // No token: out = 0 (a NaN sum stays NaN).
-        W::put_out(out, v >> 5, lane, a, lA != 0.f ? 1.f / lA : 0.f, lB != 0.f ? 1.f / lB : 0.f);
+        // No token: out = 0.  Tokens without any weight, or with a NaN: NaN.
+        const bool any = done.len > 0 && !aborted;
+        W::put_out(out, v >> 5, lane, a, any ? 1.f / lA : 0.f, any ? 1.f / lB : 0.f);
       } else {
         __stcg(reinterpret_cast<float4*>(rec) + v, a);
       }
@@ -862,7 +866,7 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
       }
       if constexpr (S::kSplit == 1) {
         const float lA = st_lr[h], lB = st_lr[h + 1];
-        W::put_out(out, it >> 5, lane, a, lA != 0.f ? 1.f / lA : 0.f, lB != 0.f ? 1.f / lB : 0.f);
+        W::put_out(out, it >> 5, lane, a, 1.f / lA, 1.f / lB);
       } else {
         sums[v] = a;
       }
@@ -874,7 +878,7 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
         const int h = W::frag_head(v >> 5, lane);
         const float lA = st_lr[h], lB = st_lr[h + 1];
         W::put_out(out, v >> 5, lane, make_float4(a.x + y.x, a.y + y.y, a.z + y.z, a.w + y.w),
-                   lA != 0.f ? 1.f / lA : 0.f, lB != 0.f ? 1.f / lB : 0.f);
+                   1.f / lA, 1.f / lB);
       }
     }
     __syncthreads();  // the next pair overwrites the sums

@@ -261,3 +261,23 @@ def test_stream_runs_cut_anywhere(fd):
             again = c.run(dec)
             assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
             assert not dec.workspace[256:256 + 4 * len(lens) * Hkv].any()
+
+
+@pytest.mark.parametrize("G,d", [(1, 128), (4, 64), (8, 128), (16, 64)])
+def test_scores_that_overflow_have_no_weight(fd, G, d):
+    """Scores of -1e45 (-inf in fp32) in whole warps' and whole CTAs' shares of a sequence: the tokens
+    with zero keys take all the weight, equal parts of it."""
+    import torch
+    c = Case(fd, "bf16_e2m1kv", d, G, 2, [3000, 100], [3, 1], seed=31, garbage=False)
+    c.q = torch.full_like(c.q, 1e38)
+    low = np.ones(188 + 7, bool)              # blocks of 16 tokens: -2688 everywhere, but zeros in some
+    low[[100, 101, 150, 188 + 5]] = False
+    k = np.zeros(tuple(c.k.shape), np.uint8)
+    k[low, :, :8 * d], k[low, :, 8 * d:] = 0xFF, 0x7E
+    c.k = torch.from_numpy(k).cuda()
+    for b, (at, blocks) in enumerate([(0, [100, 101, 150]), (3000, [5])]):
+        tokens = np.concatenate([at + 16 * j + np.arange(16) for j in blocks])
+        mean = np.repeat(c.values[1][tokens].mean(0), G, axis=0)
+        c.ref[0][b], c.ref[1][b] = mean, np.log(len(tokens))
+    for flags in (0, fd.FD_PLAN_TWO_LAUNCH, fd.FD_PLAN_WAITS):
+        c.check(*c.run(c.decoder(flags=flags)))
