@@ -30,6 +30,17 @@ def launch(index, stream, call, *args):
         return call(*args, address)
 
 
+def empty(stream, shape, dtype, device):
+    """torch.empty from the memory pool of the stream that will write it: memory just freed on the
+    current stream may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def cache_shape(dtype, Hkv, d, seqlens=None, num_pages=None, page_size=0):
     """Shape of the K (and of the V) cache: of the contiguous cache of `seqlens`, or of a pool of
     `num_pages` pages.  4-bit caches are made of blocks of 16 tokens (include/fd.h)."""
@@ -93,9 +104,9 @@ class Decoder:
         """call(plan, q, *kv, out, lse, workspace, stream), out and lse allocated where missing."""
         q_ptr = self._check("q", q, self._q_shape, self._t16)
         if out is None:
-            out = torch.empty_like(q)
+            out = empty(stream, self._q_shape, self._t16, self.device)
         if lse is None:
-            lse = torch.empty(self._lse_shape, dtype=torch.float32, device=self.device)
+            lse = empty(stream, self._lse_shape, torch.float32, self.device)
         rc = launch(self.device.index, stream, call, self.plan.handle, q_ptr, *kv, B._ptr(out), B._ptr(lse),
                     self.workspace.data_ptr())
         if rc != B.FD_OK:

@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _binding as B
-from .decode import _KV_DTYPE, _TORCH_DTYPE, cache_shape, launch
+from .decode import _KV_DTYPE, _TORCH_DTYPE, cache_shape, empty, launch
 
 
 class Rope:
@@ -125,7 +125,7 @@ class KVRows:
         if q is not None:
             q_in = self._input("q", q, self._q_shape)
             if q_out is None:
-                q_out = torch.empty(self._q_shape, dtype=self._t16, device=self.device)
+                q_out = empty(stream, self._q_shape, self._t16, self.device)
                 q_to = q_out.data_ptr()
             else:
                 q_to = self._whole("q_out", q_out, self._q_shape, self._t16)
@@ -172,12 +172,12 @@ class KVRows:
         """The rows of K and V back in 16 bits: (k, v), each [T, Hkv, d]."""
         cache = self._caches(k_cache, v_cache, block_table)
         if k_out is None:
-            k_out = torch.empty(self._k_shape, dtype=self._t16, device=self.device)
+            k_out = empty(stream, self._k_shape, self._t16, self.device)
             k_to = k_out.data_ptr()
         else:
             k_to = self._whole("k_out", k_out, self._k_shape, self._t16)
         if v_out is None:
-            v_out = torch.empty(self._k_shape, dtype=self._t16, device=self.device)
+            v_out = empty(stream, self._k_shape, self._t16, self.device)
             v_to = v_out.data_ptr()
         else:
             v_to = self._whole("v_out", v_out, self._k_shape, self._t16)

@@ -281,3 +281,25 @@ def test_scores_that_overflow_have_no_weight(fd, G, d):
         c.ref[0][b], c.ref[1][b] = mean, np.log(len(tokens))
     for flags in (0, fd.FD_PLAN_TWO_LAUNCH, fd.FD_PLAN_WAITS):
         c.check(*c.run(c.decoder(flags=flags)))
+
+
+def test_outputs_come_from_the_pool_of_their_stream(fd):
+    """Memory freed on the current stream may still be read there: a call on another stream does not
+    take it for its outputs."""
+    import torch
+    c = Case(fd, "f16_e2m1kv", 128, 4, 2, [300], [2], seed=32)
+    dec = c.decoder()
+    side = torch.cuda.Stream()
+    want = c.run(dec)
+    for stream in (side, side.cuda_stream):
+        freed = [torch.empty_like(c.q) for _ in range(4)] + [torch.empty(1, 8, device="cuda") for _ in range(4)]
+        places = {x.data_ptr() for x in freed}
+        del freed
+        side.wait_stream(torch.cuda.current_stream())
+        out, lse = dec(c.q, c.k, c.v, stream=stream)
+        side.synchronize()
+        assert not {out.data_ptr(), lse.data_ptr()} & places
+        assert np.array_equal(f64(out), want[0]) and np.array_equal(f64(lse), want[1])
+    out, lse = dec(c.q, c.k, c.v, stream=0)
+    torch.cuda.synchronize()
+    assert np.array_equal(f64(out), want[0]) and np.array_equal(f64(lse), want[1])
