@@ -51,21 +51,24 @@ struct Kv4Warp {
   // l: sums of the fp32 weights (for lse); lr: of the weights P.V uses (for out).
   float mA[NT], mB[NT], lA[NT], lB[NT], lrA[NT], lrB[NT];
 
-  // q of (sequence, KV head) as it is stored: issues the loads.
+  // q of (sequence, KV head) as it is stored: issues the loads.  (All warps read all of it, 16 lines
+  // per load: 8-byte loads took 0.6 us more at G = 16.)
   __device__ __forceinline__ void fetch_q(const Params& p, int b, int kvh) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int head = kTwice ? g & 3 : nt * 8 + g;
       const bool real = head < G;
-      const uint2* qh = reinterpret_cast<const uint2*>(
+      const uint4* qh = reinterpret_cast<const uint4*>(
           reinterpret_cast<const T*>(p.q) + ((int64_t)b * p.Hq + kvh * G + (real ? head : 0)) * D +
           t * (D / 4));
 #pragma unroll
-      for (int kk = 0; kk < KT; ++kk) {
-        const uint2 x = real ? qh[kk] : make_uint2(0u, 0u);
+      for (int kk = 0; kk < KT; kk += 2) {
+        const uint4 x = real ? qh[kk / 2] : make_uint4(0u, 0u, 0u, 0u);
         qb[nt][kk][0] = x.x;
         qb[nt][kk][1] = x.y;
+        qb[nt][kk + 1][0] = x.z;
+        qb[nt][kk + 1][1] = x.w;
       }
     }
   }
@@ -466,8 +469,14 @@ struct Kv4Stream {
   static constexpr int kHeads = G < 4 ? 4 : G;    // of a record (padded)
   static constexpr int kItems = kHeads * D / 4;   // fragments of a state or record
   static constexpr int kRecord = kHeads * (D + 4);  // floats: the fragments, then (m, l, l~, 0) per head
-  // Threads per fragment in the combine (each takes every kSplit-th record).
-  static constexpr int kSplit = kThreads / kItems >= 2 ? 2 : 1;
+  // The combine: thread (q, l) takes the fragments l, l + kLanes, .. (kPer of them) of every kSplit-th
+  // record from q on, sixteen loads at a time.  (G = 16, 21 records: 28 loads per thread, 1.4 us less
+  // than with one thread per fragment in two passes.  Each load sent off as soon as its register
+  // is free was slower, 128K tokens of G = 8 by 3.4 us: a warp can wait for six sets of loads only.)
+  static constexpr int kLanes = kItems < (kThreads & -kThreads) ? kItems : (kThreads & -kThreads);
+  static constexpr int kPer = kItems / kLanes;
+  static constexpr int kSplit = kPer > 1 ? kThreads / kLanes : kThreads / kItems >= 2 ? 2 : 1;
+  static constexpr int kDeep = 16 / kPer;
   static constexpr uint32_t kRowsBytes = kSub * 16 * ring_row_bytes(kPathMmaKv4, D);  // K (or V) of a slot
   static constexpr uint32_t kSlotBytes = 2 * kRowsBytes;
   // States of the warps: fragments [kWarps][kItems], m, l, lr [kHeads][kWarps].
@@ -484,7 +493,7 @@ struct Kv4Stream {
   static_assert(kWarps % 4 == 0 && kStateBytes % 16 == 0, "float4 rows");
 };
 
-// Merge of (max, sum, sum) triples; a -inf max (a CTA that gave up) comes with sums of 0.
+// Merge of (max, sum, sum) triples with finite maxima.
 __device__ __forceinline__ void stream_merge(float& M, float& l, float& lr, float m2, float l2, float lr2) {
   if (m2 > M) {
     const float c = ex2(M - m2);
@@ -492,7 +501,7 @@ __device__ __forceinline__ void stream_merge(float& M, float& l, float& lr, floa
     lr = fmaf(lr, c, lr2);
     M = m2;
   } else {
-    const float c = m2 == -INFINITY ? 1.f : ex2(m2 - M);
+    const float c = ex2(m2 - M);
     l = fmaf(l2, c, l);
     lr = fmaf(lr2, c, lr);
   }
@@ -813,72 +822,104 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
     const float* rec1 = p.part + (int64_t)c_first * 2 * S::kRecord;
     const float* rec0 = rec1 + (stream_begin(p, c_first) >= pr.at ? 0 : S::kRecord);
     auto record = [&](int r) { return r == 0 ? rec0 : rec1 + (int64_t)r * 2 * S::kRecord; };
-    // Thread v: fragment v mod kItems of every kSplit-th record, sixteen at a time; the first sixteen
-    // are on their way while the coefficients are computed.
-    constexpr int kAhead = 16;
-    float4 x[kAhead];
-    auto fetch = [&](int it, int r) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (r + u * S::kSplit < nrec) x[u] = __ldcg(reinterpret_cast<const float4*>(record(r + u * S::kSplit)) + it);
+    const int q = tid / S::kLanes, l0 = tid % S::kLanes;
+    // Maxima and sums of this warp's heads, then the first fragments, are on their way together.
+    constexpr int kMine = (H + NW - 1) / NW;
+    auto sums_of = [&](int g, int r) {
+      float4 y = __ldcg(reinterpret_cast<const float4*>(record(r) + H * D) + g);
+      y.x = fmaxf(y.x, -FLT_MAX);  // -inf: a CTA that gave up
+      return y;
     };
-    if (tid < S::kItems * S::kSplit) fetch(tid % S::kItems, tid / S::kItems);
-    for (int g = warp; g < H; g += NW) {
-      float M = -INFINITY, l = 0.f, lr = 0.f;
-      for (int r = lane; r < nrec; r += 32) {
-        const float4 ml = __ldcg(reinterpret_cast<const float4*>(record(r) + H * D) + g);
-        coef[g * nrec + r] = ml.x;
-        stream_merge(M, l, lr, ml.x, ml.y, ml.z);
+    float4 ml[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      ml[j] = make_float4(-FLT_MAX, 0.f, 0.f, 0.f);
+      if (warp + j * NW < H && lane < nrec) ml[j] = sums_of(warp + j * NW, lane);
+    }
+    float4 x[S::kDeep][S::kPer];
+    auto fetch = [&](int u, int r) {
+      if (r >= nrec) return;
+      const float4* src = reinterpret_cast<const float4*>(record(r)) + l0;
+#pragma unroll
+      for (int j = 0; j < S::kPer; ++j) x[u][j] = __ldcg(src + j * S::kLanes);
+    };
+    const int r_first = q < S::kSplit ? q : nrec;
+#pragma unroll
+    for (int u = 0; u < S::kDeep; ++u) fetch(u, r_first + u * S::kSplit);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int g = warp + j * NW;
+      if (g >= H) break;
+      float M = ml[j].x, l = ml[j].y, lr = ml[j].z;
+      if (lane < nrec) coef[g * nrec + lane] = M;
+      for (int r = lane + 32; r < nrec; r += 32) {
+        const float4 y = sums_of(g, r);
+        coef[g * nrec + r] = y.x;
+        stream_merge(M, l, lr, y.x, y.y, y.z);
       }
+      const float own = M;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      const float c = ex2(own - M);
+      l *= c;
+      lr *= c;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, M, off);
-        const float l2 = __shfl_xor_sync(0xffffffffu, l, off);
-        const float lr2 = __shfl_xor_sync(0xffffffffu, lr, off);
-        stream_merge(M, l, lr, m2, l2, lr2);
+        l += __shfl_xor_sync(0xffffffffu, l, off);
+        lr += __shfl_xor_sync(0xffffffffu, lr, off);
       }
-      for (int r = lane; r < nrec; r += 32)
-        coef[g * nrec + r] = M == -INFINITY ? 0.f : ex2(coef[g * nrec + r] - M);
+      for (int r = lane; r < nrec; r += 32) coef[g * nrec + r] = ex2(coef[g * nrec + r] - M);
       if (lane == 0) {
         st_lr[g] = lr;
         if (lse != nullptr && g < G) lse[g] = l != 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
       }
     }
     __syncthreads();
-#pragma unroll 1
-    for (int v = tid; v < S::kItems * S::kSplit; v += S::kThreads) {
-      const int q = v / S::kItems, it = v - q * S::kItems, h = W::frag_head(it >> 5, lane);
-      const float *cA = coef + h * nrec, *cB = cA + nrec;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int r = q; r < nrec; r += kAhead * S::kSplit) {
-        if (v != tid || r != q) fetch(it, r);
+    float4 a[S::kPer];
+    int head[S::kPer];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (r + u * S::kSplit < nrec) {
-            const float fA = cA[r + u * S::kSplit], fB = cB[r + u * S::kSplit];
-            a.x = fmaf(x[u].x, fA, a.x);
-            a.y = fmaf(x[u].y, fB, a.y);
-            a.z = fmaf(x[u].z, fA, a.z);
-            a.w = fmaf(x[u].w, fB, a.w);
+    for (int j = 0; j < S::kPer; ++j) {
+      a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      head[j] = W::frag_head((l0 + j * S::kLanes) >> 5, lane);
+    }
+#pragma unroll 1
+    for (int r0 = r_first; r0 < nrec; r0 += S::kDeep * S::kSplit) {
+      if (r0 != r_first)
+#pragma unroll
+        for (int u = 0; u < S::kDeep; ++u) fetch(u, r0 + u * S::kSplit);
+#pragma unroll
+      for (int u = 0; u < S::kDeep; ++u) {
+        const int r = r0 + u * S::kSplit;
+        if (r < nrec) {
+#pragma unroll
+          for (int j = 0; j < S::kPer; ++j) {
+            const float fA = coef[head[j] * nrec + r], fB = coef[(head[j] + 1) * nrec + r];
+            a[j].x = fmaf(x[u][j].x, fA, a[j].x);
+            a[j].y = fmaf(x[u][j].y, fB, a[j].y);
+            a[j].z = fmaf(x[u][j].z, fA, a[j].z);
+            a[j].w = fmaf(x[u][j].w, fB, a[j].w);
           }
         }
       }
-      if constexpr (S::kSplit == 1) {
-        const float lA = st_lr[h], lB = st_lr[h + 1];
-        W::put_out(out, it >> 5, lane, a, 1.f / lA, 1.f / lB);
-      } else {
-        sums[v] = a;
-      }
     }
-    if constexpr (S::kSplit == 2) {
+    if constexpr (S::kSplit == 1) {
+#pragma unroll
+      for (int j = 0; j < S::kPer; ++j)
+        W::put_out(out, (l0 + j * S::kLanes) >> 5, lane, a[j], 1.f / st_lr[head[j]], 1.f / st_lr[head[j] + 1]);
+    } else {
+      if (q < S::kSplit)
+#pragma unroll
+        for (int j = 0; j < S::kPer; ++j) sums[q * S::kItems + j * S::kLanes + l0] = a[j];
       __syncthreads();
       for (int v = tid; v < S::kItems; v += S::kThreads) {
-        const float4 a = sums[v], y = sums[S::kItems + v];
+        float4 y = sums[v];
+#pragma unroll
+        for (int k = 1; k < S::kSplit; ++k) {
+          const float4 z = sums[k * S::kItems + v];
+          y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+        }
         const int h = W::frag_head(v >> 5, lane);
-        const float lA = st_lr[h], lB = st_lr[h + 1];
-        W::put_out(out, v >> 5, lane, make_float4(a.x + y.x, a.y + y.y, a.z + y.z, a.w + y.w),
-                   1.f / lA, 1.f / lB);
+        W::put_out(out, v >> 5, lane, y, 1.f / st_lr[h], 1.f / st_lr[h + 1]);
       }
     }
     __syncthreads();  // the next pair overwrites the sums
