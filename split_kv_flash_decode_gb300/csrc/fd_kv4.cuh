@@ -471,8 +471,8 @@ struct Kv4Stream {
   static constexpr int kRecord = kHeads * (D + 4);  // floats: the fragments, then (m, l, l~, 0) per head
   // The combine: thread (q, l) takes the fragments l, l + kLanes, .. (kPer of them) of every kSplit-th
   // record from q on, sixteen loads at a time.  (G = 16, 21 records: 28 loads per thread, 1.4 us less
-  // than with one thread per fragment in two passes.  Each load sent off as soon as its register
-  // is free was slower, 128K tokens of G = 8 by 3.4 us: a warp can wait for six sets of loads only.)
+  // than with one thread per fragment in two passes.  A load issued as soon as its register is
+  // free, instead of sixteen together, was slower: 128K tokens of G = 8 by 3.4 us.)
   static constexpr int kLanes = kItems < (kThreads & -kThreads) ? kItems : (kThreads & -kThreads);
   static constexpr int kPer = kItems / kLanes;
   static constexpr int kSplit = kPer > 1 ? kThreads / kLanes : kThreads / kItems >= 2 ? 2 : 1;

@@ -26,7 +26,7 @@ constexpr int kMaxAxes = 4;
 constexpr int kMaxPairs = 64;
 constexpr double kMaxFreq = 1 << 20;
 // Warps that an append is split into while it has enough head rows: 16 on each of 152 SMs.  (2090
-// tokens of 40 head rows: 11.9 us with 16, 13.1 with 32, 14.0 with 64: a token's angles are computed
+// tokens of 40 head rows: 11.5 us with 16; 32 and 64 took 1.2 and 2.1 us more: a token's angles are computed
 // once per warp.)
 constexpr int64_t kAppendWarps = 16 * 152;
 
@@ -160,11 +160,13 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // rest.  Position x frequency is a 64-bit product of turns that wraps where whole turns drop out,
 // so no position is too far.
 //
-// Bound by HBM: 805 MB (32K tokens of 48 head rows) in 125 us, 6.4 TB/s.  It takes many warps to
-// keep enough loads in flight: with the registers of 5 blocks per SM (92) the same took 145 us, of
-// 8 (64) 125 us; 4-bit caches, whose quantisation needs the registers, are faster with 4.
+// Bound by HBM: 805 MB (32K tokens of 48 head rows) in 126 us, 6.4 TB/s; fewer tokens by the chain of
+// each warp's rows, so two rounds of rows are on their way ahead of the one at work (2090 tokens of 40
+// head rows: 11.5 us; with one round ahead 12.1).  Many warps keep the loads in flight: 7 blocks per
+// SM (72 registers) take 126 us for the 32K tokens, 6 take 131, 5 take 140 and 8, which spill, 129;
+// 4-bit caches, whose quantisation needs the registers, are faster with 4.
 template <typename T, int D, int KV>
-__global__ void __launch_bounds__(kRowsThreads, KV == kKvE2m1 ? 4 : 8) fd_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kRowsThreads, KV == kKvE2m1 ? 4 : 7) fd_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPH = D / 16;       // lanes per head row
   constexpr int HPW = 32 / LPH;     // head rows a warp handles at a time
   constexpr int OWN = 8 / HPW;      // angles a lane computes
@@ -186,10 +188,10 @@ __global__ void __launch_bounds__(kRowsThreads, KV == kKvE2m1 ? 4 : 8) fd_append
   const bool rotates = l < rl;
   const int ea = rotates ? 8 * l : p.rot + 8 * (l - rl);
   const int eb = rotates ? half + 8 * l : ((p.rot + D) >> 1) + 8 * (l - rl);
-  // The warp's first rows, on their way while the angles are computed.
+  // The warp's first rows, on their way while the angles are computed; m: those after them.
   const int first_kind = lo < Hq ? 0 : lo < Hq + Hk ? 1 : 2;
-  uint4 na, nb;
-  auto load = [&](const T* src, int64_t stride, int h, int last) {
+  uint4 na, nb, ma, mb;
+  auto load = [&](uint4& na, uint4& nb, const T* src, int64_t stride, int h, int last) {
     const T* at = src + (int64_t)min(h + sub, last - 1) * stride;  // rows past the end repeat the last one
     na = *reinterpret_cast<const uint4*>(at + ea);
     nb = *reinterpret_cast<const uint4*>(at + eb);
@@ -198,8 +200,10 @@ __global__ void __launch_bounds__(kRowsThreads, KV == kKvE2m1 ? 4 : 8) fd_append
     const int64_t* stride = first_kind == 0 ? p.q_stride : first_kind == 1 ? p.k_stride : p.v_stride;
     const void* in = first_kind == 0 ? p.q : first_kind == 1 ? p.k : p.v;
     const int before = first_kind == 0 ? 0 : first_kind == 1 ? Hq : Hq + Hk;
-    load(reinterpret_cast<const T*>(in) + (int64_t)t * stride[0], stride[1], lo - before,
-         min(hi - before, first_kind == 0 ? Hq : p.m.Hkv));
+    const T* src = reinterpret_cast<const T*>(in) + (int64_t)t * stride[0];
+    const int last = min(hi - before, first_kind == 0 ? Hq : p.m.Hkv);
+    load(na, nb, src, stride[1], lo - before, last);
+    load(ma, mb, src, stride[1], lo - before + HPW, last);
   }
   // Pair i of a lane: (ea + i, eb + i), or, interleaved, neighbours of run a (i < 4) or run b.
   float c[8], s[8];
@@ -233,7 +237,10 @@ __global__ void __launch_bounds__(kRowsThreads, KV == kKvE2m1 ? 4 : 8) fd_append
     const T* src = reinterpret_cast<const T*>(in) + (int64_t)t * stride[0];
     const uint4* wa = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + ea);
     const uint4* wb = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + eb);
-    if (kind != first_kind) load(src, stride[1], first, last);
+    if (kind != first_kind) {
+      load(na, nb, src, stride[1], first, last);
+      load(ma, mb, src, stride[1], first + HPW, last);
+    }
 #pragma unroll 1
     for (int h0 = first; h0 < last; h0 += HPW) {
       {
@@ -242,7 +249,9 @@ __global__ void __launch_bounds__(kRowsThreads, KV == kKvE2m1 ? 4 : 8) fd_append
         float a[8], x[8];
         dev::unpack8<T>(na, a);
         dev::unpack8<T>(nb, x);
-        if (h0 + HPW < last) load(src, stride[1], h0 + HPW, last);
+        na = ma;
+        nb = mb;
+        if (h0 + 2 * HPW < last) load(ma, mb, src, stride[1], h0 + 2 * HPW, last);
         if (kind < 2 && norm) {
           float ss = 0.f;
 #pragma unroll
