@@ -57,10 +57,10 @@ FD_HD constexpr int stream_warps(int G) { return G <= 8 ? 8 : 12; }
 FD_HD constexpr int stream_ctas(int G) { return G <= 8 ? 2 : 1; }
 constexpr int kStreamTile = 128;       // tokens that four warps take together
 constexpr int kStreamSlotTokens = 32;  // tokens of a ring slot, and of a warp's share of a tile
-// What a (sequence, KV head) pair costs a run beyond its tiles, in tiles.  (A ragged batch of 17, G =
-// 16: 39 us with 0, 19.4 with 2, 18.9 with 4, 17.4 with 6; 64 sequences of 8K: 99.7, 99.7, 100.3
-// with 2, 4, 6.)
-constexpr int kPairUnits = 6;
+// What a (sequence, KV head) pair costs a run beyond its tiles, in tiles.  (With 2, 4 and 6: a ragged
+// batch of 17, G = 16: 17.4, 15.0 and 15.4 us; 64 sequences of 8K tokens: 98.7, 98.6 and 99.4; geometric
+// mean over 45 batches of all kinds: 6.29, 6.25 and 6.25.)
+constexpr int kPairUnits = 4;
 // Host mode of the 4-bit stream kernel, and its largest grid.
 constexpr int kModeStream = 8;
 constexpr int kMaxStreamCtas = 320;
