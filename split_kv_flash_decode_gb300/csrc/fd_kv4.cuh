@@ -449,14 +449,14 @@ struct Kv4Warp {
 // CTA is written at once, else the CTA publishes a record and the last one to arrive at the pair's
 // counter combines them, in order.  No CTA waits for another.
 //
-// What bounds it: HBM for long sequences (64 sequences of 8K tokens, 604 MB, G = 4: 100 us, 6.05 TB/s
-// of the 6.8 TB/s that a copy reaches; 128K tokens, G = 8: 32.1 us for 151 MB).  The loads alone
+// What bounds it: HBM for long sequences (64 sequences of 8K tokens, 604 MB, G = 4: 98.6 us, 6.13 TB/s
+// of the 6.8 TB/s that a copy reaches; 128K tokens, G = 8: 31.9 us for 151 MB).  The loads alone
 // take 90 us there and the arithmetic alone 55 us (238 instructions per block and warp, 104 of
 // them on the half-rate ALU pipe), so a slot must not be held for longer than the loads of the
 // others take: a warp is done with its 32 tokens in about 2100 cycles; held for 3000, the loads alone
 // would take 115 us.  Rings shared by four warps and refilled by the last of them to finish ran at
 // 118 us, one CTA per partial (8192 short CTAs) at 212 us.  Short inputs are bound by latencies: one
-// 32K-token sequence (G = 4) takes 13.1 us for 38 MB, of which the first loads 2 us, the merge and the
+// 32K-token sequence (G = 4) takes 13.2 us for 38 MB, of which the first loads 2 us, the merge and the
 // arrival 2 us and the combine of 15 records 3 us.
 template <int D, int G>
 struct Kv4Stream {
