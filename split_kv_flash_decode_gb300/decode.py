@@ -65,7 +65,6 @@ class Decoder:
         self.Hq, self.Hkv, self.d, self.dtype = int(Hq), int(Hkv), int(d), dtype
         self.n_tokens = sum(self.seqlens)
         self.page_size = int(page_size)
-        self._q_shape = (self.Bsz, self.Hq, self.d)
         with torch.cuda.device(self.device):
             if self.page_size:
                 self.plan = B.fd_plan_paged(self.Bsz, Hq, Hkv, d, self.seqlens, W, self.page_size,
@@ -75,7 +74,12 @@ class Decoder:
                                       num_sms)
             self.workspace = torch.zeros(max(1, self.plan.workspace_bytes), dtype=torch.uint8,
                                          device=self.device)
-        self._lse_shape = (self.Bsz, self.Hq)
+        self._shapes()
+
+    def _shapes(self):
+        """What every call compares its tensors with."""
+        dtype = self.dtype
+        self._q_shape, self._lse_shape = (self.Bsz, self.Hq, self.d), (self.Bsz, self.Hq)
         self._t16, self._kv = _TORCH_DTYPE.get(dtype), _KV_DTYPE.get(dtype)
         self._decode, self._decode_paged = B.lib().fd_decode, B.lib().fd_decode_paged
         self._kv_shape = cache_shape(dtype, self.Hkv, self.d, self.seqlens)
@@ -105,19 +109,21 @@ class Decoder:
         q_ptr = self._check("q", q, self._q_shape, self._t16)
         if out is None:
             out = empty(stream, self._q_shape, self._t16, self.device)
+            out_ptr = out.data_ptr()
+        else:
+            out_ptr = self._check("out", out, self._q_shape, self._t16)
         if lse is None:
             lse = empty(stream, self._lse_shape, torch.float32, self.device)
-        rc = launch(self.device.index, stream, call, self.plan.handle, q_ptr, *kv, B._ptr(out), B._ptr(lse),
+            lse_ptr = lse.data_ptr()
+        else:
+            lse_ptr = self._check("lse", lse, self._lse_shape, torch.float32)
+        rc = launch(self.device.index, stream, call, self.plan.handle, q_ptr, *kv, out_ptr, lse_ptr,
                     self.workspace.data_ptr())
         if rc != B.FD_OK:
             raise B.FdError(rc, name)
         return out, lse
 
     def __call__(self, q, k, v, out=None, lse=None, stream=None):
-        if out is not None:
-            self._check("out", out, self._q_shape, self._t16)
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != self._lse_shape):
-            raise ValueError("lse must be float32 [B, Hq]")
         kv = (self._check("k", k, self._kv_shape, self._kv), self._check("v", v, self._kv_shape, self._kv))
         return self._run(self._decode, "fd_decode", q, kv, out, lse, stream)
 

@@ -1,0 +1,65 @@
+"""Host logic of Decoder (no GPU: what it would launch is recorded instead)."""
+import pytest
+import torch
+
+import split_kv_flash_decode_gb300 as fd
+from split_kv_flash_decode_gb300 import build
+from split_kv_flash_decode_gb300 import decode as decode_mod
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_lib():
+    build.build()
+    return fd.lib()
+
+
+class HostDecoder(fd.Decoder):
+    """A Decoder whose tensors lie in host memory."""
+
+    def __init__(self, seqlens, page_size=0, Hq=8, Hkv=2, d=64, dtype="f16"):
+        self.device = torch.device("cpu")
+        self.seqlens, self.Bsz, self.page_size = seqlens, len(seqlens), page_size
+        self.Hq, self.Hkv, self.d, self.dtype = Hq, Hkv, d, dtype
+        args = (self.Bsz, Hq, Hkv, d, seqlens, 1)
+        self.plan = fd.fd_plan_paged(*args, page_size, dtype, num_sms=152) if page_size else \
+            fd.fd_plan(*args, dtype, num_sms=152)
+        self.workspace = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8)
+        self._shapes()
+
+
+@pytest.fixture
+def launched(monkeypatch):
+    calls = []
+
+    def record(index, stream, call, *args):
+        calls.append(args)
+        return fd.FD_OK
+    monkeypatch.setattr(decode_mod, "launch", record)
+    return calls
+
+
+@pytest.mark.parametrize("page_size", [0, 16])
+def test_outputs_of_the_caller_are_checked(launched, page_size):
+    """out and lse reach the kernel as addresses: only whole tensors of its types on its device do."""
+    dec = HostDecoder([20, 3], page_size)
+    q = torch.zeros(2, 8, 64, dtype=torch.float16)
+    kv = torch.zeros((4, 16, 2, 64) if page_size else (23, 2, 64), dtype=torch.float16)
+    table = torch.zeros(2, 2, dtype=torch.int32)
+
+    def run(**kw):
+        return dec.decode_paged(q, kv, kv, table, **kw) if page_size else dec(q, kv, kv, **kw)
+
+    out, lse = torch.empty_like(q), torch.empty(2, 8)
+    got = run(out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    assert launched[-1][-3:] == (out.data_ptr(), lse.data_ptr(), dec.workspace.data_ptr())
+    assert len(launched) == 1
+    for bad in (dict(out=out[:1]), dict(out=out.bfloat16()), dict(out=out[..., :32]), dict(out=out.to("meta")),
+                dict(out=torch.empty(2, 64, 8, dtype=torch.float16).transpose(1, 2)), dict(out=out.view(16, 64)),
+                dict(lse=lse[:1]), dict(lse=lse.half()), dict(lse=lse.to("meta")), dict(lse=torch.empty(8, 2).T),
+                dict(lse=torch.empty(2, 1).expand(2, 8)), dict(lse=lse.double())):
+        with pytest.raises(ValueError):
+            run(**bad)
+    assert len(launched) == 1
+    out, lse = run()
+    assert out.shape == (2, 8, 64) and out.dtype == torch.float16 and lse.shape == (2, 8) and lse.dtype == torch.float32
