@@ -5,6 +5,8 @@ of compute happens in fd_decode's kernel.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _binding as B
@@ -21,23 +23,34 @@ _device_now = getattr(torch._C, "_cuda_getDevice", None)  # missing in builds wi
 _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def launch(index, stream, call, *args):
-    """call(*args, stream) with device `index` current; None is that device's current stream."""
-    address = _stream_now(index) if stream is None else B._stream(stream)
+def stream_address(index, stream):
+    """Raw stream of a torch.cuda.Stream or address; None is the current stream of device `index`."""
+    return _stream_now(index) if stream is None else B._stream(stream)
+
+
+def launch(index, address, call, *args):
+    """call(*args, address) with device `index` current."""
     if _device_now() == index:
         return call(*args, address)
     with torch.cuda.device(index):
         return call(*args, address)
 
 
-def empty(stream, shape, dtype, device):
-    """torch.empty from the memory pool of the stream that will write it: memory just freed on the
-    current stream may still be in use there."""
+def on_stream(stream, device):
+    """Context in which allocations come from the pool of `stream` (None: the current one), in whose
+    order they are used: memory just freed on another stream may still be in use there."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return contextlib.nullcontext()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    return torch.cuda.stream(stream)
+
+
+def empty(stream, shape, dtype, device):
+    """torch.empty from the pool of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with on_stream(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -51,7 +64,14 @@ def cache_shape(dtype, Hkv, d, seqlens=None, num_pages=None, page_size=0):
 
 
 class Decoder:
-    """Plan + zeroed workspace for one decode shape on one device."""
+    """Plan and zeroed workspaces for one decode shape on one device.
+
+    Every stream that a call runs on has a workspace of its own, allocated and zeroed in that
+    stream's order (``workspace`` is the one of the stream that was current at construction).  A
+    captured call allocates none: it takes its stream's, or else the first.  Replays of such
+    graphs, and calls on the streams whose workspace they took, must not overlap, and the Decoder
+    outlives the graphs.
+    """
 
     def __init__(self, Hq, Hkv, d, seqlens, W, dtype="f16", flags=0, chunks=0, device=None,
                  num_sms=0, page_size=0):
@@ -72,9 +92,25 @@ class Decoder:
             else:
                 self.plan = B.fd_plan(self.Bsz, Hq, Hkv, d, self.seqlens, W, dtype, flags, chunks,
                                       num_sms)
-            self.workspace = torch.zeros(max(1, self.plan.workspace_bytes), dtype=torch.uint8,
-                                         device=self.device)
+            self.workspace = self._zeros()
+            self._home = stream_address(self.device.index, None)
+        self._others = {}  # workspaces of other streams, by address
         self._shapes()
+
+    def _zeros(self):
+        return torch.zeros(max(1, self.plan.workspace_bytes), dtype=torch.uint8, device=self.device)
+
+    def _workspace(self, address):
+        """The workspace of the stream at this address."""
+        if address == self._home:
+            return self.workspace
+        ws = self._others.get(address)
+        if ws is None:
+            with on_stream(address, self.device):
+                if torch.cuda.is_current_stream_capturing():
+                    return self.workspace
+                ws = self._others[address] = self._zeros()
+        return ws
 
     def _shapes(self):
         """What every call compares its tensors with."""
@@ -117,8 +153,10 @@ class Decoder:
             lse_ptr = lse.data_ptr()
         else:
             lse_ptr = self._check("lse", lse, self._lse_shape, torch.float32)
-        rc = launch(self.device.index, stream, call, self.plan.handle, q_ptr, *kv, out_ptr, lse_ptr,
-                    self.workspace.data_ptr())
+        index = self.device.index
+        address = stream_address(index, stream)
+        rc = launch(index, address, call, self.plan.handle, q_ptr, *kv, out_ptr, lse_ptr,
+                    self._workspace(address).data_ptr())
         if rc != B.FD_OK:
             raise B.FdError(rc, name)
         return out, lse
@@ -143,8 +181,13 @@ class Decoder:
         return self._run(self._decode_paged, "fd_decode_paged", q, kv, out, lse, stream)
 
     def status(self, stream=None) -> int:
+        """fd_workspace_status of this Decoder's decodes: synchronises `stream` (None: the current
+        one), or the device where calls ran on several streams."""
         with torch.cuda.device(self.device):
-            return B.fd_workspace_status(self.plan, self.workspace, stream)
+            if self._others:
+                torch.cuda.synchronize()
+            found = [B.fd_workspace_status(self.plan, ws, stream) for ws in (self.workspace, *self._others.values())]
+        return next((x for x in found if x != B.FD_OK), B.FD_OK)
 
 
 def flash_decode(q, k, v, seqlens, W, flags=0, chunks=0):

@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _binding as B
-from .decode import _KV_DTYPE, _TORCH_DTYPE, cache_shape, empty, launch
+from .decode import _KV_DTYPE, _TORCH_DTYPE, cache_shape, empty, launch, stream_address
 
 
 class Rope:
@@ -162,7 +162,8 @@ class KVRows:
             q_w, k_w, eps, weight_offset, rope_ptr, pos, pos_stride, q_to, k_to, cache[0], cache[1],
             k_mul, v_mul, cache[2], cache[4], cache[3], self._status(status))
         if self.tokens:  # no rows: empty tensors have null addresses
-            rc = launch(self.device.index, stream, self._append, self.rows.handle, args)
+            index = self.device.index
+            rc = launch(index, stream_address(index, stream), self._append, self.rows.handle, args)
             if rc != B.FD_OK:
                 raise B.FdError(rc, "fd_append")
         return q_out
@@ -182,7 +183,8 @@ class KVRows:
         else:
             v_to = self._whole("v_out", v_out, self._k_shape, self._t16)
         if self.tokens:
-            rc = launch(self.device.index, stream, self._gather, self.rows.handle, *cache, k_to, v_to,
+            index = self.device.index
+            rc = launch(index, stream_address(index, stream), self._gather, self.rows.handle, *cache, k_to, v_to,
                         self._status(status))
             if rc != B.FD_OK:
                 raise B.FdError(rc, "fd_gather")

@@ -1,4 +1,6 @@
 """Host logic of Decoder (no GPU: what it would launch is recorded instead)."""
+import contextlib
+
 import pytest
 import torch
 
@@ -23,18 +25,22 @@ class HostDecoder(fd.Decoder):
         args = (self.Bsz, Hq, Hkv, d, seqlens, 1)
         self.plan = fd.fd_plan_paged(*args, page_size, dtype, num_sms=152) if page_size else \
             fd.fd_plan(*args, dtype, num_sms=152)
-        self.workspace = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8)
+        self.workspace, self._home, self._others = self._zeros(), 0, {}
         self._shapes()
 
 
 @pytest.fixture
 def launched(monkeypatch):
+    """The arguments of every call that would have been made; streams are addresses (0: the current)."""
     calls = []
 
-    def record(index, stream, call, *args):
+    def record(index, address, call, *args):
         calls.append(args)
         return fd.FD_OK
     monkeypatch.setattr(decode_mod, "launch", record)
+    monkeypatch.setattr(decode_mod, "stream_address", lambda index, stream: stream or 0)
+    monkeypatch.setattr(decode_mod, "on_stream", lambda stream, device: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return calls
 
 
@@ -63,3 +69,25 @@ def test_outputs_of_the_caller_are_checked(launched, page_size):
     assert len(launched) == 1
     out, lse = run()
     assert out.shape == (2, 8, 64) and out.dtype == torch.float16 and lse.shape == (2, 8) and lse.dtype == torch.float32
+
+
+def test_every_stream_has_its_own_workspace(launched, monkeypatch):
+    """One workspace a stream, kept for its later calls; captured calls take what is there."""
+    dec = HostDecoder([20, 3])
+    q, kv = torch.zeros(2, 8, 64, dtype=torch.float16), torch.zeros(23, 2, 64, dtype=torch.float16)
+
+    def used(stream):
+        dec(q, kv, kv, stream=stream)
+        return launched[-1][-1]
+
+    first = dec.workspace.data_ptr()
+    assert used(None) == first
+    side, other = used(256), used(512)
+    assert len({first, side, other}) == 3
+    assert used(256) == side and used(512) == other and used(None) == first
+    for ws in dec._others.values():
+        assert ws.shape == dec.workspace.shape and not ws.any()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    assert used(768) == first and used(256) == side
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    assert used(768) not in (first, side, other)
