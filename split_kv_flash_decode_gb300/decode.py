@@ -24,7 +24,7 @@ _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def stream_address(index, stream):
-    """Raw stream of a torch.cuda.Stream or address; None is the current stream of device `index`."""
+    """Raw stream of an address or of anything with a cuda_stream; None is the current stream of device `index`."""
     return _stream_now(index) if stream is None else B._stream(stream)
 
 
@@ -41,8 +41,9 @@ def on_stream(stream, device):
     order they are used: memory just freed on another stream may still be in use there."""
     if stream is None:
         return contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        address = B._stream(stream)
+        stream = torch.cuda.ExternalStream(address, device) if address else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 

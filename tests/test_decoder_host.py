@@ -91,3 +91,19 @@ def test_every_stream_has_its_own_workspace(launched, monkeypatch):
     assert used(768) == first and used(256) == side
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     assert used(768) not in (first, side, other)
+
+
+def test_streams_of_other_libraries(monkeypatch):
+    """Anything with a cuda_stream is a stream: its address is what counts."""
+    class Stream:
+        cuda_stream = 4096
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda address, device: seen.append(address) or "external")
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: seen.append(stream) or contextlib.nullcontext())
+    with decode_mod.on_stream(Stream(), torch.device("cuda", 0)):
+        pass
+    with decode_mod.on_stream(4096, torch.device("cuda", 0)):
+        pass
+    assert seen == [4096, "external"] * 2
+    assert decode_mod.stream_address(0, Stream()) == 4096
