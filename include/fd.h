@@ -443,8 +443,9 @@ typedef struct fd_append_args {
  * values by a weight of 0; a new pool is cleared once (cudaMemset), so that they are finite.  Over a
  * 4-bit cache they may hold anything.
  *
- * FD_ERR_INVALID: a missing pointer, a negative stride, an output (caches included) that overlaps
- * an input or another output (but for the in-place case), bt_stride < ceil(L_b / page_size), a bad
+ * FD_ERR_INVALID: a missing pointer, a negative stride, an output (caches and status included) that
+ * overlaps an input (weights, positions and block table included) or another output (but for the
+ * in-place case), bt_stride < ceil(L_b / page_size), a bad
  * rope or factor.
  * FD_ERR_ALIGN: a device pointer not 16-byte aligned (positions, block_table, status: 4) or a
  * stride not a multiple of 8.  FD_ERR_UNSUPPORTED: rot_dim, num_pages * page_size >= 2^31.
@@ -459,7 +460,7 @@ int fd_append(fd_rows_t rows, const fd_append_args* args, cudaStream_t stream);
  *
  *   k_cache, v_cache, num_pages, block_table, bt_stride, status   as for fd_append
  *   k_out, v_out   device [T, Hkv, d] in the q type, contiguous, overlapping neither each other
- *                  nor the caches (FD_ERR_INVALID)
+ *                  nor the caches, the block table or status (FD_ERR_INVALID)
  *
  * A row whose page index lies outside [0, num_pages) reads zeros.  Errors as for fd_append.
  */

@@ -536,6 +536,8 @@ bool overlap(const Span& a, const Span& b) { return a.n > 0 && b.n > 0 && a.at <
 int64_t cache_span(const fd_rows_s* r, int num_pages) {
   return r->page_size ? (int64_t)num_pages * r->cache_bytes : r->cache_bytes;
 }
+// Bytes of the page table that a call may read.
+int64_t table_bytes(const fd_rows_s* r, int64_t bt_stride) { return 4 * ((r->B - 1) * bt_stride + r->max_pages); }
 bool in_place(const void* out, const void* in, const int64_t* stride, int64_t T, int H, int d) {
   return out == in && (stride[1] == d || H == 1) && (stride[0] == (int64_t)H * d || T == 1);
 }
@@ -653,13 +655,22 @@ int fd_append(fd_rows_t rows, const fd_append_args* a, cudaStream_t stream) {
   if (T == 0) return FD_OK;
   const int heads[3] = {r->Hq, r->Hkv, r->Hkv};
   const int64_t cache = a->k_cache ? fd::cache_span(r, a->num_pages) : 0;
-  const fd::Span outs[4] = {fd::span(a->q_out, 2 * T * r->Hq * d), fd::span(a->k_out, 2 * T * r->Hkv * d),
-                            fd::span(a->k_cache, cache), fd::span(a->v_cache, cache)};
-  for (int o = 0; o < 4; ++o) {
-    for (int i = 0; i < 3; ++i) {
+  const int64_t axes = p.rot > 0 && a->positions ? a->rope->num_axes : 0;
+  const fd::Span outs[5] = {fd::span(a->q_out, 2 * T * r->Hq * d), fd::span(a->k_out, 2 * T * r->Hkv * d),
+                            fd::span(a->k_cache, cache), fd::span(a->v_cache, cache),
+                            fd::span(a->k_cache ? a->status : nullptr, 4)};
+  // q, k and v first.
+  const fd::Span reads[7] = {fd::input_span(a->q, a->q_stride, T, r->Hq, d), fd::input_span(a->k, a->k_stride, T, r->Hkv, d),
+                             fd::input_span(a->v, a->v_stride, T, r->Hkv, d),
+                             fd::span(a->q_norm ? a->q_weight : nullptr, 2 * d),
+                             fd::span(a->k_norm ? a->k_weight : nullptr, 2 * d),
+                             fd::span(axes ? a->positions : nullptr, 4 * ((axes - 1) * a->pos_stride + T)),
+                             fd::span(p.m.block_table, fd::table_bytes(r, a->bt_stride))};
+  for (int o = 0; o < 5; ++o) {
+    for (int i = 0; i < 7; ++i) {
       // q_out may be q and k_out k, element for element.
       if (o == i && o < 2 && fd::in_place(o ? a->k_out : a->q_out, ins[i], strides[i], T, heads[i], d)) continue;
-      if (ins[i] && fd::overlap(outs[o], fd::input_span(ins[i], strides[i], T, heads[i], d))) return FD_ERR_INVALID;
+      if (fd::overlap(outs[o], reads[i])) return FD_ERR_INVALID;
     }
     for (int k = 0; k < o; ++k)
       if (fd::overlap(outs[o], outs[k])) return FD_ERR_INVALID;
@@ -698,10 +709,15 @@ int fd_gather(fd_rows_t rows, const void* k_cache, const void* v_cache, int num_
   if (rc != FD_OK) return rc;
   if (rows->T == 0) return FD_OK;
   const int64_t cache = fd::cache_span(rows, num_pages), bytes = 2 * rows->T * rows->Hkv * rows->d;
-  const fd::Span outs[2] = {fd::span(k_out, bytes), fd::span(v_out, bytes)};
-  for (const fd::Span& o : outs)
-    if (fd::overlap(o, fd::span(k_cache, cache)) || fd::overlap(o, fd::span(v_cache, cache))) return FD_ERR_INVALID;
-  if (fd::overlap(outs[0], outs[1])) return FD_ERR_INVALID;
+  const fd::Span outs[3] = {fd::span(k_out, bytes), fd::span(v_out, bytes), fd::span(status, 4)};
+  const fd::Span reads[3] = {fd::span(k_cache, cache), fd::span(v_cache, cache),
+                             fd::span(block_table, fd::table_bytes(rows, bt_stride))};
+  for (int o = 0; o < 3; ++o) {
+    for (const fd::Span& in : reads)
+      if (fd::overlap(outs[o], in)) return FD_ERR_INVALID;
+    for (int k = 0; k < o; ++k)
+      if (fd::overlap(outs[o], outs[k])) return FD_ERR_INVALID;
+  }
   p.k_cache = k_cache; p.v_cache = v_cache;
   p.k_out = k_out; p.v_out = v_out;
   p.T = (int32_t)rows->T;
