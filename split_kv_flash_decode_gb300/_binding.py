@@ -200,11 +200,10 @@ def _check(rc: int, where: str) -> None:
 
 
 def _i32_array(values, n: int):
-    arr = (ctypes.c_int32 * n)()
-    vals = list(values)
-    for i in range(n):
-        arr[i] = int(vals[i])
-    return arr
+    try:
+        return (ctypes.c_int32 * n).from_buffer_copy(struct.pack(f"{n}i", *map(int, values)))
+    except struct.error:  # ctypes would wrap what does not fit
+        raise FdError(FD_ERR_INVALID, "a length outside int32") from None
 
 
 def _ptr(t) -> int:

@@ -107,3 +107,17 @@ def test_streams_of_other_libraries(monkeypatch):
         pass
     assert seen == [4096, "external"] * 2
     assert decode_mod.stream_address(0, Stream()) == 4096
+
+
+def test_lengths_past_32_bits_are_refused():
+    """Host lengths become int32: one that does not fit is an error, not another length."""
+    for bad in ([2 ** 32 + 5], [2 ** 31], [-2 ** 32 + 1]):
+        for call in (lambda: fd.fd_plan(1, 8, 8, 128, bad, 1, "f16", num_sms=152),
+                     lambda: fd.fd_plan(1, 8, 8, 128, [10], bad, "f16", num_sms=152),
+                     lambda: fd.fd_plan_paged(1, 8, 8, 128, bad, 1, 16, "f16", num_sms=152),
+                     lambda: fd.fd_rows_plan(1, 8, 8, 128, bad, [0], [1], 0, "f16"),
+                     lambda: fd.fd_rows_plan(1, 8, 8, 128, [10], bad, [1], 0, "f16"),
+                     lambda: fd.fd_rows_plan(1, 8, 8, 128, [10], [0], bad, 0, "f16")):
+            with pytest.raises(fd.FdError) as e:
+                call()
+            assert e.value.status == fd.FD_ERR_INVALID
