@@ -438,10 +438,8 @@ typedef struct fd_append_args {
  * there, in pieces of 4 bytes or more.  A row whose page index lies outside [0, num_pages) is not
  * stored in the cache (q_out and k_out are).  T = 0 launches nothing.
  *
- * Before a cache's first decode: fd_decode over a 16-bit or E4M3 cache also reads the rows behind
- * a sequence's last token up to the end of its 32-, 64- or 128-token tile, and multiplies their
- * values by a weight of 0; a new pool is cleared once (cudaMemset), so that they are finite.  Over a
- * 4-bit cache they may hold anything.
+ * Rows behind a sequence's last token (of the next sequence, of a page's earlier owner, never written)
+ * may hold anything: no decode lets them into a result.
  *
  * FD_ERR_INVALID: a missing pointer, a negative stride, an output (caches and status included) that
  * overlaps an input (weights, positions and block table included) or another output (but for the

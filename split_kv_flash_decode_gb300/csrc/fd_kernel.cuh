@@ -1077,6 +1077,24 @@ __device__ __forceinline__ void finish_cta(const Params& p, const Work& wk, floa
 namespace fd {
 namespace dev {
 
+// Rows [first, first + ROWS) of a V tile in the ring, of NBOX boxes of TILE 128-byte rows: those from
+// `ntok` on become zero.  They are no tokens of this CTA (the next sequence's, an earlier owner's of the
+// page) and their weights are 0, but 0 times a NaN or an infinity would be NaN.  One warp, which syncs
+// before it reads them; only in a CTA's last tile, so no load overwrites them.
+template <int ROWS, int NBOX, int TILE>
+__device__ __forceinline__ void clear_rows(uint32_t v, int first, int ntok) {
+  int lane;  // read here: nothing of this is worth a register in the loop around it
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+  const int row = first + (lane >> 3);
+  const uint32_t at = v + row * 128 + (lane & 7) * 16;
+#pragma unroll
+  for (int j = 0; j < ROWS; j += 4)
+    if (row + j >= ntok)
+#pragma unroll
+      for (int bx = 0; bx < NBOX; ++bx)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + (bx * TILE + j) * 128), "r"(0) : "memory");
+}
+
 // MODE 0: fused split + last-arriver combine.  MODE 1: split only (partials).
 // MODE 3: fused split + fine-grained waits.  MODE 4 / 5: MODE 0 / 1 with each
 // segment's chunk partials merged inside a thread-block cluster (rps == 1).
@@ -1439,6 +1457,13 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
           *reinterpret_cast<uint4*>(lrow + ((sw ^ 1) << 4)) = make_uint4(pl[4], pl[5], pl[6], pl[7]);
         }
       }
+      if (ntok < TILE) {
+        // The last tile: V rows past the end become zero (see clear_rows), once they have landed.
+        const int jl = kt * 2 + 1, s = jl % NSLOT;
+        if (mbar_wait(full_bar(s), (jl / NSLOT) & 1))
+          clear_rows<32, NBOX, TILE>(smem_addr(smem + (size_t)s * kSlotBytes), warp * 32, ntok);
+        __syncwarp();
+      }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       tc::named_sync(1, 4 * 32);
@@ -1655,6 +1680,11 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
             const int r = tb + 2 * t + (i & 1) + 8 * (i >> 1);
             vw[i] = *reinterpret_cast<const uint4*>(vslot + r * 128 + ((g ^ (r & 7)) << 4));
           }
+          if (ntok < tok0 + 16 * SUB) {  // rows past the end: zero (see clear_rows)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (tb + 2 * t + (i & 1) + 8 * (i >> 1) >= ntok) vw[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
 #pragma unroll
           for (int mi = 0; mi < KT; ++mi) {
             const int wi = mi >> 1;
@@ -1799,6 +1829,7 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
       if (tok0 < ntok) {
         const uint32_t kbase = smem_addr(smem + (size_t)s * kSlotBytes);
         const uint32_t vbase = kbase + kRowsBytes;
+        if (ntok < tok0 + 16) clear_rows<16, NBOX, TILE>(vbase, tok0, ntok);
         // Two accumulators (even and odd k-steps) halve the chain of dependent mma.
         float sc[NT][4], sd[NT][4];
 #pragma unroll
@@ -1871,6 +1902,7 @@ __global__ void __launch_bounds__(kThreads, CPS) fd_split_kernel(const __grid_co
           pb0[nt] = movmatrix_trans(r0);
           pb1[nt] = movmatrix_trans(r1);
         }
+        __syncwarp();
 #pragma unroll
         for (int mi = 0; mi < KT; ++mi) {
           uint32_t a[4];
