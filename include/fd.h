@@ -85,6 +85,9 @@ enum fd_dtype {
  * result does not depend on it).  Explicit chunks, or one of the flags LITERAL_W, TWO_LAUNCH,
  * WAITS, CLUSTER, NO_CLUSTER, CLUSTER_COMBINE, COMBINERS_n and TEST_DROP_ARRIVAL, gives the
  * W * C partials of the other dtypes.
+ *
+ * Over a 4-bit cache a score that overflows fp32 to -inf has no weight, and a sequence whose scores all
+ * do is like one without tokens: out 0, lse -inf.
  */
 
 enum fd_status {

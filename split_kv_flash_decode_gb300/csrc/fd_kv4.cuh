@@ -507,6 +507,10 @@ __device__ __forceinline__ void stream_merge(float& M, float& l, float& lr, floa
   }
 }
 
+// What out is multiplied by for a sum of weights: 0 where no token has any (none there, or all scores
+// -inf), so that out is 0; a NaN stays.
+__device__ __forceinline__ float stream_inverse(float l) { return l != 0.f ? 1.f / l : 0.f; }
+
 // First unit of CTA c's run: run_len or run_len + 1 of them each.
 __device__ __forceinline__ int stream_begin(const Params& p, int c) {
   return c * p.run_len + min(c, p.run_extra);
@@ -768,9 +772,7 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
         const int h = W::frag_head(v >> 5, lane);
         const float lA = aborted ? 0.f : W::template head_sum<NW>(st_lr, h);
         const float lB = aborted ? 0.f : W::template head_sum<NW>(st_lr, h + 1);
-        // No token: out = 0.  Tokens without any weight, or with a NaN: NaN.
-        const bool any = done.len > 0 && !aborted;
-        W::put_out(out, v >> 5, lane, a, any ? 1.f / lA : 0.f, any ? 1.f / lB : 0.f);
+        W::put_out(out, v >> 5, lane, a, stream_inverse(lA), stream_inverse(lB));
       } else {
         __stcg(reinterpret_cast<float4*>(rec) + v, a);
       }
@@ -905,7 +907,8 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
     if constexpr (S::kSplit == 1) {
 #pragma unroll
       for (int j = 0; j < S::kPer; ++j)
-        W::put_out(out, (l0 + j * S::kLanes) >> 5, lane, a[j], 1.f / st_lr[head[j]], 1.f / st_lr[head[j] + 1]);
+        W::put_out(out, (l0 + j * S::kLanes) >> 5, lane, a[j], stream_inverse(st_lr[head[j]]),
+                   stream_inverse(st_lr[head[j] + 1]));
     } else {
       if (q < S::kSplit)
 #pragma unroll
@@ -919,7 +922,7 @@ __global__ void __launch_bounds__((Kv4Stream<D, G>::kThreads), (Kv4Stream<D, G>:
           y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
         }
         const int h = W::frag_head(v >> 5, lane);
-        W::put_out(out, v >> 5, lane, y, 1.f / st_lr[h], 1.f / st_lr[h + 1]);
+        W::put_out(out, v >> 5, lane, y, stream_inverse(st_lr[h]), stream_inverse(st_lr[h + 1]));
       }
     }
     __syncthreads();  // the next pair overwrites the sums
