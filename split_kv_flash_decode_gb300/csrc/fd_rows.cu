@@ -163,7 +163,8 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // Bound by HBM: 805 MB (32K tokens of 48 head rows) in 126 us, 6.4 TB/s; fewer tokens by the chain of
 // each warp's rows, so two rounds of rows are on their way ahead of the one at work (2090 tokens of 40
 // head rows: 11.5 us; with one round ahead 12.1).  Many warps keep the loads in flight: 7 blocks per
-// SM (72 registers) take 126 us for the 32K tokens, 6 take 131, 5 take 140 and 8, which spill, 129;
+// SM (72 registers, and 16 bytes a thread that 16-bit caches spill) take 126 us for the 32K tokens,
+// 6 take 131, 5 take 140 and 8, which spill more, 129;
 // 4-bit caches, whose quantisation needs the registers, are faster with 4.
 template <typename T, int D, int KV>
 __global__ void __launch_bounds__(kRowsThreads, KV == kKvE2m1 ? 4 : 7) fd_append_kernel(const __grid_constant__ AppendParams p) {
