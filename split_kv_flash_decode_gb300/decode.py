@@ -69,9 +69,9 @@ class Decoder:
 
     Every stream that a call runs on has a workspace of its own, allocated and zeroed in that
     stream's order (``workspace`` is the one of the stream that was current at construction).  A
-    captured call allocates none: it takes its stream's, or else the first.  Replays of such
-    graphs, and calls on the streams whose workspace they took, must not overlap, and the Decoder
-    outlives the graphs.
+    captured call allocates none: it takes its stream's, or else the first, whose zeroing has to be
+    over when the capture begins (torch.cuda.graph waits for it).  Replays of such graphs, and calls
+    on the streams whose workspace they took, must not overlap, and the Decoder outlives the graphs.
     """
 
     def __init__(self, Hq, Hkv, d, seqlens, W, dtype="f16", flags=0, chunks=0, device=None,
