@@ -43,7 +43,8 @@ def on_stream(stream, device):
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         address = B._stream(stream)
-        stream = torch.cuda.ExternalStream(address, device) if address else torch.cuda.default_stream(device)
+        # 1 is the runtime's handle of the default stream, which torch would read as an id of its own.
+        stream = torch.cuda.ExternalStream(address, device) if address > 1 else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 

@@ -121,3 +121,13 @@ def test_lengths_past_32_bits_are_refused():
             with pytest.raises(fd.FdError) as e:
                 call()
             assert e.value.status == fd.FD_ERR_INVALID
+
+
+def test_both_handles_of_the_default_stream(monkeypatch):
+    """0 and 1 (the runtime's own handle) are the default stream; torch takes 1 for one of its pool."""
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda address, device: pytest.fail("external"))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: "default")
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext(stream))
+    for handle in (0, 1):
+        with decode_mod.on_stream(handle, torch.device("cuda", 0)) as stream:
+            assert stream == "default"
