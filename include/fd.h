@@ -472,6 +472,144 @@ int fd_gather(fd_rows_t rows, const void* k_cache, const void* v_cache, int num_
               const int32_t* block_table, int bt_stride, void* k_out, void* v_out,
               uint32_t* status, cudaStream_t stream);
 
+/*
+ * A step of speculative decoding: drafted tokens of every sequence, a chain or a tree, are attended
+ * over the cache at once (fd_tree_decode), judged (fd_tree_verify), and those that stand are moved
+ * together in the cache (fd_tree_keep).
+ *
+ * The n_b drafted tokens of sequence b are the last n_b of its L_b cache rows (fd_append writes them,
+ * at the positions that their depths give).  Token t of a call (0 <= t < T = sum_b n_b) is the t-th
+ * drafted token, sequence by sequence; node i of a sequence is its i-th.
+ *
+ * fd_tree_plan -- plan a step (host only; no CUDA call unless num_sms == 0).
+ *
+ *   B, Hq, Hkv, d, dtype   as for fd_plan, with any group Hq / Hkv and with d = 64 as well for
+ *                          FD_F16_E4M3KV
+ *   seqlens    host array [B]: the lengths L_b that the cache is laid out for, the drafted tokens included
+ *   drafts     host array [B]: 0 <= n_b <= min(L_b, FD_MAX_DRAFTS)
+ *   page_size  0: contiguous cache (rows packed as for fd_decode); else as fd_plan_paged
+ *   num_sms    SM count to plan for; 0 = query the current device
+ *   out_tree   receives the handle; release it with fd_tree_destroy
+ *
+ * The handle is immutable, owns host memory only and may be shared by threads.
+ */
+#define FD_MAX_DRAFTS 64 /* drafted tokens of a sequence */
+
+typedef struct fd_tree_s* fd_tree_t;
+
+int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32_t* drafts,
+                 int page_size, int dtype, int num_sms, fd_tree_t* out_tree);
+
+/* Release a handle (NULL is accepted).  No CUDA call. */
+int fd_tree_destroy(fd_tree_t tree);
+
+typedef struct fd_tree_info {
+  int64_t tokens;           /* T */
+  int32_t max_drafts;       /* max_b n_b */
+  int32_t ctas;             /* CTAs that fd_tree_decode streams the cache with */
+  uint64_t workspace_bytes; /* of fd_tree_decode */
+  uint64_t kv_bytes;        /* bytes of K and V of the sequences that have drafted tokens */
+} fd_tree_info;
+
+int fd_tree_get_info(fd_tree_t tree, fd_tree_info* info);
+
+/* Bits of a tree call's status word: set (never cleared) by the kernels, so the word may serve many
+ * calls. */
+#define FD_TREE_BAD_PAGE 1u  /* fd_tree_keep: a page index outside the pool */
+#define FD_TREE_BAD_PATH 2u  /* fd_tree_keep: a path that does not ascend within its sequence */
+#define FD_TREE_TIMEOUT 4u   /* fd_tree_decode: a bounded in-kernel wait gave up; out and lse are unusable */
+
+/*
+ * fd_tree_decode -- attention of the drafted tokens over the cache (one launch, or two: partial
+ * results of sequences that several CTAs share are combined by the second).
+ *
+ *   q          device [T, Hq, d] in the q type, contiguous
+ *   k, v, num_pages, block_table, bt_stride   the cache, as for fd_gather
+ *   mask       device uint64 [T]: bit j of a token's mask is set where node j of its sequence is
+ *              visible to it (its own bit is not implied; bits past n_b do not matter); NULL: a chain,
+ *              each token sees itself and the nodes before it.  The L_b - n_b rows before the drafted
+ *              ones are visible to all.
+ *   out        device [T, Hq, d] in the q type, written; lse device [T, Hq] float, written, may be NULL
+ *   workspace  device, fd_tree_info.workspace_bytes bytes (NULL where that is 0), in any state; calls
+ *              that overlap in time need workspaces of their own
+ *   status     device word or NULL
+ *
+ * out = sum_j softmax(s)_j V_j over the visible rows j, s_j = <q, K_j> / sqrt(d), lse = ln sum_j exp(s_j);
+ * a token that sees no row has out = 0 and lse = -inf.  Scores, softmax statistics and sums are fp32.
+ * Softmax weights enter the product with V with fp16's 11 significant bits, over a bf16 cache with 16.
+ * Rows that no token of a sequence sees (behind its last row, of nodes in no mask) may hold anything; a row
+ * that only some tokens see must be finite in V.  Page indices outside the pool read zeros.
+ *
+ * All pointers 16-byte aligned (mask: 8; block_table, status: 4), else FD_ERR_ALIGN.  FD_ERR_INVALID: a
+ * missing pointer, bt_stride < ceil(L_b / page_size), an output, workspace or status that overlaps an
+ * input or another of them.  T = 0 launches nothing.  Asynchronous; launched with programmatic
+ * dependent launch like fd_decode.
+ */
+int fd_tree_decode(fd_tree_t tree, const void* q, const void* k, const void* v, int num_pages,
+                   const int32_t* block_table, int bt_stride, const uint64_t* mask, void* out,
+                   float* lse, void* workspace, uint32_t* status, cudaStream_t stream);
+
+/*
+ * fd_tree_verify -- which drafted tokens stand, and the token that follows them (one launch).
+ *
+ * Node 0 of a sequence is its last emitted token, which stands; the walk goes on from node to child
+ * until it finds none.  Row t of target is the target's distribution after token t.
+ *   drafts given  (draft = NULL): the children i of a node are tried in ascending order; with P the
+ *                 target's probability of the child's token and S the sum of those of the tokens tried
+ *                 before it there, the child stands if uniform_i (1 - S) < P.  (A token tried before
+ *                 counts as 0.)  Where none stands, the next token is drawn from the node's
+ *                 target without the tried tokens.
+ *   drafts drawn  (draft given; chains only): node i + 1 stands if uniform x draft < target, both
+ *                 of its token; row t of draft is the distribution that token t was drawn from (row 0
+ *                 of a sequence is not read).  Where it does not, the next token is drawn from
+ *                 max(target - draft, 0).
+ * After the last node the next token is drawn from its target.  The draw takes the first token whose
+ * sum of weights up to it exceeds uniform_0 of the sequence times the sum of all (the root needs no
+ * other); weights without a sum are replaced by the target's, and if that has none the token is -1.
+ *
+ *   target         device float [T, vocab], rows target_stride elements apart (>= vocab); probabilities:
+ *                  NaN and negative values count as 0, values over 2 as 2
+ *   draft          device float [T, vocab], rows draft_stride apart, or NULL
+ *   vocab          1 .. FD_MAX_VOCAB
+ *   tokens         device int32 [T]; a token outside [0, vocab) never stands
+ *   parents        device int32 [T]: each node's parent within its sequence, below the node itself (a node
+ *                  with any other value but the root's is never reached); NULL: a chain
+ *   uniform        device float [T] in [0, 1)
+ *   path           device int32 [B, max_drafts], written: the nodes that stand, ascending, then -1
+ *   emitted        device int32 [B, max_drafts], written: the tokens of path[1..], then the next
+ *                  token, then -1 (so count tokens)
+ *   count          device int32 [B], written: nodes that stand (0 for a sequence without drafted tokens)
+ *
+ * The products and differences of probabilities are exact or in 64 bits; sums of weights are in units of 2^-60,
+ * so that they do not depend on an order (a row's sum must stay below 8).
+ * FD_ERR_INVALID: a missing pointer, a short stride, an output that overlaps an input or another output;
+ * FD_ERR_UNSUPPORTED: draft with parents, vocab; FD_ERR_ALIGN: a pointer not 4-byte aligned.  T = 0 still
+ * writes count (and max_drafts = 0: nothing else).
+ */
+#define FD_MAX_VOCAB (1 << 20)
+int fd_tree_verify(fd_tree_t tree, const float* target, int64_t target_stride, const float* draft,
+                   int64_t draft_stride, int vocab, const int32_t* tokens, const int32_t* parents,
+                   const float* uniform, int32_t* path, int32_t* emitted, int32_t* count,
+                   cudaStream_t stream);
+
+/*
+ * fd_tree_keep -- move the rows of the tokens that stand to the front of the drafted ones, in place
+ * (one launch): K and V row L_b - n_b + i of sequence b becomes row L_b - n_b + path[b][i], for
+ * i < count_b.  All other rows stay as they were.
+ *
+ *   k_cache, v_cache, num_pages, block_table, bt_stride   as for fd_append
+ *   path    device int32 [B, path_stride], path_stride >= max_drafts; nodes, ascending
+ *   count   device int32 [B]; taken as 0 where negative, as n_b where larger
+ *   status  device word or NULL
+ *
+ * Where a path does not ascend, or leaves [0, n_b), that entry and those behind it move nothing
+ * (FD_TREE_BAD_PATH); a row from or to a page outside the pool is not moved (FD_TREE_BAD_PAGE).
+ * Errors as for fd_append; path, count, block_table and status 4-byte aligned.
+ */
+int fd_tree_keep(fd_tree_t tree, void* k_cache, void* v_cache, int num_pages,
+                 const int32_t* block_table, int bt_stride, const int32_t* path, int path_stride,
+                 const int32_t* count, uint32_t* status, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fd_strerror(int status);
 

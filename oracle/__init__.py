@@ -4,7 +4,8 @@ Only ``tests/``, ``__graft_entry__.smoke()`` and ``bench.py``'s cpu-baseline and
 reference legs may import this package.  The CUDA library never imports, links
 or calls it, and it imports nothing from the CUDA library.
 
-Every function is pinned by ``tests/test_oracle.py`` or ``tests/test_oracle_rows.py`` (``-m "not gpu"``) against
+Every function is pinned by ``tests/test_oracle.py``, ``tests/test_oracle_rows.py`` or
+``tests/test_oracle_tree.py`` (``-m "not gpu"``) against
 brute force, closed forms, invariants and library routines; no function here is
 "parity unpinned".
 """
@@ -28,4 +29,10 @@ from .fd_rows_oracle import (  # noqa: F401
     pack_blocks,
     quantise,
     unpack_blocks,
+)
+from .fd_tree_oracle import (  # noqa: F401
+    ancestors,
+    keep_rows,
+    tree_reference,
+    verify_walk,
 )

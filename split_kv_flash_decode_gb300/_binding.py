@@ -50,6 +50,11 @@ FD_PLAN_COMBINERS = {n: (k + 1) << FD_PLAN_COMBINERS_SHIFT for k, n in enumerate
 FD_PLAN_SINGLE_COMBINER = FD_PLAN_COMBINERS[1]
 FD_MAX_BATCH = 256
 FD_MAX_PARTIALS = 1024
+FD_MAX_DRAFTS = 64
+FD_MAX_VOCAB = 1 << 20
+FD_TREE_BAD_PAGE = 1
+FD_TREE_BAD_PATH = 2
+FD_TREE_TIMEOUT = 4
 
 DTYPES = {"f16": FD_F16, "bf16": FD_BF16, "f16_e4m3kv": FD_F16_E4M3KV,
           "f16_e2m1kv": FD_F16_E2M1KV, "bf16_e2m1kv": FD_BF16_E2M1KV}
@@ -60,6 +65,8 @@ EXPORTED = (
     "fd_workspace_status", "fd_strerror", "fd_plan_get_info", "fd_plan_get_range", "fd_version",
     "fd_decode_noalloc", "fd_noalloc_status", "fd_plan_paged", "fd_decode_paged",
     "fd_rows_plan", "fd_rows_destroy", "fd_rows_get_info", "fd_append", "fd_gather",
+    "fd_tree_plan", "fd_tree_destroy", "fd_tree_get_info", "fd_tree_decode", "fd_tree_verify",
+    "fd_tree_keep",
 )
 FD_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -86,6 +93,11 @@ class PlanInfo(ctypes.Structure):
 
 class RowsInfo(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("cache_bytes", ctypes.c_int64)]
+
+
+class TreeInfo(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("max_drafts", ctypes.c_int32), ("ctas", ctypes.c_int32),
+                ("workspace_bytes", ctypes.c_uint64), ("kv_bytes", ctypes.c_uint64)]
 
 
 class RopeArgs(ctypes.Structure):
@@ -184,6 +196,23 @@ def lib() -> ctypes.CDLL:
             L.fd_append.restype = ctypes.c_int
             L.fd_gather.argtypes = [vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, vp]
             L.fd_gather.restype = ctypes.c_int
+            L.fd_tree_plan.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                       ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.c_int,
+                                       ctypes.c_int, ctypes.c_int, ctypes.POINTER(vp)]
+            L.fd_tree_plan.restype = ctypes.c_int
+            L.fd_tree_destroy.argtypes = [vp]
+            L.fd_tree_destroy.restype = ctypes.c_int
+            L.fd_tree_get_info.argtypes = [vp, ctypes.POINTER(TreeInfo)]
+            L.fd_tree_get_info.restype = ctypes.c_int
+            L.fd_tree_decode.argtypes = [vp, vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp,
+                                         vp, vp, vp]
+            L.fd_tree_decode.restype = ctypes.c_int
+            L.fd_tree_verify.argtypes = [vp, vp, ctypes.c_int64, vp, ctypes.c_int64, ctypes.c_int,
+                                         vp, vp, vp, vp, vp, vp, vp]
+            L.fd_tree_verify.restype = ctypes.c_int
+            L.fd_tree_keep.argtypes = [vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_int,
+                                       vp, vp, vp]
+            L.fd_tree_keep.restype = ctypes.c_int
             L.fd_version.argtypes = []
             L.fd_version.restype = ctypes.c_int
             _lib = L
@@ -395,6 +424,74 @@ def fd_gather(rows: Rows, k_cache, v_cache, num_pages, block_table, bt_stride, k
     _check(lib().fd_gather(rows.handle, _ptr(k_cache), _ptr(v_cache), int(num_pages),
                            _ptr(block_table), int(bt_stride), _ptr(k_out), _ptr(v_out),
                            _ptr(status), _stream(stream)), "fd_gather")
+
+
+class Tree:
+    """Owns one fd_tree_t handle (fd_tree_destroy on close / garbage collection)."""
+
+    def __init__(self, handle: int):
+        self.handle = handle
+        self.info = fd_tree_get_info(self)
+
+    def close(self) -> None:
+        if self.handle:
+            lib().fd_tree_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def fd_tree_plan(B, Hq, Hkv, d, seqlens, drafts, page_size=0, dtype="f16", num_sms=0) -> Tree:
+    """fd_tree_plan: the last drafts_b rows of every sequence are drafted tokens (host only)."""
+    seqlens, drafts = list(seqlens), list(drafts)
+    if len(seqlens) != B or len(drafts) != B:
+        raise FdError(FD_ERR_INVALID, "fd_tree_plan: seqlens and drafts need B entries")
+    handle = ctypes.c_void_p()
+    rc = lib().fd_tree_plan(int(B), int(Hq), int(Hkv), int(d), _i32_array(seqlens, B),
+                            _i32_array(drafts, B), int(page_size),
+                            DTYPES[dtype] if isinstance(dtype, str) else int(dtype), int(num_sms),
+                            ctypes.byref(handle))
+    _check(rc, "fd_tree_plan")
+    return Tree(handle.value)
+
+
+def fd_tree_destroy(tree: Tree) -> None:
+    tree.close()
+
+
+def fd_tree_get_info(tree: Tree) -> dict:
+    info = TreeInfo()
+    _check(lib().fd_tree_get_info(tree.handle, ctypes.byref(info)), "fd_tree_get_info")
+    return {name: getattr(info, name) for name, _ in TreeInfo._fields_}
+
+
+def fd_tree_decode(tree: Tree, q, k, v, num_pages, block_table, bt_stride, mask, out, lse, workspace,
+                   status=None, stream=None) -> None:
+    """fd_tree_decode: attention of all drafted tokens over the cache."""
+    _check(lib().fd_tree_decode(tree.handle, _ptr(q), _ptr(k), _ptr(v), int(num_pages),
+                                _ptr(block_table), int(bt_stride), _ptr(mask), _ptr(out), _ptr(lse),
+                                _ptr(workspace), _ptr(status), _stream(stream)), "fd_tree_decode")
+
+
+def fd_tree_verify(tree: Tree, target, target_stride, draft, draft_stride, vocab, tokens, parents,
+                   uniform, path, emitted, count, stream=None) -> None:
+    """fd_tree_verify: which drafted tokens stand, and the token that follows (one launch)."""
+    _check(lib().fd_tree_verify(tree.handle, _ptr(target), int(target_stride), _ptr(draft),
+                                int(draft_stride), int(vocab), _ptr(tokens), _ptr(parents),
+                                _ptr(uniform), _ptr(path), _ptr(emitted), _ptr(count),
+                                _stream(stream)), "fd_tree_verify")
+
+
+def fd_tree_keep(tree: Tree, k_cache, v_cache, num_pages, block_table, bt_stride, path, path_stride,
+                 count, status=None, stream=None) -> None:
+    """fd_tree_keep: the rows of the tokens that stand move together, in place (one launch)."""
+    _check(lib().fd_tree_keep(tree.handle, _ptr(k_cache), _ptr(v_cache), int(num_pages),
+                              _ptr(block_table), int(bt_stride), _ptr(path), int(path_stride),
+                              _ptr(count), _ptr(status), _stream(stream)), "fd_tree_keep")
 
 
 def fd_version() -> int:

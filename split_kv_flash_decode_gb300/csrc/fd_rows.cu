@@ -8,6 +8,7 @@
 #include <initializer_list>
 #include <new>
 
+#include "fd_host.h"
 #include "fd_kernel.cuh"
 
 struct fd_rows_s {
@@ -33,8 +34,6 @@ constexpr int64_t kAppendWarps = 16 * 152;
 // Tokens of one gather warp: two rounds of its lanes.  (32K tokens of a 4-bit cache, 172 MB: 27.2 us;
 // with one round 34.0, three 27.6, four 28.5 us.)
 FD_HD constexpr int gather_tokens(int d) { return 2 * (512 / d); }
-
-enum KvKind { kKv16 = 0, kKvE4m3 = 1, kKvE2m1 = 2 };
 
 // Where the rows of a call lie.
 struct RowMap {
@@ -413,19 +412,7 @@ __global__ void __launch_bounds__(kRowsThreads) fd_gather_kernel(const __grid_co
   }
 }
 
-int kv_kind(int dtype) {
-  return dtype == FD_F16_E4M3KV                                  ? kKvE4m3
-         : dtype == FD_F16_E2M1KV || dtype == FD_BF16_E2M1KV ? kKvE2m1
-                                                               : kKv16;
-}
-bool is_bf16(int dtype) { return dtype == FD_BF16 || dtype == FD_BF16_E2M1KV; }
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-int64_t row_bytes(const fd_rows_s* r) {
-  const int kind = kv_kind(r->dtype);
-  return kind == kKv16 ? 2 * r->d : kind == kKvE4m3 ? r->d : r->d * 9 / 16;
-}
+int64_t row_bytes(const fd_rows_s* r) { return cache_row_bytes(r->dtype, r->d); }
 
 // Page-table checks shared by both calls, and the map of the rows.
 int make_map(const fd_rows_s* r, int num_pages, const int32_t* block_table, int bt_stride,
@@ -523,16 +510,9 @@ int set_rope(const fd_rope* rope, int d, bool four_bit_cache, AppendParams* p) {
   return FD_OK;
 }
 
-// A range of bytes.
-struct Span {
-  uintptr_t at;
-  uint64_t n;
-};
-Span span(const void* p, int64_t n) { return {reinterpret_cast<uintptr_t>(p), p == nullptr ? 0 : (uint64_t)n}; }
 Span input_span(const void* p, const int64_t* stride, int64_t T, int H, int d) {
   return span(p, 2 * ((T - 1) * stride[0] + (H - 1) * stride[1] + d));
 }
-bool overlap(const Span& a, const Span& b) { return a.n > 0 && b.n > 0 && a.at < b.at + b.n && b.at < a.at + a.n; }
 // Bytes of one cache.
 int64_t cache_span(const fd_rows_s* r, int num_pages) {
   return r->page_size ? (int64_t)num_pages * r->cache_bytes : r->cache_bytes;

@@ -1,0 +1,579 @@
+// A step of speculative decoding: the plan, the verdict on drafted tokens (fd_tree_verify) and the
+// rows that stand (fd_tree_keep).  The attention is in fd_tree_attn.cu.  See fd.h for the contract.
+#include "fd_tree.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "fd_kernel.cuh"
+
+namespace fd {
+namespace {
+
+// ------------------------------------------------------------------ verify
+
+constexpr int kVerifyThreads = 256;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyCluster = 8;  // CTAs of a sequence: each reads a slice of its row
+
+struct VerifyParams {
+  const float *target, *draft;
+  int64_t target_stride, draft_stride;
+  const int32_t *tokens, *parents;
+  const float* uniform;
+  int32_t *path, *emitted, *count;
+  int32_t vocab, max_drafts;
+  int32_t cu[FD_MAX_BATCH + 1];
+};
+
+__device__ __forceinline__ float weight(float x) { return x > 0.f ? fminf(x, 2.f) : 0.f; }
+// A weight in units of 2^-60.
+__device__ __forceinline__ uint64_t fixed(float x) { return __float2ull_rn(weight(x) * 0x1p60f); }
+__device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? a - b : 0; }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Store into the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_cluster_u64(uint32_t addr, uint32_t rank, uint64_t v) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+               "st.shared::cluster.u64 [a], %2;\n\t}" ::"r"(addr), "r"(rank), "l"(v) : "memory");
+}
+
+// One cluster per sequence.  The walk is the same in every CTA: a lane holds two nodes, with the target's
+// probability of their tokens (all gathered at once: the walk's chain is one load long), and a ballot finds
+// the children of a node.  Then each CTA sums a slice of the last node's row, the cluster adds the slices up,
+// and the CTA in whose slice the draw falls looks for it there.
+__global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluster, 1, 1)
+    fd_verify_kernel(const __grid_constant__ VerifyParams p) {
+  __shared__ int32_t tokens[FD_MAX_DRAFTS];
+  __shared__ uint64_t warp_sum[2][kVerifyWarps];
+  __shared__ uint64_t slice_sum[2][kVerifyCluster];
+  __shared__ uint64_t stands_s, tried_s;
+  dev::pdl_launch_dependents();
+  dev::pdl_wait();
+  const int b = blockIdx.x / kVerifyCluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
+  const int first = p.cu[b], n = p.cu[b + 1] - first, V = p.vocab;
+  if (n == 0) {
+    if (rank == 0) {
+      for (int i = tid; i < p.max_drafts; i += kVerifyThreads)
+        p.path[(int64_t)b * p.max_drafts + i] = p.emitted[(int64_t)b * p.max_drafts + i] = -1;
+      if (tid == 0) p.count[b] = 0;
+    }
+    return;
+  }
+  if (warp == 0) {
+    int up[2], tok[2];
+    float u[2], pt[2], qt[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = lane + 32 * k;
+      up[k] = tok[k] = -1;
+      u[k] = pt[k] = qt[k] = 0.f;
+      if (i < n) {
+        tok[k] = p.tokens[first + i];
+        tokens[i] = tok[k];
+        u[k] = p.uniform[first + i];
+        const int parent = p.parents != nullptr ? p.parents[first + i] : i - 1;
+        if (i > 0 && parent >= 0 && parent < i) {
+          up[k] = parent;
+          if ((uint32_t)tok[k] < (uint32_t)V) {
+            pt[k] = weight(p.target[(first + parent) * p.target_stride + tok[k]]);
+            if (p.draft != nullptr) qt[k] = weight(p.draft[(first + i) * p.draft_stride + tok[k]]);
+          }
+        }
+      }
+    }
+    auto bits = [&](bool a, bool b) {
+      const uint32_t lo = __ballot_sync(0xffffffffu, a), hi = __ballot_sync(0xffffffffu, b);
+      return (uint64_t)hi << 32 | lo;
+    };
+    uint64_t stands = 1, tried = 0;
+    int node = 0;
+    for (;;) {  // at most n rounds: a child lies above its parent
+      uint64_t below = bits(up[0] == node, up[1] == node);
+      double mass = 1.0;
+      int went = -1;
+      tried = 0;
+      while (below != 0) {
+        const int i = __ffsll((long long)below) - 1, src = i & 31;
+        below &= below - 1;
+        const float pi = __shfl_sync(0xffffffffu, i < 32 ? pt[0] : pt[1], src);
+        const float ui = __shfl_sync(0xffffffffu, i < 32 ? u[0] : u[1], src);
+        if (p.draft != nullptr) {
+          const float qi = __shfl_sync(0xffffffffu, i < 32 ? qt[0] : qt[1], src);
+          if ((double)ui * (double)qi < (double)pi) went = i;
+        } else {
+          const int ti = __shfl_sync(0xffffffffu, i < 32 ? tok[0] : tok[1], src);
+          const uint64_t same = bits(tok[0] == ti, tok[1] == ti);
+          const float left = (same & tried) ? 0.f : pi;
+          if ((double)ui * mass < (double)left) went = i;
+          else mass -= (double)left;
+        }
+        if (went >= 0) break;
+        tried |= 1ull << i;
+      }
+      if (went < 0) break;
+      node = went;
+      stands |= 1ull << node;
+    }
+    if (lane == 0) {
+      stands_s = stands;
+      tried_s = tried;
+    }
+    if (rank == 0) {
+      const int count = __popcll(stands);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        if ((stands >> i) & 1) {
+          const int at = __popcll(stands & ((1ull << i) - 1));
+          p.path[(int64_t)b * p.max_drafts + at] = i;
+          if (at > 0) p.emitted[(int64_t)b * p.max_drafts + at - 1] = tok[k];
+        }
+        if (i >= count && i < p.max_drafts)
+          p.path[(int64_t)b * p.max_drafts + i] = p.emitted[(int64_t)b * p.max_drafts + i] = -1;
+      }
+      if (lane == 0) p.count[b] = count;
+    }
+  }
+  __syncthreads();
+  const uint64_t stands = stands_s, tried = tried_s;
+  const int node = 63 - __clzll((long long)stands);
+  const float u0 = p.uniform[first];
+  const float* target = p.target + (first + node) * p.target_stride;
+  // The slice of this CTA, and this warp's part of it.
+  const int per_cta = (V + kVerifyCluster - 1) / kVerifyCluster;
+  const int c0 = min((int)rank * per_cta, V), c1 = min(c0 + per_cta, V);
+  const int per_warp = (c1 - c0 + kVerifyWarps - 1) / kVerifyWarps;
+  const int w0 = min(c0 + warp * per_warp, c1), w1 = min(w0 + per_warp, c1);
+
+  for (int attempt = 0;; ++attempt) {
+    // The second attempt draws from the target itself: nothing was left.
+    const bool rest = attempt == 0 && tried != 0;
+    const float* draft = rest && p.draft != nullptr ? p.draft + (first + __ffsll((long long)tried) - 1) * p.draft_stride : nullptr;
+    const uint64_t gone = rest && p.draft == nullptr ? tried : 0;
+    uint64_t sum = 0;
+    if (draft != nullptr) {
+#pragma unroll 8
+      for (int i = w0 + lane; i < w1; i += 32) sum += less(fixed(target[i]), fixed(draft[i]));
+    } else {
+#pragma unroll 16
+      for (int i = w0 + lane; i < w1; i += 32) sum += fixed(target[i]);
+    }
+    // Tokens that were tried weigh nothing; one that was tried twice goes once.
+    for (uint64_t m = gone; m != 0; m &= m - 1) {
+      const int i = __ffsll((long long)m) - 1, t = tokens[i];
+      bool again = false;
+      for (uint64_t e = gone & ((1ull << i) - 1); e != 0; e &= e - 1) again |= tokens[__ffsll((long long)e) - 1] == t;
+      if (t >= w0 && t < w1 && ((t - w0) & 31) == lane && !again) sum -= fixed(target[t]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) warp_sum[attempt][warp] = sum;
+    __syncthreads();
+    if (tid < kVerifyCluster) {
+      uint64_t all = 0;
+      for (int w = 0; w < kVerifyWarps; ++w) all += warp_sum[attempt][w];
+      store_cluster_u64(dev::smem_addr(&slice_sum[attempt][rank]), tid, all);
+    }
+    cluster_sync();
+    uint64_t total = 0, before = 0;
+    for (int r = 0; r < kVerifyCluster; ++r) {
+      before += r < (int)rank ? slice_sum[attempt][r] : 0;
+      total += slice_sum[attempt][r];
+    }
+    if (total == 0) {
+      if (rest) continue;
+      if (rank == 0 && tid == 0) p.emitted[(int64_t)b * p.max_drafts + __popcll(stands) - 1] = -1;
+      return;
+    }
+    // The first token with a sum up to it over uniform x total.
+    const uint64_t r64 = u0 >= 1.f ? ~0ull : u0 > 0.f ? __double2ull_rz((double)u0 * 0x1p64) : 0;
+    const uint64_t at = __umul64hi(total, r64);
+    if (at < before || at >= before + slice_sum[attempt][rank]) return;
+    int w = 0;
+    while (at >= before + warp_sum[attempt][w]) before += warp_sum[attempt][w++];
+    const int s0 = min(c0 + w * per_warp, c1), s1 = min(s0 + per_warp, c1);
+    // All threads look through that warp's part: eight tokens each.
+    for (int at0 = s0; at0 < s1; at0 += 8 * kVerifyThreads) {
+      uint64_t x[8], mine = 0;
+      const int i0 = at0 + 8 * tid;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k;
+        x[k] = i < s1 ? fixed(target[i]) : 0;
+        if (draft != nullptr && i < s1) x[k] = less(x[k], fixed(draft[i]));
+      }
+      for (uint64_t m = gone; m != 0; m &= m - 1) {
+        const int t = tokens[__ffsll((long long)m) - 1] - i0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (t == k) x[k] = 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mine += x[k];
+      uint64_t upto = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += o;
+      }
+      __syncthreads();  // the sums of the last round are read
+      if (lane == 31) warp_sum[attempt ^ 1][warp] = upto;
+      __syncthreads();
+      uint64_t sum0 = before;
+      for (int k = 0; k < kVerifyWarps; ++k) {
+        if (k < warp) sum0 += warp_sum[attempt ^ 1][k];
+        before += warp_sum[attempt ^ 1][k];
+      }
+      sum0 += upto - mine;
+      if (at >= sum0 && at < sum0 + mine) {
+        int k = 0;
+#pragma unroll
+        for (int j = 0; j < 7; ++j) {
+          if (k == j && at >= sum0 + x[j]) {
+            sum0 += x[j];
+            k = j + 1;
+          }
+        }
+        p.emitted[(int64_t)b * p.max_drafts + __popcll(stands) - 1] = i0 + k;
+      }
+      if (at < before) return;  // the same in every thread
+    }
+    return;
+  }
+}
+
+// ------------------------------------------------------------------ keep
+
+constexpr int kKeepThreads = 128;
+
+struct KeepParams {
+  uint8_t *k_cache, *v_cache;
+  const int32_t *block_table, *path, *count;
+  uint32_t* status;
+  int32_t Hkv, d, page_shift, num_pages, bt_stride, path_stride, pieces;
+  int32_t cu[FD_MAX_BATCH + 1];
+  int32_t first[FD_MAX_BATCH];  // row of node 0 in its sequence
+  int32_t base[FD_MAX_BATCH];
+};
+
+// Moves one piece of n rows; where(row) is the piece's place in the cache.  Sources lie behind their
+// destinations, so a batch of loads ahead of its stores never reads what was written.
+template <typename W, typename F>
+__device__ __forceinline__ void move_rows(uint8_t* cache, const int64_t* from, const int64_t* to, int n, F where) {
+  constexpr int kBatch = 8;
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    W x[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k < n && from[i0 + k] >= 0) x[k] = *reinterpret_cast<const W*>(cache + where(from[i0 + k]));
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k < n && from[i0 + k] >= 0) *reinterpret_cast<W*>(cache + where(to[i0 + k])) = x[k];
+  }
+}
+
+// One thread: one piece of K (even blocks of a sequence) or V of a row, through all rows of its sequence
+// that move: nothing is shared between threads, so the move needs no order among them.  Pieces are 16
+// bytes; of a 4-bit block, whose rows lie in parts, 4 bytes, and single bytes for V's scales.
+template <int KV>
+__global__ void __launch_bounds__(kKeepThreads) fd_keep_kernel(const __grid_constant__ KeepParams p) {
+  __shared__ int64_t from[FD_MAX_DRAFTS], to[FD_MAX_DRAFTS];
+  __shared__ int bad[2];
+  dev::pdl_launch_dependents();
+  dev::pdl_wait();
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  const int n = p.cu[b + 1] - p.cu[b];
+  const int count = min(max(p.count[b], 0), n);
+  if (count == 0) return;
+  auto row_of = [&](int r) {
+    r += p.first[b];
+    if (p.block_table == nullptr) return (int64_t)p.base[b] + r;
+    const int pg = p.block_table[(int64_t)b * p.bt_stride + (r >> p.page_shift)];
+    if ((uint32_t)pg >= (uint32_t)p.num_pages) {
+      if (p.status != nullptr) atomicOr(p.status, FD_TREE_BAD_PAGE);
+      return (int64_t)-1;
+    }
+    return ((int64_t)pg << p.page_shift) + (r & ((1 << p.page_shift) - 1));
+  };
+  if (tid < FD_MAX_DRAFTS) {
+    const int32_t* path = p.path + (int64_t)b * p.path_stride;
+    const int node = tid < count ? path[tid] : -1;
+    const bool ascends = node >= 0 && node < n && (tid == 0 || node > path[tid - 1]);
+    const uint32_t wrong = __ballot_sync(0xffffffffu, tid < count && !ascends);
+    if (lane == 0) bad[tid >> 5] = wrong != 0 ? tid + __ffs(wrong) - 1 : FD_MAX_DRAFTS;
+    int64_t src = -1, dst = -1;
+    if (tid < count && ascends && node != tid) {
+      src = row_of(node);
+      dst = row_of(tid);
+    }
+    from[tid] = dst < 0 ? -1 : src;
+    to[tid] = dst;
+  }
+  __syncthreads();
+  const int good = min(bad[0], bad[1]), rows = min(count, good);
+  if (good < count && p.status != nullptr && tid == 0) atomicOr(p.status, FD_TREE_BAD_PATH);
+  const bool is_v = blockIdx.x & 1;
+  const int piece = (blockIdx.x >> 1) * kKeepThreads + tid;
+  if (piece >= p.pieces) return;
+  uint8_t* cache = is_v ? p.v_cache : p.k_cache;
+  const int d = p.d;
+  if constexpr (KV != kKvE2m1) {
+    const int64_t row_bytes = (int64_t)p.Hkv * d * (KV == kKv16 ? 2 : 1);
+    move_rows<uint4>(cache, from, to, rows, [&](int64_t row) { return row * row_bytes + 16 * piece; });
+  } else {
+    // Pieces of a KV head: d / 8 of codes, then its scales: d / 16 bytes, of K together, of V 16 apart.
+    const int per_head = d / 8 + d / 16, h = piece / per_head, i = piece - h * per_head;
+    const int64_t block_bytes = (int64_t)p.Hkv * 9 * d;
+    cache += (int64_t)h * 9 * d;
+    if (i < d / 8) {
+      // V: piece i lies in group i / (d / 64) of d / 8 elements.
+      const int g = i / (d / 64), swap = ((d == 128 ? g : g >> 1) & 1) << 2, part = 4 * (i - g * (d / 64));
+      move_rows<uint32_t>(cache, from, to, rows, [&](int64_t row) {
+        const int r = (int)(row & (kBlockTokens - 1));
+        return (row >> kBlockShift) * block_bytes +
+               (is_v ? g * d + ((r >> 1) ^ swap) * (d / 8) + (r & 1) * (d / 16) + part : r * (d / 2) + 4 * i);
+      });
+    } else {
+      const int j = i - d / 8;
+      move_rows<uint8_t>(cache, from, to, rows, [&](int64_t row) {
+        const int r = (int)(row & (kBlockTokens - 1));
+        return (row >> kBlockShift) * block_bytes + 8 * d + (is_v ? 16 * j + r : r * (d / 16) + j);
+      });
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+int launch(const void* fn, dim3 grid, int threads, const void* params, cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* args[] = {const_cast<void*>(params)};
+  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    cudaGetLastError();
+    return FD_ERR_CUDA;
+  }
+  return FD_OK;
+}
+
+// Page-table arguments of a call; sets the page's bits.
+int check_pages(const fd_tree_s* t, int num_pages, const int32_t* block_table, int bt_stride, int32_t* shift) {
+  *shift = 0;
+  if (!t->page_size) return block_table != nullptr ? FD_ERR_INVALID : FD_OK;
+  if (num_pages < 1 || block_table == nullptr || bt_stride < t->max_pages) return FD_ERR_INVALID;
+  if ((int64_t)num_pages * t->page_size >= (int64_t)1 << 31) return FD_ERR_UNSUPPORTED;
+  while ((1 << *shift) < t->page_size) ++*shift;
+  return FD_OK;
+}
+int64_t cache_rows(const fd_tree_s* t, int num_pages) {
+  if (t->page_size) return (int64_t)num_pages * t->page_size;
+  return kv_kind(t->dtype) == kKvE2m1 ? t->n_blocks * kBlockTokens : t->n_tokens;
+}
+Span cache_span(const fd_tree_s* t, const void* p, int num_pages) {
+  return span(p, cache_rows(t, num_pages) * t->Hkv * cache_row_bytes(t->dtype, t->d));
+}
+Span table_span(const fd_tree_s* t, const int32_t* table, int64_t bt_stride) {
+  return span(table, 4 * ((t->B - 1) * bt_stride + t->max_pages));
+}
+// Whether an output overlaps an input or another output.
+template <size_t N, size_t M>
+bool any_overlap(const Span (&outs)[N], const Span (&ins)[M]) {
+  for (size_t o = 0; o < N; ++o) {
+    for (const Span& i : ins)
+      if (overlap(outs[o], i)) return true;
+    for (size_t k = 0; k < o; ++k)
+      if (overlap(outs[o], outs[k])) return true;
+  }
+  return false;
+}
+
+}  // namespace
+}  // namespace fd
+
+extern "C" {
+
+int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const int32_t* drafts, int page_size,
+                 int dtype, int num_sms, fd_tree_t* out_tree) {
+  if (!out_tree) return FD_ERR_INVALID;
+  *out_tree = nullptr;
+  if (!seqlens || !drafts) return FD_ERR_INVALID;
+  if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || page_size < 0 || num_sms < 0 || Hq % Hkv != 0) return FD_ERR_INVALID;
+  if (dtype != FD_F16 && dtype != FD_BF16 && dtype != FD_F16_E4M3KV && dtype != FD_F16_E2M1KV &&
+      dtype != FD_BF16_E2M1KV)
+    return FD_ERR_INVALID;
+  if (page_size != 0 && (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))))
+    return FD_ERR_UNSUPPORTED;
+  if (B > FD_MAX_BATCH || (d != 64 && d != 128)) return FD_ERR_UNSUPPORTED;
+  const int64_t limit = (int64_t)1 << 31;
+  // Token x head offsets of q and the heads of a grid stay within 32 bits.
+  if (Hq > 4096) return FD_ERR_UNSUPPORTED;
+  const bool four = fd::kv_kind(dtype) == fd::kKvE2m1;
+  int64_t T = 0, tokens = 0, blocks = 0, read = 0;
+  int max_pages = 0, max_drafts = 0;
+  for (int b = 0; b < B; ++b) {
+    if (seqlens[b] < 0 || drafts[b] < 0 || drafts[b] > seqlens[b]) return FD_ERR_INVALID;
+    if (drafts[b] > FD_MAX_DRAFTS) return FD_ERR_UNSUPPORTED;
+    T += drafts[b];
+    tokens += seqlens[b];
+    blocks += ((int64_t)seqlens[b] + fd::kBlockTokens - 1) / fd::kBlockTokens;
+    if (drafts[b]) read += seqlens[b];
+    max_drafts = std::max(max_drafts, (int)drafts[b]);
+    if (page_size) max_pages = std::max(max_pages, (int)(((int64_t)seqlens[b] + page_size - 1) / page_size));
+  }
+  if ((four ? blocks * fd::kBlockTokens : tokens) >= limit) return FD_ERR_UNSUPPORTED;
+  if (num_sms == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return FD_ERR_CUDA;
+    }
+  }
+  fd_tree_s* t = new (std::nothrow) fd_tree_s();
+  if (!t) return FD_ERR_NOMEM;
+  t->B = B; t->Hq = Hq; t->Hkv = Hkv; t->d = d; t->dtype = dtype; t->page_size = page_size;
+  t->max_pages = max_pages; t->max_drafts = max_drafts; t->num_sms = num_sms;
+  t->T = T; t->n_tokens = tokens; t->n_blocks = blocks;
+  t->kv_bytes = (uint64_t)read * Hkv * 2 * fd::cache_row_bytes(dtype, d);
+  int32_t cu = 0;
+  int64_t base = 0;
+  for (int b = 0; b < B; ++b) {
+    t->cu_q[b] = cu;
+    t->len[b] = seqlens[b];
+    t->base[b] = (int32_t)base;
+    cu += drafts[b];
+    base += four ? ((int64_t)seqlens[b] + fd::kBlockTokens - 1) / fd::kBlockTokens * fd::kBlockTokens : seqlens[b];
+  }
+  t->cu_q[B] = cu;
+  t->ctas = (int)(T * Hq);
+  t->ws_bytes = 0;
+  *out_tree = t;
+  return FD_OK;
+}
+
+int fd_tree_destroy(fd_tree_t tree) {
+  delete tree;
+  return FD_OK;
+}
+
+int fd_tree_get_info(fd_tree_t t, fd_tree_info* info) {
+  if (!t || !info) return FD_ERR_INVALID;
+  info->tokens = t->T;
+  info->max_drafts = t->max_drafts;
+  info->ctas = t->ctas;
+  info->workspace_bytes = t->ws_bytes;
+  info->kv_bytes = t->kv_bytes;
+  return FD_OK;
+}
+
+int fd_tree_decode(fd_tree_t t, const void* q, const void* k, const void* v, int num_pages, const int32_t* block_table,
+                   int bt_stride, const uint64_t* mask, void* out, float* lse, void* workspace, uint32_t* status,
+                   cudaStream_t stream) {
+  if (!t) return FD_ERR_INVALID;
+  if (t->T == 0) return FD_OK;
+  if (!q || !k || !v || !out || (t->ws_bytes && !workspace)) return FD_ERR_INVALID;
+  for (const void* p : {q, k, v, (const void*)out, (const void*)lse, (const void*)workspace})
+    if (!fd::aligned(p, 16)) return FD_ERR_ALIGN;
+  if (!fd::aligned(mask, 8) || !fd::aligned(block_table, 4) || !fd::aligned(status, 4)) return FD_ERR_ALIGN;
+  fd::TreeParams p;
+  int rc = fd::check_pages(t, num_pages, block_table, bt_stride, &p.page_shift);
+  if (rc != FD_OK) return rc;
+  const int64_t rows = t->T * t->Hq;
+  const fd::Span outs[] = {fd::span(out, 2 * rows * t->d), fd::span(lse, 4 * rows),
+                           fd::span(workspace, (int64_t)t->ws_bytes), fd::span(status, 4)};
+  const fd::Span ins[] = {fd::span(q, 2 * rows * t->d), fd::cache_span(t, k, num_pages), fd::cache_span(t, v, num_pages),
+                          fd::span(mask, 8 * t->T), fd::table_span(t, block_table, bt_stride)};
+  if (fd::any_overlap(outs, ins)) return FD_ERR_INVALID;
+  p.q = q; p.k = k; p.v = v; p.mask = mask; p.out = out; p.lse = lse; p.status = status;
+  p.block_table = block_table; p.bt_stride = bt_stride; p.num_pages = num_pages;
+  p.B = t->B; p.Hq = t->Hq; p.Hkv = t->Hkv;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)t->d));
+  std::memcpy(p.cu_q, t->cu_q, sizeof(p.cu_q));
+  std::memcpy(p.len, t->len, sizeof(p.len));
+  std::memcpy(p.base, t->base, sizeof(p.base));
+  if (fd::launch_tree(p, t->dtype, t->d, (int)t->T, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return FD_ERR_CUDA;
+  }
+  return FD_OK;
+}
+
+int fd_tree_verify(fd_tree_t t, const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                   int vocab, const int32_t* tokens, const int32_t* parents, const float* uniform, int32_t* path,
+                   int32_t* emitted, int32_t* count, cudaStream_t stream) {
+  if (!t || !count || vocab < 1) return FD_ERR_INVALID;
+  if (t->T && (!target || !tokens || !uniform || !path || !emitted)) return FD_ERR_INVALID;
+  if (vocab > FD_MAX_VOCAB || (draft && parents)) return FD_ERR_UNSUPPORTED;
+  if (t->T && (target_stride < vocab || (draft && draft_stride < vocab))) return FD_ERR_INVALID;
+  for (const void* p : {(const void*)target, (const void*)draft, (const void*)tokens, (const void*)parents,
+                        (const void*)uniform, (const void*)path, (const void*)emitted, (const void*)count})
+    if (!fd::aligned(p, 4)) return FD_ERR_ALIGN;
+  const int64_t T = t->T, said = 4 * (int64_t)t->B * t->max_drafts;
+  const fd::Span outs[] = {fd::span(path, said), fd::span(emitted, said), fd::span(count, 4 * (int64_t)t->B)};
+  const fd::Span ins[] = {fd::span(T ? target : nullptr, 4 * ((T - 1) * target_stride + vocab)),
+                          fd::span(T ? draft : nullptr, 4 * ((T - 1) * draft_stride + vocab)), fd::span(tokens, 4 * T),
+                          fd::span(parents, 4 * T), fd::span(uniform, 4 * T)};
+  if (fd::any_overlap(outs, ins)) return FD_ERR_INVALID;
+  fd::VerifyParams p;
+  p.target = target; p.draft = draft;
+  p.target_stride = target_stride; p.draft_stride = draft_stride;
+  p.tokens = tokens; p.parents = parents; p.uniform = uniform;
+  p.path = path; p.emitted = emitted; p.count = count;
+  p.vocab = vocab;
+  p.max_drafts = t->max_drafts;
+  std::memcpy(p.cu, t->cu_q, sizeof(p.cu));
+  return fd::launch(reinterpret_cast<const void*>(&fd::fd_verify_kernel), dim3(t->B * fd::kVerifyCluster),
+                    fd::kVerifyThreads, &p, stream);
+}
+
+int fd_tree_keep(fd_tree_t t, void* k_cache, void* v_cache, int num_pages, const int32_t* block_table, int bt_stride,
+                 const int32_t* path, int path_stride, const int32_t* count, uint32_t* status, cudaStream_t stream) {
+  if (!t) return FD_ERR_INVALID;
+  if (t->T == 0) return FD_OK;
+  if (!k_cache || !v_cache || !path || !count || path_stride < t->max_drafts) return FD_ERR_INVALID;
+  if (!fd::aligned(k_cache, 16) || !fd::aligned(v_cache, 16)) return FD_ERR_ALIGN;
+  if (!fd::aligned(path, 4) || !fd::aligned(count, 4) || !fd::aligned(block_table, 4) || !fd::aligned(status, 4))
+    return FD_ERR_ALIGN;
+  fd::KeepParams p;
+  int rc = fd::check_pages(t, num_pages, block_table, bt_stride, &p.page_shift);
+  if (rc != FD_OK) return rc;
+  const fd::Span outs[] = {fd::cache_span(t, k_cache, num_pages), fd::cache_span(t, v_cache, num_pages),
+                           fd::span(status, 4)};
+  const fd::Span ins[] = {fd::span(path, 4 * ((int64_t)(t->B - 1) * path_stride + t->max_drafts)),
+                          fd::span(count, 4 * (int64_t)t->B), fd::table_span(t, block_table, bt_stride)};
+  if (fd::any_overlap(outs, ins)) return FD_ERR_INVALID;
+  p.k_cache = static_cast<uint8_t*>(k_cache); p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.block_table = block_table; p.path = path; p.count = count; p.status = status;
+  p.Hkv = t->Hkv; p.d = t->d; p.num_pages = num_pages; p.bt_stride = bt_stride; p.path_stride = path_stride;
+  const int kind = fd::kv_kind(t->dtype);
+  p.pieces = kind == fd::kKvE2m1 ? t->Hkv * (t->d / 8 + t->d / 16)
+                                 : (int)(t->Hkv * fd::cache_row_bytes(t->dtype, t->d) / 16);
+  std::memcpy(p.cu, t->cu_q, sizeof(p.cu));
+  std::memcpy(p.base, t->base, sizeof(p.base));
+  for (int b = 0; b < t->B; ++b) p.first[b] = t->len[b] - (t->cu_q[b + 1] - t->cu_q[b]);
+  const dim3 grid(2 * ((p.pieces + fd::kKeepThreads - 1) / fd::kKeepThreads), t->B);
+  const void* fn = kind == fd::kKv16     ? reinterpret_cast<const void*>(&fd::fd_keep_kernel<fd::kKv16>)
+                   : kind == fd::kKvE4m3 ? reinterpret_cast<const void*>(&fd::fd_keep_kernel<fd::kKvE4m3>)
+                                         : reinterpret_cast<const void*>(&fd::fd_keep_kernel<fd::kKvE2m1>);
+  return fd::launch(fn, grid, fd::kKeepThreads, &p, stream);
+}
+
+}  // extern "C"

@@ -41,7 +41,41 @@ class Rope:
         self.address = ctypes.addressof(self.args)
 
 
-class KVRows:
+class CacheCalls:
+    """Argument checks of calls on a cache: of KVRows, and of TreeDecoder.
+
+    Uses device, Bsz, page_size, _kv and _cache_shape (of a paged cache: with any number of pages)."""
+
+    def _refuse(self, name, t, shape, dtype):
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}, expected "
+                         f"a contiguous {dtype} {tuple(shape)} on {self.device}")
+
+    def _whole(self, name, t, shape, dtype):
+        """Address of a contiguous tensor."""
+        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            self._refuse(name, t, shape, dtype)
+        return t.data_ptr()
+
+    def _caches(self, k_cache, v_cache, block_table):
+        """(k, v, num_pages, block table, its stride)."""
+        num_pages, stride, table, shape = 0, 0, 0, self._cache_shape
+        if self.page_size:
+            if block_table is None:
+                raise ValueError("a paged cache needs its block_table")
+            num_pages = k_cache.shape[0]
+            shape = (num_pages, *shape[1:])
+            stride = block_table.shape[-1] if block_table.dim() == 2 else -1
+            table = self._whole("block_table", block_table, (self.Bsz, stride), torch.int32)
+        elif block_table is not None:
+            raise ValueError("these rows are of a contiguous cache")
+        return (self._whole("k_cache", k_cache, shape, self._kv), self._whole("v_cache", v_cache, shape, self._kv),
+                num_pages, table, stride)
+
+    def _status(self, status):
+        return 0 if status is None else self._whole("status", status, (1,), torch.int32)
+
+
+class KVRows(CacheCalls):
     """The rows [begin_b, begin_b + count_b) of every sequence of a cache (default: all rows).
 
     ``seqlens`` are the lengths the cache is laid out for, the rows of the call included: the
@@ -71,16 +105,6 @@ class KVRows:
         self._k_shape = (self.tokens, self.Hkv, self.d)
         self._cache_shape = cache_shape(dtype, self.Hkv, self.d, self.seqlens, 0, self.page_size)
 
-    def _refuse(self, name, t, shape, dtype):
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}, expected "
-                         f"a contiguous {dtype} {tuple(shape)} on {self.device}")
-
-    def _whole(self, name, t, shape, dtype):
-        """Address of a contiguous tensor."""
-        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
-            self._refuse(name, t, shape, dtype)
-        return t.data_ptr()
-
     def _input(self, name, t, shape):
         """Address and strides of q, k or v (0 for a dimension of size 1: it is never stepped along)."""
         if t.dtype != self._t16 or t.shape != shape or t.device != self.device:
@@ -89,24 +113,6 @@ class KVRows:
         if c != 1 and shape[0] > 0:
             raise ValueError(f"the elements of a head of {name} must be contiguous")
         return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
-
-    def _caches(self, k_cache, v_cache, block_table):
-        """(k, v, num_pages, block table, its stride)."""
-        num_pages, stride, table, shape = 0, 0, 0, self._cache_shape
-        if self.page_size:
-            if block_table is None:
-                raise ValueError("a paged cache needs its block_table")
-            num_pages = k_cache.shape[0]
-            shape = (num_pages, *shape[1:])
-            stride = block_table.shape[-1] if block_table.dim() == 2 else -1
-            table = self._whole("block_table", block_table, (self.Bsz, stride), torch.int32)
-        elif block_table is not None:
-            raise ValueError("these rows are of a contiguous cache")
-        return (self._whole("k_cache", k_cache, shape, self._kv), self._whole("v_cache", v_cache, shape, self._kv),
-                num_pages, table, stride)
-
-    def _status(self, status):
-        return 0 if status is None else self._whole("status", status, (1,), torch.int32)
 
     def append(self, q=None, k=None, v=None, k_cache=None, v_cache=None, *, q_norm=None, k_norm=None,
                q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, rope=None, positions=None,
