@@ -25,7 +25,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["fd_api.cpp", "fd_kernel_f16.cu", "fd_kernel_bf16.cu", "fd_kernel_f16_ffma.cu",
            "fd_kernel_bf16_ffma.cu", "fd_kernel_umma_f16.cu", "fd_kernel_umma_bf16.cu",
            "fd_kernel_kv4_f16.cu", "fd_kernel_kv4_bf16.cu", "fd_noalloc.cu", "fd_rows.cu",
-           "fd_tree.cu", "fd_tree_attn.cu"]
+           "fd_tree.cu", "fd_tree_16.cu", "fd_tree_8.cu", "fd_tree_4.cu"]
 
 
 def _nvcc() -> str:

@@ -62,8 +62,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // swizzle; the FFMA path loads whole unswizzled rows.
 int fd::encode_kv_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows,
                       const fd_plan_s* pl) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return FD_ERR_CUDA;
   const bool kv4 = pl->path == fd::kPathMmaKv4;
   const int rt = fd::row_tokens(pl->path);
   const cuuint64_t row = (cuuint64_t)fd::kv_row_bytes(pl->path, pl->d) * rt;
@@ -72,19 +70,26 @@ int fd::encode_kv_map(CUtensorMap* map, const void* base, int64_t rows, int box_
   const cuuint64_t strides[2] = {row, (cuuint64_t)pl->Hkv * row};
   const cuuint32_t box[3] = {(cuuint32_t)fd::box_cols_for(pl->path, pl->d), 1u,
                              (cuuint32_t)(box_rows / rt)};
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUtensorMapDataType ty = pl->dtype == FD_F16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : pl->dtype == FD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                  : kv4                  ? CU_TENSOR_MAP_DATA_TYPE_UINT64
                                                         : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const CUtensorMapSwizzle swz =
       fd::is_mma(pl->path) && !kv4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUresult r = enc(map, ty, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                   // 4-bit blocks start at multiples of 128 bytes only: 256-byte sectors would
-                   // fetch beyond them (the loads of 604 MB alone: 94 against 90 us).
-                   kv4 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  // 4-bit blocks start at multiples of 128 bytes only: 256-byte sectors would fetch beyond
+  // them (the loads of 604 MB alone: 94 against 90 us).
+  return encode_map(map, ty, base, dims, strides, box, swz,
+                    kv4 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+int fd::encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, const cuuint64_t (&dims)[3],
+                   const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle,
+                   CUtensorMapL2promotion promotion) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return FD_ERR_CUDA;
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = enc(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FD_OK : FD_ERR_CUDA;
 }
 

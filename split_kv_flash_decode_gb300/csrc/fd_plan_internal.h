@@ -27,6 +27,10 @@ namespace fd {
 // (9 d / 8 words, Hkv, blocks), `rows` and `box_rows` still in tokens.
 int encode_kv_map(CUtensorMap* map, const void* base, int64_t rows, int box_rows,
                   const fd_plan_s* pl);
+// Encode a 3-D tensor map with unit element strides (zeros out of bounds).
+int encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, const cuuint64_t (&dims)[3],
+               const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle,
+               CUtensorMapL2promotion promotion);
 // Token rows of the plan's contiguous cache.
 inline int64_t contiguous_rows(const fd_plan_s* pl) {
   return pl->path == kPathMmaKv4 ? pl->n_blocks * kBlockTokens : pl->n_tokens;

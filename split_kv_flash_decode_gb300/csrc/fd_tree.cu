@@ -1,5 +1,5 @@
 // A step of speculative decoding: the plan, the verdict on drafted tokens (fd_tree_verify) and the
-// rows that stand (fd_tree_keep).  The attention is in fd_tree_attn.cu.  See fd.h for the contract.
+// rows that stand (fd_tree_keep).  The attention is in fd_tree_attn.cuh.  See fd.h for the contract.
 #include "fd_tree.h"
 
 #include <algorithm>
@@ -8,6 +8,7 @@
 #include <new>
 
 #include "fd_kernel.cuh"
+#include "fd_plan_internal.h"
 
 namespace fd {
 namespace {
@@ -393,6 +394,26 @@ Span cache_span(const fd_tree_s* t, const void* p, int num_pages) {
 Span table_span(const fd_tree_s* t, const int32_t* table, int64_t bt_stride) {
   return span(table, 4 * ((t->B - 1) * bt_stride + t->max_pages));
 }
+// The 3-D view of a cache that the attention's loads take: (d, Hkv, rows); 16 bits in boxes of 64 columns with
+// the 128-byte swizzle, as the tensor cores read them, E4M3 in whole rows, 4 bits in whole blocks.
+int encode_cache(CUtensorMap* map, const fd_tree_s* t, const void* cache, int num_pages) {
+  const int kind = kv_kind(t->dtype), d = t->d, unit = kind == kKvE2m1 ? kBlockTokens : 1;
+  const cuuint64_t row = (cuuint64_t)cache_row_bytes(t->dtype, d) * unit;
+  const cuuint64_t dims[3] = {(cuuint64_t)(kind == kKvE2m1 ? 9 * d / 8 : d), (cuuint64_t)t->Hkv,
+                              (cuuint64_t)(cache_rows(t, num_pages) / unit)};
+  const cuuint64_t strides[2] = {row, row * t->Hkv};
+  const cuuint32_t box[3] = {(cuuint32_t)(kind == kKv16   ? 64
+                                          : kind == kKvE4m3 ? d
+                                                            : ring_row_bytes(kPathMmaKv4, d) * kBlockTokens / 8),
+                             1u, (cuuint32_t)(t->params.box_rows / unit)};
+  return encode_map(map,
+                    kind == kKvE4m3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                    : kind == kKvE2m1 ? CU_TENSOR_MAP_DATA_TYPE_UINT64
+                    : is_bf16(t->dtype) ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    cache, dims, strides, box, kind == kKv16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    kind == kKvE2m1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
 // Whether an output overlaps an input or another output.
 template <size_t N, size_t M>
 bool any_overlap(const Span (&outs)[N], const Span (&ins)[M]) {
@@ -447,24 +468,59 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
       return FD_ERR_CUDA;
     }
   }
+  // Units of work: the tiles of every item, and what an item costs beyond them.
+  const int G = Hq / Hkv;
+  int64_t units = 0, tiles = 0;
+  int rows = 0;
+  for (int b = 0; b < B; ++b) {
+    if (!drafts[b]) continue;
+    const int64_t items = (int64_t)Hkv * fd::tree_groups(drafts[b] * G);
+    units += items * (fd::tree_tiles(seqlens[b]) + fd::kTreeItemUnits);
+    tiles += items * fd::tree_tiles(seqlens[b]);
+    rows = std::max(rows, drafts[b] * G);
+  }
+  if (units >= limit) return FD_ERR_UNSUPPORTED;
   fd_tree_s* t = new (std::nothrow) fd_tree_s();
   if (!t) return FD_ERR_NOMEM;
   t->B = B; t->Hq = Hq; t->Hkv = Hkv; t->d = d; t->dtype = dtype; t->page_size = page_size;
-  t->max_pages = max_pages; t->max_drafts = max_drafts; t->num_sms = num_sms;
+  t->max_pages = max_pages; t->max_drafts = max_drafts;
   t->T = T; t->n_tokens = tokens; t->n_blocks = blocks;
   t->kv_bytes = (uint64_t)read * Hkv * 2 * fd::cache_row_bytes(dtype, d);
-  int32_t cu = 0;
+  fd::TreeParams& p = t->params;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = G;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
+  p.box_rows = page_size ? std::min(fd::kTreeTile, page_size) : fd::kTreeTile;
+  p.q_tiles = rows > fd::kTreeTile ? 2 : 1;
+  p.rec_rows = fd::kTreeTile * p.q_tiles;
+  p.ctas = (int)std::min<int64_t>({tiles, (int64_t)num_sms, (int64_t)fd::kTreeMaxCtas});
+  if (p.ctas) {
+    p.run_len = (int32_t)(units / p.ctas);
+    p.run_extra = (int32_t)(units % p.ctas);
+  }
+  int32_t cu = 0, unit = 0, cta = 1;
   int64_t base = 0;
   for (int b = 0; b < B; ++b) {
-    t->cu_q[b] = cu;
-    t->len[b] = seqlens[b];
-    t->base[b] = (int32_t)base;
+    p.cu_q[b] = cu;
+    p.len[b] = seqlens[b];
+    p.base[b] = (int32_t)base;
+    p.unit_base[b] = unit;
     cu += drafts[b];
     base += four ? ((int64_t)seqlens[b] + fd::kBlockTokens - 1) / fd::kBlockTokens * fd::kBlockTokens : seqlens[b];
+    if (!drafts[b]) continue;
+    // The runs that begin behind an item's first tile: the first of them combines the item's records.
+    const int items = Hkv * fd::tree_groups(drafts[b] * G), per = fd::tree_tiles(seqlens[b]) + fd::kTreeItemUnits;
+    int last = -1;
+    for (; cta < p.ctas && fd::tree_run_begin(p, cta) < unit + items * per; ++cta) {
+      const int at = fd::tree_run_begin(p, cta) - unit, item = at / per;
+      if (at - item * per <= fd::kTreeItemUnits || item == last) continue;
+      p.split[t->splits++] = (uint16_t)cta;
+      last = item;
+    }
+    unit += items * per;
   }
-  t->cu_q[B] = cu;
-  t->ctas = (int)(T * Hq);
-  t->ws_bytes = 0;
+  p.cu_q[B] = cu;
+  p.unit_base[B] = unit;
+  t->ws_bytes = t->splits ? sizeof(float) * 2 * p.ctas * (size_t)fd::tree_record_floats(d, p.rec_rows) : 0;
   *out_tree = t;
   return FD_OK;
 }
@@ -478,7 +534,7 @@ int fd_tree_get_info(fd_tree_t t, fd_tree_info* info) {
   if (!t || !info) return FD_ERR_INVALID;
   info->tokens = t->T;
   info->max_drafts = t->max_drafts;
-  info->ctas = t->ctas;
+  info->ctas = t->params.ctas;
   info->workspace_bytes = t->ws_bytes;
   info->kv_bytes = t->kv_bytes;
   return FD_OK;
@@ -493,7 +549,7 @@ int fd_tree_decode(fd_tree_t t, const void* q, const void* k, const void* v, int
   for (const void* p : {q, k, v, (const void*)out, (const void*)lse, (const void*)workspace})
     if (!fd::aligned(p, 16)) return FD_ERR_ALIGN;
   if (!fd::aligned(mask, 8) || !fd::aligned(block_table, 4) || !fd::aligned(status, 4)) return FD_ERR_ALIGN;
-  fd::TreeParams p;
+  fd::TreeParams p = t->params;  // per-call copy: the handle stays immutable
   int rc = fd::check_pages(t, num_pages, block_table, bt_stride, &p.page_shift);
   if (rc != FD_OK) return rc;
   const int64_t rows = t->T * t->Hq;
@@ -502,14 +558,18 @@ int fd_tree_decode(fd_tree_t t, const void* q, const void* k, const void* v, int
   const fd::Span ins[] = {fd::span(q, 2 * rows * t->d), fd::cache_span(t, k, num_pages), fd::cache_span(t, v, num_pages),
                           fd::span(mask, 8 * t->T), fd::table_span(t, block_table, bt_stride)};
   if (fd::any_overlap(outs, ins)) return FD_ERR_INVALID;
-  p.q = q; p.k = k; p.v = v; p.mask = mask; p.out = out; p.lse = lse; p.status = status;
+  rc = fd::encode_cache(&p.tm_k, t, k, num_pages);
+  if (rc == FD_OK) rc = fd::encode_cache(&p.tm_v, t, v, num_pages);
+  if (rc != FD_OK) return rc;
+  p.q = q; p.mask = mask; p.out = out; p.lse = lse; p.status = status;
+  p.part = static_cast<float*>(workspace);
   p.block_table = block_table; p.bt_stride = bt_stride; p.num_pages = num_pages;
-  p.B = t->B; p.Hq = t->Hq; p.Hkv = t->Hkv;
-  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)t->d));
-  std::memcpy(p.cu_q, t->cu_q, sizeof(p.cu_q));
-  std::memcpy(p.len, t->len, sizeof(p.len));
-  std::memcpy(p.base, t->base, sizeof(p.base));
-  if (fd::launch_tree(p, t->dtype, t->d, (int)t->T, stream) != cudaSuccess) {
+  const int kind = fd::kv_kind(t->dtype);
+  const bool bf16 = fd::is_bf16(t->dtype);
+  const cudaError_t err = kind == fd::kKv16     ? fd::launch_tree_16(p, bf16, t->d, t->splits, stream)
+                          : kind == fd::kKvE4m3 ? fd::launch_tree_8(p, t->d, t->splits, stream)
+                                                : fd::launch_tree_4(p, bf16, t->d, t->splits, stream);
+  if (err != cudaSuccess) {
     cudaGetLastError();
     return FD_ERR_CUDA;
   }
@@ -539,7 +599,7 @@ int fd_tree_verify(fd_tree_t t, const float* target, int64_t target_stride, cons
   p.path = path; p.emitted = emitted; p.count = count;
   p.vocab = vocab;
   p.max_drafts = t->max_drafts;
-  std::memcpy(p.cu, t->cu_q, sizeof(p.cu));
+  std::memcpy(p.cu, t->params.cu_q, sizeof(p.cu));
   return fd::launch(reinterpret_cast<const void*>(&fd::fd_verify_kernel), dim3(t->B * fd::kVerifyCluster),
                     fd::kVerifyThreads, &p, stream);
 }
@@ -566,9 +626,9 @@ int fd_tree_keep(fd_tree_t t, void* k_cache, void* v_cache, int num_pages, const
   const int kind = fd::kv_kind(t->dtype);
   p.pieces = kind == fd::kKvE2m1 ? t->Hkv * (t->d / 8 + t->d / 16)
                                  : (int)(t->Hkv * fd::cache_row_bytes(t->dtype, t->d) / 16);
-  std::memcpy(p.cu, t->cu_q, sizeof(p.cu));
-  std::memcpy(p.base, t->base, sizeof(p.base));
-  for (int b = 0; b < t->B; ++b) p.first[b] = t->len[b] - (t->cu_q[b + 1] - t->cu_q[b]);
+  std::memcpy(p.cu, t->params.cu_q, sizeof(p.cu));
+  std::memcpy(p.base, t->params.base, sizeof(p.base));
+  for (int b = 0; b < t->B; ++b) p.first[b] = t->params.len[b] - (p.cu[b + 1] - p.cu[b]);
   const dim3 grid(2 * ((p.pieces + fd::kKeepThreads - 1) / fd::kKeepThreads), t->B);
   const void* fn = kind == fd::kKv16     ? reinterpret_cast<const void*>(&fd::fd_keep_kernel<fd::kKv16>)
                    : kind == fd::kKvE4m3 ? reinterpret_cast<const void*>(&fd::fd_keep_kernel<fd::kKvE4m3>)

@@ -1,37 +1,82 @@
-// Internal definitions of a step of speculative decoding: the handle and the attention's parameters.
+// Internal definitions of a step of speculative decoding: the handle, and what the host and the
+// attention's kernels (fd_tree_attn.cuh) share.
 #pragma once
 
 #include "fd_common.h"
 #include "fd_host.h"
 
-struct fd_tree_s {
-  int B, Hq, Hkv, d, dtype, page_size, max_pages, max_drafts, num_sms;
-  int64_t T, n_tokens, n_blocks;
-  uint64_t kv_bytes;
-  int32_t cu_q[FD_MAX_BATCH + 1];  // prefix sums of drafts
-  int32_t len[FD_MAX_BATCH];       // L_b
-  int32_t base[FD_MAX_BATCH];      // contiguous caches: cache row (in tokens) of the sequence's row 0
-  int ctas;
-  size_t ws_bytes;
-};
-
 namespace fd {
 
+constexpr int kTreeTile = 128;    // tokens of a tile, and query rows of one
+constexpr int kTreeRows = 256;    // query rows that stream the cache together: two tiles
+constexpr int kTreeMaxCtas = 512;
+// What an item (a sequence's KV head and up to kTreeRows of its query rows) costs a CTA beyond its tiles, in tiles.
+constexpr int kTreeItemUnits = 2;
+
+// One CTA: operand tiles in the 16-bit swizzled layout (Q, then K and V in a ring of slots); over 8- and 4-bit
+// caches a second ring of the rows as they are stored, which converter warps widen into the operand slots.
+FD_HD constexpr int tree_operand_bytes(int d) { return kTreeTile * d * 2; }
+FD_HD constexpr int tree_raw_bytes(int kv, int d) {
+  return kv == kKvE2m1 ? kTreeTile * ring_row_bytes(kPathMmaKv4, d) : kTreeTile * d;
+}
+constexpr int kTreeSmemTiles = 224 * 1024;
+constexpr int kTreeMaxSlots = 14;
+FD_HD constexpr int tree_slots(int kv, int d, int q_tiles) {
+  return kv == kKv16 ? kTreeSmemTiles / tree_operand_bytes(d) - q_tiles : d == 128 ? 5 - q_tiles : 4;
+}
+FD_HD constexpr int tree_raw_slots(int kv, int d, int q_tiles) {
+  return kv == kKv16 ? 0
+         : (kTreeSmemTiles - (q_tiles + tree_slots(kv, d, q_tiles)) * tree_operand_bytes(d)) / tree_raw_bytes(kv, d) > 12
+             ? 12
+             : (kTreeSmemTiles - (q_tiles + tree_slots(kv, d, q_tiles)) * tree_operand_bytes(d)) / tree_raw_bytes(kv, d);
+}
+// After the tiles: barriers, flags, the query rows' scales.
+constexpr int kTreeMetaBytes = 2048;
+constexpr int kTreeSmemBytes = kTreeSmemTiles + kTreeMetaBytes;
+
+// Floats of a CTA's partial record of `rows` query rows: m, l, then O as [d / 4][rows][4].
+FD_HD constexpr int64_t tree_record_floats(int d, int rows) { return (int64_t)rows * (d + 2); }
+
 struct TreeParams {
-  const void *q, *k, *v;
+  CUtensorMap tm_k, tm_v;  // 3-D views of the caches; a box holds whole rows (16 bits: 64 columns of them)
+  const void* q;
   const uint64_t* mask;
   void* out;
   float* lse;
+  float* part;             // records: two per CTA (the item it goes on with, the item it leaves unfinished)
   uint32_t* status;
   const int32_t* block_table;
   int32_t bt_stride, page_shift, num_pages;
-  int32_t B, Hq, Hkv;
-  float scale_log2;  // log2(e) / sqrt(d)
+  int32_t box_rows;        // tokens of a box: a tile, or a page that is smaller
+  int32_t B, Hq, Hkv, G;
+  int32_t q_tiles;         // 1 or 2 tiles of query rows at most in an item
+  int32_t rec_rows;        // kTreeTile x q_tiles
+  int32_t ctas, run_len, run_extra;  // units per CTA; the first run_extra CTAs take one more
+  float scale_log2;        // log2(e) / sqrt(d)
   int32_t cu_q[FD_MAX_BATCH + 1];
   int32_t len[FD_MAX_BATCH];
-  int32_t base[FD_MAX_BATCH];
+  int32_t base[FD_MAX_BATCH];           // contiguous caches: cache row (in tokens) of the sequence's row 0
+  int32_t unit_base[FD_MAX_BATCH + 1];  // prefix sums of units: items x (tiles + kTreeItemUnits)
+  uint16_t split[kTreeMaxCtas];         // CTAs whose run begins within an item, the first one of each item
 };
 
-cudaError_t launch_tree(const TreeParams& p, int dtype, int d, int T, cudaStream_t s);
+FD_HD int tree_groups(int rows) { return (rows + kTreeRows - 1) / kTreeRows; }
+FD_HD int tree_tiles(int L) { return (int)(((int64_t)L + kTreeTile - 1) / kTreeTile); }
+FD_HD int tree_run_begin(const TreeParams& p, int cta) {
+  return cta * p.run_len + (cta < p.run_extra ? cta : p.run_extra);
+}
+
+// The attention, and the combination of the records of `splits` items.
+cudaError_t launch_tree_16(const TreeParams& p, bool bf16, int d, int splits, cudaStream_t s);
+cudaError_t launch_tree_8(const TreeParams& p, int d, int splits, cudaStream_t s);
+cudaError_t launch_tree_4(const TreeParams& p, bool bf16, int d, int splits, cudaStream_t s);
 
 }  // namespace fd
+
+struct fd_tree_s {
+  int B, Hq, Hkv, d, dtype, page_size, max_pages, max_drafts, splits;
+  int64_t T, n_tokens, n_blocks;
+  uint64_t kv_bytes;
+  size_t ws_bytes;
+  fd::TreeParams params;  // pointers and maps filled per call
+};

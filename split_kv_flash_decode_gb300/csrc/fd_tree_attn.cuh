@@ -1,0 +1,754 @@
+// Attention of drafted tokens over the cache (fd_tree_decode) on the fifth-generation tensor cores.
+//
+// All query rows of a (sequence, KV head), its drafted tokens times the heads of its group, meet every K and V
+// row, so the work is two matrix products per tile of 128 tokens: S = Q K^T (rows on M, tokens on N) and
+// O += P V, with the online softmax between them.  A row is a lane of tensor memory and belongs to one
+// thread: no shuffle is needed for its maximum or its sum.  Rows are padded to 128, which costs nothing
+// while HBM is the bound (the two products of a tile take a third of the time that its bytes take).
+//
+// One CTA per SM runs through an equal share of the tiles of all items (an item: a KV head of a sequence and up
+// to 256 of its query rows).  Two groups of four softmax warps work in turn, so that the tensor cores have one
+// group's products while the other computes its weights: they take the two row tiles of an item, or, of an
+// item with one row tile, alternate tiles of tokens, whose two results they merge at its end.  An item that
+// several CTAs share leaves fp32 records (m, l, O), which a second launch combines: no CTA waits for
+// another.  (The records of an item that one CTA had alone are never written.)
+//
+// Warps: 0-3 and 4-7 softmax, 8 issues the products, 9 the TMA loads, and over 8- and 4-bit caches 10 on widen
+// the stored rows to fp16 in the layout that the products read.
+#pragma once
+
+#include "fd_kernel.cuh"
+#include "fd_tree.h"
+
+namespace fd {
+namespace tree {
+
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvertWarp = 10;
+FD_HD constexpr int convert_warps(int kv) { return kv == kKv16 ? 0 : 4; }
+FD_HD constexpr int threads(int kv) { return 32 * (kConvertWarp + convert_warps(kv)); }
+// Tensor memory: S (and P in its place) of the two groups, then their O.
+constexpr uint32_t kTmemAll = 512, kTmemS = 128, kTmemO = 256;
+constexpr int kMaxOperandSlots = 4;  // of 8- and 4-bit caches
+
+// ------------------------------------------------------------------ primitives
+
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]; A's 16-bit elements lie in pairs, row by row in the lanes.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ the work of a CTA
+
+// Tiles [tile0, tile0 + nt) of an item.
+struct Portion {
+  int b, kvh, r0, rows, n, L, tile0, nt, slot;
+  bool two;    // two row tiles; else one, and the groups take alternate tiles of tokens
+  bool whole;  // all tiles of the item
+  int row_tile;  // rows of a row tile
+  __device__ __forceinline__ int jobs() const { return two ? 2 * nt : nt; }
+  __device__ __forceinline__ int tile_of(int job) const { return two ? job >> 1 : job; }
+  // Places of a tile's K and V among the portion's 2 nt loads: in the order in which the products want them.
+  __device__ __forceinline__ int seq_k(int t) const { return two ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
+  __device__ __forceinline__ int seq_v(int t) const { return two || t == nt - 1 ? 2 * t + 1 : 2 * t + 2; }
+  // The tile and kind of load s.
+  __device__ __forceinline__ bool is_v(int s) const { return two || s == 2 * nt - 1 ? s & 1 : s != 0 && !(s & 1); }
+  __device__ __forceinline__ int load_tile(int s) const {
+    return two || s == 2 * nt - 1 ? s >> 1 : s == 0 ? 0 : s & 1 ? (s + 1) >> 1 : (s >> 1) - 1;
+  }
+};
+
+// The portions of a run of units, in order; the same in every warp.
+struct Cursor {
+  int u, u1, b;
+  __device__ __forceinline__ Cursor(const TreeParams& p, int cta) {
+    u = tree_run_begin(p, cta);
+    u1 = tree_run_begin(p, cta + 1);
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.unit_base[mid] <= u) lo = mid; else hi = mid;
+    }
+    b = lo;
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p, Portion& o) {
+    while (u < u1) {
+      while (p.unit_base[b + 1] <= u) ++b;
+      o.b = b;
+      o.L = p.len[b];
+      o.n = p.cu_q[b + 1] - p.cu_q[b];
+      const int tiles = tree_tiles(o.L), per = tiles + kTreeItemUnits, rows = o.n * p.G, groups = tree_groups(rows);
+      const int at = u - p.unit_base[b], item = at / per, off = at - item * per;
+      const int end = min(u1 - u + off, per);
+      u += end - off;
+      const int lo = max(0, off - kTreeItemUnits), hi = max(0, end - kTreeItemUnits);
+      if (hi <= lo) continue;
+      o.kvh = item / groups;
+      o.r0 = (item - o.kvh * groups) * kTreeRows;
+      o.rows = min(rows - o.r0, kTreeRows);
+      o.two = o.rows > kTreeTile;
+      o.row_tile = o.two ? (o.rows / 2 + 31) / 32 * 32 : kTreeTile;
+      if (o.two && o.row_tile * 2 < o.rows) o.row_tile += 32;
+      o.tile0 = lo;
+      o.nt = hi - lo;
+      o.whole = lo == 0 && hi == tiles;
+      o.slot = lo > 0 ? 0 : 1;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Nodes of a sequence as bits.
+__device__ __forceinline__ uint64_t all_nodes(int n) { return n >= 64 ? ~0ull : (1ull << n) - 1; }
+// Of a tile's columns 32 k .. 32 k + 31, those that a token sees: the columns before `off`, where the drafted rows
+// begin, and the nodes of its mask behind.
+__device__ __forceinline__ uint32_t seen(uint64_t mask, int off, int k) {
+  const int lim = off - 32 * k;
+  uint32_t v = lim >= 32 ? ~0u : lim > 0 ? (1u << lim) - 1 : 0u;
+  if (lim <= 0 && lim > -64) v |= (uint32_t)(mask >> -lim);
+  else if (lim > 0 && lim < 32) v |= (uint32_t)(mask << lim);
+  return v;
+}
+// The nodes that any token of the sequence sees, by a whole warp.
+__device__ __forceinline__ uint64_t seen_by_any(const TreeParams& p, int b, int n) {
+  if (p.mask == nullptr) return all_nodes(n);
+  const int lane = threadIdx.x & 31;
+  uint64_t m = lane < n ? p.mask[p.cu_q[b] + lane] : 0;
+  if (lane + 32 < n) m |= p.mask[p.cu_q[b] + lane + 32];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m |= __shfl_xor_sync(0xffffffffu, m, off);
+  return m & all_nodes(n);
+}
+
+// Waits for a barrier's phase.  Where that takes over a second the CTA is given up: the status word says so, and
+// no later wait of the CTA waits.
+struct Waiter {
+  volatile int* dead;
+  uint32_t* status;
+  __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
+    if (dev::mbar_try_wait(bar, parity)) return;
+    slow(bar, parity);
+  }
+  __device__ __noinline__ void slow(uint32_t bar, uint32_t parity) const {
+    const uint64_t start = dev::global_timer_ns();
+    while (!*dead) {
+#pragma unroll 1
+      for (int i = 0; i < 64; ++i)
+        if (dev::mbar_try_wait(bar, parity)) return;
+      if (dev::global_timer_ns() - start > dev::kWaitLimitNs) {
+        *dead = 1;
+        if (status != nullptr) atomicOr(status, FD_TREE_TIMEOUT);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ the kernel
+
+template <typename T, int D, int KV>
+__global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_constant__ TreeParams p) {
+  // Operands: bf16 over a bf16 cache, else fp16.
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value && KV == kKv16;
+  using Op = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+  constexpr bool kScaledQ = std::is_same<T, __nv_bfloat16>::value && !kBf16;
+  constexpr int kOperand = tree_operand_bytes(D), kRaw = tree_raw_bytes(KV, D), kHalf = kTreeTile * 128;
+  constexpr int CPR = D / 8;  // 16-byte chunks of a row
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int q_tiles = p.q_tiles, nslot = tree_slots(KV, D, q_tiles), nraw = tree_raw_slots(KV, D, q_tiles);
+  uint8_t* slots = smem + q_tiles * kOperand;
+  uint8_t* raws = slots + nslot * kOperand;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTreeSmemTiles);
+  // The loads' ring (16 bits: the operand slots themselves), then the operand slots of other caches.
+  const uint32_t full0 = dev::smem_addr(bars), empty0 = full0 + 8 * kTreeMaxSlots;
+  const uint32_t wide0 = empty0 + 8 * kTreeMaxSlots;
+  const uint32_t op_full0 = KV == kKv16 ? full0 : wide0;
+  const uint32_t op_empty0 = KV == kKv16 ? empty0 : wide0 + 8 * kMaxOperandSlots;
+  const uint32_t s_full0 = wide0 + 16 * kMaxOperandSlots, p_ready0 = s_full0 + 16, o_full0 = p_ready0 + 16,
+                 q_ready = o_full0 + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kTreeSmemTiles + 400);
+  int* dead = reinterpret_cast<int*>(smem + kTreeSmemTiles + 404);
+  float* q_scale = reinterpret_cast<float*>(smem + kTreeSmemTiles + 512);  // [kTreeRows]
+  static_assert(8 * (2 * kTreeMaxSlots + 2 * kMaxOperandSlots + 7) <= 400, "barriers");
+  const int nload = KV == kKv16 ? nslot : nraw;  // slots of the loads' ring
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  dev::pdl_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < nload; ++s) {
+      dev::mbar_init(full0 + 8 * s, 1);
+      dev::mbar_init(empty0 + 8 * s, KV == kKv16 ? 1 : convert_warps(KV));
+    }
+    if (KV != kKv16)
+      for (int s = 0; s < nslot; ++s) {
+        dev::mbar_init(op_full0 + 8 * s, convert_warps(KV));
+        dev::mbar_init(op_empty0 + 8 * s, 1);
+      }
+    for (int w = 0; w < 2; ++w) {
+      dev::mbar_init(s_full0 + 8 * w, 1);
+      dev::mbar_init(p_ready0 + 8 * w, 4);
+      dev::mbar_init(o_full0 + 8 * w, 1);
+    }
+    dev::mbar_init(q_ready, 8);
+    dev::fence_mbar_init();
+    *dead = 0;
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(dev::smem_addr(tmem_slot), kTmemAll);
+    tc::tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    dev::prefetch_tensormap(&p.tm_k);
+    dev::prefetch_tensormap(&p.tm_v);
+  }
+  dev::pdl_wait();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const Waiter wait{dead, p.status};
+  Cursor cur(p, blockIdx.x);
+  Portion o;
+
+  if (warp == kLoadWarp) {
+    // ---------------- loads: a lane issues a box (a page's rows, or half the columns)
+    const uint64_t policy = dev::l2_evict_first_policy();
+    constexpr int NBOX = KV == kKv16 ? D / 64 : 1;
+    constexpr int kUnit = KV == kKvE2m1 ? kBlockTokens : 1;
+    constexpr int kLoadBytes = KV == kKv16 ? kOperand : kRaw;
+    constexpr int kBoxRow = KV == kKv16 ? 128 : kRaw / kTreeTile;  // bytes of a token's row in a box
+    const int pieces = kTreeTile / p.box_rows, boxes = pieces * NBOX;
+    int i = 0;
+    while (cur.next(p, o)) {
+      for (int s = 0; s < 2 * o.nt; ++s, ++i) {
+        const int slot = i % nload;
+        const int t0 = (o.tile0 + o.load_tile(s)) * kTreeTile;
+        int row = 0;
+        const int piece = lane / NBOX, bx = lane - piece * NBOX, r = piece * p.box_rows;
+        if (lane < boxes) {
+          if (p.block_table == nullptr) {
+            row = p.base[o.b] + t0;
+          } else {
+            // Boxes past the end of the sequence reload its last page; an index outside the pool reads zeros.
+            const int pg = min((t0 + r) >> p.page_shift, (o.L - 1) >> p.page_shift);
+            const uint32_t page = (uint32_t)p.block_table[(int64_t)o.b * p.bt_stride + pg];
+            row = (int)(min(page, (uint32_t)p.num_pages) << p.page_shift) + ((t0 + r) & ((1 << p.page_shift) - 1));
+            if (page >= (uint32_t)p.num_pages) row = p.num_pages << p.page_shift;
+          }
+        }
+        if (i >= nload) wait(empty0 + 8 * slot, (i / nload - 1) & 1);
+        if (*(volatile int*)dead) continue;
+        if (lane == 0) dev::mbar_arrive_expect_tx(full0 + 8 * slot, kLoadBytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const uint32_t dst = dev::smem_addr(KV == kKv16 ? slots + slot * kOperand : raws + slot * kRaw);
+          dev::tma_load_3d(dst + bx * kHalf + r * kBoxRow, o.is_v(s) ? &p.tm_v : &p.tm_k, bx * 64, o.kvh, row / kUnit,
+                           full0 + 8 * slot, policy);
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- products, issued by one lane
+    if (lane == 0) {
+      constexpr uint32_t kIdS = tc::idesc_f16(kBf16, false, false, kTreeTile, kTreeTile);
+      constexpr uint32_t kIdO = tc::idesc_f16(kBf16, false, true, kTreeTile, D);
+      const uint32_t q0 = dev::smem_addr(smem), slot0 = dev::smem_addr(slots);
+      uint32_t base = 0, q_phase = 0, p_phase[2] = {0, 0};
+      while (cur.next(p, o)) {
+        const int jobs = o.jobs();
+        wait(q_ready, q_phase & 1);
+        ++q_phase;
+        tc::fence_after_sync();
+        auto scores = [&](int j) {
+          const int w = j & 1, t = o.tile_of(j);
+          const uint32_t i = base + o.seq_k(t), slot = i % nslot;
+          wait(op_full0 + 8 * slot, (i / nslot) & 1);
+          tc::fence_after_sync();
+          const uint32_t qa = q0 + (o.two ? w * kOperand : 0), ka = slot0 + slot * kOperand;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_f16_ss(tmem + w * kTmemS, tc::smem_desc(qa + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024, tc::kSwizzle128B),
+                           tc::smem_desc(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024, tc::kSwizzle128B), kIdS, kk > 0);
+          tc::commit(s_full0 + 8 * w);
+          if (!o.two || w == 1) tc::commit(op_empty0 + 8 * slot);
+        };
+        scores(0);
+        if (jobs > 1) scores(1);
+        for (int j = 0; j < jobs; ++j) {
+          const int w = j & 1, t = o.tile_of(j);
+          const uint32_t i = base + o.seq_v(t), slot = i % nslot;
+          wait(p_ready0 + 8 * w, p_phase[w] & 1);
+          ++p_phase[w];
+          wait(op_full0 + 8 * slot, (i / nslot) & 1);
+          tc::fence_after_sync();
+          const uint32_t va = slot0 + slot * kOperand, ps = tmem + w * kTmemS, od = tmem + kTmemO + w * kTmemS;
+#pragma unroll
+          for (int kk = 0; kk < kTreeTile / 16; ++kk) {
+            const uint64_t vd = tc::smem_desc(va + kk * 2048, kHalf, 1024, tc::kSwizzle128B);
+            mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8, vd, kIdO, j > 1 || kk > 0);
+            if (kBf16) mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8 + 16, vd, kIdO, 1u);
+          }
+          if (!o.two || w == 1) tc::commit(op_empty0 + 8 * slot);
+          if (j + 2 >= jobs) tc::commit(o_full0 + 8 * w);
+          else scores(j + 2);
+        }
+        base += 2 * o.nt;
+      }
+    }
+    __syncwarp();
+  } else if (warp < kMmaWarp) {
+    // ---------------- softmax
+    const int w = warp >> 2, wl = tid & 127;             // group, and thread in it: the row in its tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + w * kTmemS, to = tmem + lanes + kTmemO + w * kTmemS;
+    uint32_t base = 0, s_phase = 0, o_phase[2] = {0, 0};
+    while (cur.next(p, o)) {
+      const int jobs = o.jobs(), G = p.G;
+      // Q: the rows of the item's tokens and heads, rows past the last one left as they are (they meet nobody).
+      for (int c = tid; c < o.rows * CPR; c += 256) {
+        const int gr = c / CPR, ch = c - gr * CPR, R = o.r0 + gr, t = R / G;
+        uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.q) +
+                      ((int64_t)(p.cu_q[o.b] + t) * p.Hq + o.kvh * G + (R - t * G)) * D + ch * 8);
+        if constexpr (kScaledQ) {
+          // bf16 into fp16 by a power of two for each row that brings its largest value below 2^15.
+          float f[8];
+          dev::unpack8<T>(x, f);
+          float m = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
+#pragma unroll
+          for (int off = 1; off < CPR; off <<= 1) m = fmaxf(m, __shfl_xor_sync(__activemask(), m, off));
+          const int e = (int)(__float_as_uint(m) >> 23);        // 2^(e - 127) <= m
+          const int up = e == 0 || e == 255 ? 0 : min(max(141 - e, -100), 100);
+          const float s = __int_as_float((127 + up) << 23);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] *= s;
+          x = make_uint4(dev::pack2<__half>(f[0], f[1]), dev::pack2<__half>(f[2], f[3]), dev::pack2<__half>(f[4], f[5]),
+                         dev::pack2<__half>(f[6], f[7]));
+          if (ch == 0) q_scale[gr] = __int_as_float((127 - up) << 23);
+        }
+        const int tile = o.two && gr >= o.row_tile ? 1 : 0, r = gr - tile * o.row_tile;
+        *reinterpret_cast<uint4*>(smem + tile * kOperand + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(q_ready);
+      if (kScaledQ) tc::named_sync(1, 256);
+
+      const int gr = (o.two ? w * o.row_tile : 0) + wl;   // row of the item
+      const int rows_here = o.two ? (w ? o.rows - o.row_tile : min(o.rows, o.row_tile)) : o.rows;
+      const bool mine = wl < rows_here;
+      const bool busy = (wl & ~31) < rows_here;           // this warp has rows
+      const int R = o.r0 + gr, t = mine ? R / G : 0;
+      const uint64_t nodes = all_nodes(o.n);
+      uint64_t mask = 0;
+      if (mine) mask = p.mask != nullptr ? p.mask[p.cu_q[o.b] + t] & nodes : all_nodes(t + 1);
+      uint64_t any = nodes;
+      if (KV == kKv16) any = seen_by_any(p, o.b, o.n);
+      const float scale = kScaledQ && mine ? p.scale_log2 * q_scale[gr] : p.scale_log2;
+      float m = -INFINITY, l = 0.f;
+      for (int j = w; j < jobs; j += 2) {
+        const int tile = o.tile_of(j), off = o.L - o.n - (o.tile0 + tile) * kTreeTile;  // columns before the drafted rows
+        const bool edge = off < kTreeTile;
+        wait(s_full0 + 8 * w, s_phase & 1);
+        ++s_phase;
+        tc::fence_after_sync();
+        if (busy) {
+          uint32_t x[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, x + 32 * c);
+          tc::wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t v = seen(mask, off, c);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(v >> k & 1)) x[32 * c + k] = 0xff800000u;
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 128; k += 8)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(x[k + 2 * c]), __uint_as_float(x[k + 2 * c + 1])));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+          // A row's maximum in use moves only when it grew by more than 2^8, which is rare.
+          const bool grew = mine && top > m + dev::kRescaleThreshold;
+          if (__any_sync(0xffffffffu, grew)) {
+            const float coef = !grew ? 1.f : m == -INFINITY ? 0.f : dev::ex2(m - top);
+            if (grew) m = top;
+            l *= coef;
+            if (j > 1) {  // the group's earlier products are done: this tile's scores were committed behind them
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t y[32];
+                ld32(to + c, y);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * coef);
+                st32(to + c, y);
+              }
+            }
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              // Product, then difference: the largest score minus the maximum in use is then exact.
+              const float a = dev::ex2(__fmul_rn(__uint_as_float(x[32 * c + 2 * k]), scale) - mm);
+              const float b = dev::ex2(__fmul_rn(__uint_as_float(x[32 * c + 2 * k + 1]), scale) - mm);
+              sum[(2 * k) & 3] += a;
+              sum[(2 * k + 1) & 3] += b;
+              y[k] = dev::pack2<Op>(a, b);
+              if constexpr (kBf16) {
+                const float2 h = dev::Elem<Op>::to_f2(y[k]);
+                y[16 + k] = dev::pack2<Op>(a - h.x, b - h.y);
+              }
+            }
+            // The weights lie where their scores lay: the scores are all read.
+            if constexpr (kBf16) st32(ts + 32 * c, y);
+            else st16(ts + 32 * c, y);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc::wait_st();
+        }
+        if (KV == kKv16 && edge) {
+          // V rows that no token sees (behind the sequence, of padding nodes) become 0: a weight of 0 times what they
+          // hold could be NaN.
+          const uint32_t i = base + o.seq_v(tile), slot = i % nslot;
+          wait(op_full0 + 8 * slot, (i / nslot) & 1);
+          uint8_t* vs = slots + slot * kOperand;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t gone = ~seen(any, off, c);
+            for (; gone != 0; gone &= gone - 1) {
+              const int row = 32 * c + __ffs(gone) - 1;
+              if (wl < CPR) *reinterpret_cast<uint4*>(vs + (wl >> 3) * kHalf + row * 128 + (wl & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          tc::fence_proxy_async_smem();
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(p_ready0 + 8 * w);
+      }
+
+      // The item's end (or this CTA's share of it).
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (k < jobs) {
+          wait(o_full0 + 8 * k, o_phase[k] & 1);
+          ++o_phase[k];
+        }
+      tc::fence_after_sync();
+      float c0 = 1.f, c1 = 0.f;
+      int col0 = 0, col1 = D;
+      if (!o.two) {
+        // The groups' results of alternate tiles: each takes half the columns of both.
+        float* ml = reinterpret_cast<float*>(smem);       // in Q's place: its products are done
+        ml[w * 256 + 2 * wl] = m;
+        ml[w * 256 + 2 * wl + 1] = l;
+        tc::named_sync(1, 256);
+        const float m0 = ml[2 * wl], l0 = ml[2 * wl + 1], m1 = ml[256 + 2 * wl], l1 = ml[256 + 2 * wl + 1];
+        m = fmaxf(m0, m1);
+        c0 = m0 == -INFINITY ? 0.f : dev::ex2(m0 - m);
+        c1 = m1 == -INFINITY ? 0.f : dev::ex2(m1 - m);
+        l = c0 * l0 + c1 * l1;
+        col0 = w * (D / 2);
+        col1 = col0 + D / 2;
+      }
+      if (busy) {
+        const uint32_t o0 = tmem + lanes + kTmemO + (o.two ? w * kTmemS : 0), o1 = tmem + lanes + kTmemO + kTmemS;
+        const bool both = !o.two && jobs > 1;
+        float* rec = p.part + (int64_t)(2 * blockIdx.x + o.slot) * tree_record_floats(D, p.rec_rows);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t out_row = (int64_t)(p.cu_q[o.b] + t) * p.Hq + o.kvh * G + (R - t * G);
+#pragma unroll 1
+        for (int c = col0; c < col1; c += 32) {
+          uint32_t y[32];
+          float f[32];
+          ld32(o0 + c, y);
+          tc::wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) f[k] = c0 != 0.f || o.two ? __uint_as_float(y[k]) * c0 : 0.f;
+          if (both) {
+            ld32(o1 + c, y);
+            tc::wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) f[k] = c1 != 0.f ? fmaf(__uint_as_float(y[k]), c1, f[k]) : f[k];
+          }
+          if (!mine) continue;
+          if (o.whole) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint4 v;
+              v.x = dev::pack2<T>(f[k] * inv, f[k + 1] * inv);
+              v.y = dev::pack2<T>(f[k + 2] * inv, f[k + 3] * inv);
+              v.z = dev::pack2<T>(f[k + 4] * inv, f[k + 5] * inv);
+              v.w = dev::pack2<T>(f[k + 6] * inv, f[k + 7] * inv);
+              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + out_row * D + c + k) = v;
+            }
+          } else {
+            // Column by column: the rows of a warp lie together.
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              __stcg(reinterpret_cast<float4*>(rec + 2 * p.rec_rows) + (int64_t)((c + k) / 4) * p.rec_rows + gr,
+                     make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]));
+          }
+        }
+        if (mine && col0 == 0) {
+          if (!o.whole) {
+            __stcg(rec + gr, m);
+            __stcg(rec + p.rec_rows + gr, l);
+          } else if (p.lse != nullptr) {
+            p.lse[out_row] = l > 0.f ? fmaf(m, dev::kLn2, logf(l)) : l == 0.f ? -INFINITY : l;
+          }
+        }
+      }
+      tc::fence_before_sync();
+      tc::named_sync(1, 256);  // O and the exchanged sums are read; Q may be written
+      base += 2 * o.nt;
+    }
+  } else {
+    // ---------------- widening of 8- and 4-bit rows
+    if constexpr (KV != kKv16) {
+      constexpr int NC = 32 * convert_warps(KV);
+      const int ct = tid - 32 * kConvertWarp;
+      uint32_t i = 0;
+      while (cur.next(p, o)) {
+        const uint64_t any = seen_by_any(p, o.b, o.n);
+        for (int s = 0; s < 2 * o.nt; ++s, ++i) {
+          const uint32_t raw = i % nraw, slot = i % nslot;
+          const bool is_v = o.is_v(s);
+          const int off = o.L - o.n - (o.tile0 + o.load_tile(s)) * kTreeTile;
+          const bool edge = is_v && off < kTreeTile;      // V rows that no token sees become 0
+          wait(full0 + 8 * raw, (i / nraw) & 1);
+          if (i >= (uint32_t)nslot) wait(op_empty0 + 8 * slot, (i / nslot - 1) & 1);
+          const uint8_t* src = raws + raw * kRaw;
+          uint8_t* dst = slots + slot * kOperand;
+          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+          if (edge)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) vis[c] = seen(any, off, c);
+          auto put = [&](int row, int ch, uint4 y) {
+            const uint32_t v = row < 64 ? (row < 32 ? vis[0] : vis[1]) : (row < 96 ? vis[2] : vis[3]);
+            if (!(v >> (row & 31) & 1)) y = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * kHalf + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = y;
+          };
+          if constexpr (KV == kKvE4m3) {
+#pragma unroll 4
+            for (int c = ct; c < kTreeTile * CPR; c += NC) {
+              const int row = c / CPR, ch = c - row * CPR;
+              const uint2 x = *reinterpret_cast<const uint2*>(src + row * D + 8 * ch);
+              uint4 y;
+              dev::e4m3x4_to_f16x4(x.x, y.x, y.y);
+              dev::e4m3x4_to_f16x4(x.y, y.z, y.w);
+              put(row, ch, y);
+            }
+          } else {
+            constexpr int kBlock = kRaw / 8;              // bytes of a block in the ring
+            // Eight elements of one scale.
+            auto widen = [&](uint32_t codes, uint32_t scale) {
+              const uint32_t z = dev::e4m3x2_to_f16x2(scale), s2 = __byte_perm(z, z, 0x1010);
+              uint32_t f[4];
+              dev::e2m1x8_to_f16x8(codes, f);
+              return make_uint4(dev::hmul2(f[0], s2), dev::hmul2(f[1], s2), dev::hmul2(f[2], s2), dev::hmul2(f[3], s2));
+            };
+            if (!is_v) {
+#pragma unroll 4
+              for (int c = ct; c < kTreeTile * CPR; c += NC) {
+                const int row = c / CPR, ch = c - row * CPR, r = row & 15;
+                const uint8_t* blk = src + (row >> 4) * kBlock;
+                put(row, ch, widen(*reinterpret_cast<const uint32_t*>(blk + r * (D / 2) + 4 * ch), blk[8 * D + r * (D / 16) + (ch >> 1)]));
+              }
+            } else {
+              // Tokens in neighbouring lanes: a group's 16 rows lie together.
+#pragma unroll 4
+              for (int c = ct; c < kTreeTile * CPR; c += NC) {
+                const int r = c & 15, rest = c >> 4, ch = rest % CPR, row = (rest / CPR) * 16 + r;
+                const uint8_t* blk = src + (row >> 4) * kBlock;
+                const int e = 8 * ch, g = e / (D / 8), swap = ((D == 128 ? g : g >> 1) & 1) << 2;
+                put(row, ch, widen(*reinterpret_cast<const uint32_t*>(blk + g * D + ((r >> 1) ^ swap) * (D / 8) + (r & 1) * (D / 16) + (e % (D / 8)) / 2),
+                                   blk[8 * D + 16 * (ch >> 1) + r]));
+              }
+            }
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            dev::mbar_arrive(op_full0 + 8 * slot);
+            dev::mbar_arrive(empty0 + 8 * raw);
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (*(volatile int*)dead) {
+    // Given up: copies and products may be in flight.  They need far less than this to end.
+    const uint64_t start = dev::global_timer_ns();
+    while (dev::global_timer_ns() - start < 20000000ull) {}
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+// ------------------------------------------------------------------ combination
+
+// 32 query rows (lanes) by 16 columns of one item that several CTAs share: the warps take its records in turn, then
+// add up.  Bound by the latency of the records' loads from L2: four independent 16-byte loads of each record.
+constexpr int kCombineThreads = 256, kCombineCols = 16;
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads) fd_tree_combine_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int NW = kCombineThreads / 32, NC = D / kCombineCols;
+  __shared__ float sm_m[NW][32], sm_l[NW][32];
+  __shared__ float4 sm_o[NW][kCombineCols / 4][32];
+  dev::pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = p.split[blockIdx.y];
+  const int rb = blockIdx.x / NC, col = (blockIdx.x - rb * NC) * kCombineCols;
+  // The item that CTA `cta` goes on with; CTA cta - 1 began it.
+  const int u = tree_run_begin(p, cta);
+  int b = 0, hi = p.B;
+  while (hi - b > 1) {
+    const int mid = (b + hi) >> 1;
+    if (p.unit_base[mid] <= u) b = mid; else hi = mid;
+  }
+  const int n = p.cu_q[b + 1] - p.cu_q[b], all = n * p.G, groups = tree_groups(all);
+  const int per = tree_tiles(p.len[b]) + kTreeItemUnits, item = (u - p.unit_base[b]) / per;
+  const int end = p.unit_base[b] + (item + 1) * per;
+  const int kvh = item / groups, r0 = (item - kvh * groups) * kTreeRows, rows = min(all - r0, kTreeRows);
+  const int gr = rb * 32 + lane;
+  if (rb * 32 >= rows) return;
+  int records = 1;
+  while (cta + records - 1 < p.ctas && tree_run_begin(p, cta + records - 1) < end) ++records;
+  dev::pdl_wait();
+  const int64_t size = tree_record_floats(D, p.rec_rows);
+  auto record = [&](int i) { return p.part + (int64_t)(2 * (cta - 1 + i) + (i == 0)) * size; };
+  float m = -INFINITY, l = 0.f;
+  for (int i = warp; i < records; i += NW) m = fmaxf(m, __ldcg(record(i) + gr));
+  float4 acc[kCombineCols / 4];
+#pragma unroll
+  for (int k = 0; k < kCombineCols / 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = warp; i < records; i += NW) {
+    const float* rec = record(i);
+    const float mi = __ldcg(rec + gr), li = __ldcg(rec + p.rec_rows + gr);
+    const float c = mi == -INFINITY ? 0.f : dev::ex2(mi - m);
+    l = fmaf(c, li, l);
+#pragma unroll
+    for (int k = 0; k < kCombineCols / 4; ++k) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + 2 * p.rec_rows) + (int64_t)(col / 4 + k) * p.rec_rows + gr);
+      acc[k].x = fmaf(c, x.x, acc[k].x);
+      acc[k].y = fmaf(c, x.y, acc[k].y);
+      acc[k].z = fmaf(c, x.z, acc[k].z);
+      acc[k].w = fmaf(c, x.w, acc[k].w);
+    }
+  }
+  sm_m[warp][lane] = m;
+  sm_l[warp][lane] = l;
+#pragma unroll
+  for (int k = 0; k < kCombineCols / 4; ++k) sm_o[warp][k][lane] = acc[k];
+  __syncthreads();
+  if (warp >= kCombineCols / 4 || gr >= rows) return;
+  float M = -INFINITY, Lsum = 0.f;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) M = fmaxf(M, sm_m[i][lane]);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    const float c = sm_m[i][lane] == -INFINITY ? 0.f : dev::ex2(sm_m[i][lane] - M);
+    const float4 x = sm_o[i][warp][lane];
+    Lsum = fmaf(c, sm_l[i][lane], Lsum);
+    a.x = fmaf(c, x.x, a.x);
+    a.y = fmaf(c, x.y, a.y);
+    a.z = fmaf(c, x.z, a.z);
+    a.w = fmaf(c, x.w, a.w);
+  }
+  const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
+  const int R = r0 + gr, t = R / p.G;
+  const int64_t out_row = (int64_t)(p.cu_q[b] + t) * p.Hq + kvh * p.G + (R - t * p.G);
+  *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + out_row * D + col + 4 * warp) =
+      make_uint2(dev::pack2<T>(a.x * inv, a.y * inv), dev::pack2<T>(a.z * inv, a.w * inv));
+  if (warp == 0 && col == 0 && p.lse != nullptr)
+    p.lse[out_row] = Lsum > 0.f ? fmaf(M, dev::kLn2, logf(Lsum)) : Lsum == 0.f ? -INFINITY : Lsum;
+}
+
+// ------------------------------------------------------------------ launch
+
+template <typename T, int D, int KV>
+cudaError_t launch(const TreeParams& p, int splits, cudaStream_t stream) {
+  const void* fn = reinterpret_cast<const void*>(&fd_tree_kernel<T, D, KV>);
+  int dev_id = 0;
+  cudaError_t err = cudaGetDevice(&dev_id);
+  if (err != cudaSuccess) return err;
+  static uint64_t done_mask = 0;  // devices whose shared-memory limit is set for this kernel
+  const uint64_t bit = 1ull << (dev_id & 63);
+  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
+    err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmemBytes);
+    if (err != cudaSuccess) return err;
+    __atomic_fetch_or(&done_mask, bit, __ATOMIC_RELEASE);
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(threads(KV));
+  cfg.dynamicSmemBytes = kTreeSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* args[] = {const_cast<TreeParams*>(&p)};
+  err = cudaLaunchKernelExC(&cfg, fn, args);
+  if (err != cudaSuccess || splits == 0) return err;
+  cfg.gridDim = dim3(p.rec_rows / 32 * (D / kCombineCols), splits);
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&fd_tree_combine_kernel<T, D>), args);
+}
+
+}  // namespace tree
+}  // namespace fd
