@@ -30,8 +30,8 @@ FD_HD constexpr int tree_raw_slots(int kv, int d, int q_tiles) {
              ? 12
              : (kTreeSmemTiles - (q_tiles + tree_slots(kv, d, q_tiles)) * tree_operand_bytes(d)) / tree_raw_bytes(kv, d);
 }
-// After the tiles: barriers, flags, the query rows' scales.
-constexpr int kTreeMetaBytes = 2048;
+// After the tiles: barriers, flags, the query rows' scales, sums that the softmax groups exchange.
+constexpr int kTreeMetaBytes = 3072;
 constexpr int kTreeSmemBytes = kTreeSmemTiles + kTreeMetaBytes;
 
 // Floats of a CTA's partial record of `rows` query rows: m, l, then O as [d / 4][rows][4].

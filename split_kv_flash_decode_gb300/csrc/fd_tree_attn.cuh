@@ -13,8 +13,8 @@
 // several CTAs share leaves fp32 records (m, l, O), which a second launch combines: no CTA waits for
 // another.  (The records of an item that one CTA had alone are never written.)
 //
-// Warps: 0-3 and 4-7 softmax, 8 issues the products, 9 the TMA loads, and over 8- and 4-bit caches 10 on widen
-// the stored rows to fp16 in the layout that the products read.
+// Warps: 0-3 and 4-7 softmax, 8 issues the products, 9 the TMA loads, 10 and 11 bring the next item's queries in, and
+// over 8- and 4-bit caches 12 on widen the stored rows to fp16 in the layout that the products read.
 #pragma once
 
 #include "fd_kernel.cuh"
@@ -23,10 +23,28 @@
 namespace fd {
 namespace tree {
 
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvertWarp = 10;
-FD_HD constexpr int convert_warps(int kv) { return kv == kKv16 ? 0 : 4; }
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kQueryWarp = 10, kQueryWarps = 2, kConvertWarp = 12;
+FD_HD constexpr int convert_warps(int kv) { return kv == kKv16 ? 0 : 8; }
 FD_HD constexpr int threads(int kv) { return 32 * (kConvertWarp + convert_warps(kv)); }
-// Tensor memory: S (and P in its place) of the two groups, then their O.
+// Registers per thread: at launch (what the compiler takes for that many threads), then softmax, warps 8-11, and
+// converters.  A softmax thread holds a row's 128 scores.
+FD_HD constexpr int launch_regs(int kv) { return kv == kKv16 ? 168 : 96; }
+FD_HD constexpr int softmax_regs(int kv) { return kv == kKv16 ? 200 : 168; }
+FD_HD constexpr int other_regs(int kv) { return kv == kKv16 ? 104 : 56; }
+constexpr int kConvertRegs = 40;
+FD_HD constexpr bool regs_fit(int kv) {
+  return 256 * softmax_regs(kv) + 128 * other_regs(kv) + 32 * convert_warps(kv) * kConvertRegs <= threads(kv) * launch_regs(kv);
+}
+static_assert(regs_fit(kKv16) && regs_fit(kKvE4m3) && regs_fit(kKvE2m1), "setmaxnreg would wait forever");
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Tensor memory, all of it (so that its addresses begin at 0): S (and P in its place) of the two groups, then their O.
 constexpr uint32_t kTmemAll = 512, kTmemS = 128, kTmemO = 256;
 constexpr int kMaxOperandSlots = 4;  // of 8- and 4-bit caches
 
@@ -72,14 +90,22 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
 // ------------------------------------------------------------------ the work of a CTA
 
 // Tiles [tile0, tile0 + nt) of an item.
 struct Portion {
-  int b, kvh, r0, rows, n, L, tile0, nt, slot;
+  int b, kvh, r0, L, tile0, nt;
+  int16_t rows, n, row_tile;  // row_tile: rows of a row tile
   bool two;    // two row tiles; else one, and the groups take alternate tiles of tokens
   bool whole;  // all tiles of the item
-  int row_tile;  // rows of a row tile
+  bool slot;   // the CTA's record: 0 of the item it goes on with, 1 of the item it leaves unfinished
   __device__ __forceinline__ int jobs() const { return two ? 2 * nt : nt; }
   __device__ __forceinline__ int tile_of(int job) const { return two ? job >> 1 : job; }
   // Places of a tile's K and V among the portion's 2 nt loads: in the order in which the products want them.
@@ -95,6 +121,7 @@ struct Portion {
 // The portions of a run of units, in order; the same in every warp.
 struct Cursor {
   int u, u1, b;
+  Cursor() = default;
   __device__ __forceinline__ Cursor(const TreeParams& p, int cta) {
     u = tree_run_begin(p, cta);
     u1 = tree_run_begin(p, cta + 1);
@@ -126,7 +153,7 @@ struct Cursor {
       o.tile0 = lo;
       o.nt = hi - lo;
       o.whole = lo == 0 && hi == tiles;
-      o.slot = lo > 0 ? 0 : 1;
+      o.slot = lo == 0;
       return true;
     }
     return false;
@@ -164,7 +191,7 @@ struct Waiter {
     if (dev::mbar_try_wait(bar, parity)) return;
     slow(bar, parity);
   }
-  __device__ __noinline__ void slow(uint32_t bar, uint32_t parity) const {
+  __device__ __forceinline__ void slow(uint32_t bar, uint32_t parity) const {
     const uint64_t start = dev::global_timer_ns();
     while (!*dead) {
 #pragma unroll 1
@@ -192,18 +219,21 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
   const int q_tiles = p.q_tiles, nslot = tree_slots(KV, D, q_tiles), nraw = tree_raw_slots(KV, D, q_tiles);
   uint8_t* slots = smem + q_tiles * kOperand;
   uint8_t* raws = slots + nslot * kOperand;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTreeSmemTiles);
+  uint8_t* meta = smem + kTreeSmemTiles;
   // The loads' ring (16 bits: the operand slots themselves), then the operand slots of other caches.
-  const uint32_t full0 = dev::smem_addr(bars), empty0 = full0 + 8 * kTreeMaxSlots;
+  const uint32_t full0 = dev::smem_addr(meta), empty0 = full0 + 8 * kTreeMaxSlots;
   const uint32_t wide0 = empty0 + 8 * kTreeMaxSlots;
   const uint32_t op_full0 = KV == kKv16 ? full0 : wide0;
   const uint32_t op_empty0 = KV == kKv16 ? empty0 : wide0 + 8 * kMaxOperandSlots;
   const uint32_t s_full0 = wide0 + 16 * kMaxOperandSlots, p_ready0 = s_full0 + 16, o_full0 = p_ready0 + 16,
-                 q_ready = o_full0 + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kTreeSmemTiles + 400);
-  int* dead = reinterpret_cast<int*>(smem + kTreeSmemTiles + 404);
-  float* q_scale = reinterpret_cast<float*>(smem + kTreeSmemTiles + 512);  // [kTreeRows]
-  static_assert(8 * (2 * kTreeMaxSlots + 2 * kMaxOperandSlots + 7) <= 400, "barriers");
+                 q_full0 = o_full0 + 16, q_empty = q_full0 + 16;
+  constexpr int kBars = 8 * (2 * kTreeMaxSlots + 2 * kMaxOperandSlots + 9);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + kBars);
+  int* dead = reinterpret_cast<int*>(meta + kBars + 4);
+  Portion* said = reinterpret_cast<Portion*>(meta + kBars + 8);  // [3]: portion k is in place k % 3; nt = 0: the end
+  int8_t* q_exp = reinterpret_cast<int8_t*>(said + 3);           // [2][kTreeRows]: the power of two taken out of a query row
+  float* ml = reinterpret_cast<float*>(meta + kTreeMetaBytes - 2048);  // [2][128][2]: the groups' m and l at an item's end
+  static_assert(kBars + 8 + 3 * sizeof(Portion) + 2 * kTreeRows + 2048 <= kTreeMetaBytes, "meta");
   const int nload = KV == kKv16 ? nslot : nraw;  // slots of the loads' ring
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,7 +253,9 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       dev::mbar_init(p_ready0 + 8 * w, 4);
       dev::mbar_init(o_full0 + 8 * w, 1);
     }
-    dev::mbar_init(q_ready, 8);
+    dev::mbar_init(q_full0, kQueryWarps);
+    dev::mbar_init(q_full0 + 8, kQueryWarps);
+    dev::mbar_init(q_empty, 1);
     dev::fence_mbar_init();
     *dead = 0;
   }
@@ -235,140 +267,86 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     dev::prefetch_tensormap(&p.tm_k);
     dev::prefetch_tensormap(&p.tm_v);
   }
-  dev::pdl_wait();
+  // What the parameters alone say is worked out ahead of the wait for the kernels before.
+  Cursor cur;
+  Portion o = {};
+  bool more = false;
+  if (warp >= kLoadWarp) {
+    cur = Cursor(p, blockIdx.x);
+    more = cur.next(p, o);
+    if (!more) o = Portion{};  // a run may lie within what an item costs beyond its tiles
+    if (warp == kQueryWarp && lane == 0) said[0] = o;
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  dev::pdl_wait();
   const Waiter wait{dead, p.status};
-  Cursor cur(p, blockIdx.x);
-  Portion o;
 
-  if (warp == kLoadWarp) {
-    // ---------------- loads: a lane issues a box (a page's rows, or half the columns)
-    const uint64_t policy = dev::l2_evict_first_policy();
-    constexpr int NBOX = KV == kKv16 ? D / 64 : 1;
-    constexpr int kUnit = KV == kKvE2m1 ? kBlockTokens : 1;
-    constexpr int kLoadBytes = KV == kKv16 ? kOperand : kRaw;
-    constexpr int kBoxRow = KV == kKv16 ? 128 : kRaw / kTreeTile;  // bytes of a token's row in a box
-    const int pieces = kTreeTile / p.box_rows, boxes = pieces * NBOX;
-    int i = 0;
-    while (cur.next(p, o)) {
-      for (int s = 0; s < 2 * o.nt; ++s, ++i) {
-        const int slot = i % nload;
-        const int t0 = (o.tile0 + o.load_tile(s)) * kTreeTile;
-        int row = 0;
-        const int piece = lane / NBOX, bx = lane - piece * NBOX, r = piece * p.box_rows;
-        if (lane < boxes) {
-          if (p.block_table == nullptr) {
-            row = p.base[o.b] + t0;
-          } else {
-            // Boxes past the end of the sequence reload its last page; an index outside the pool reads zeros.
-            const int pg = min((t0 + r) >> p.page_shift, (o.L - 1) >> p.page_shift);
-            const uint32_t page = (uint32_t)p.block_table[(int64_t)o.b * p.bt_stride + pg];
-            row = (int)(min(page, (uint32_t)p.num_pages) << p.page_shift) + ((t0 + r) & ((1 << p.page_shift) - 1));
-            if (page >= (uint32_t)p.num_pages) row = p.num_pages << p.page_shift;
-          }
-        }
-        if (i >= nload) wait(empty0 + 8 * slot, (i / nload - 1) & 1);
-        if (*(volatile int*)dead) continue;
-        if (lane == 0) dev::mbar_arrive_expect_tx(full0 + 8 * slot, kLoadBytes);
-        __syncwarp();
-        if (lane < boxes) {
-          const uint32_t dst = dev::smem_addr(KV == kKv16 ? slots + slot * kOperand : raws + slot * kRaw);
-          dev::tma_load_3d(dst + bx * kHalf + r * kBoxRow, o.is_v(s) ? &p.tm_v : &p.tm_k, bx * 64, o.kvh, row / kUnit,
-                           full0 + 8 * slot, policy);
+  // Writes query rows of portion q: chunks of 16 bytes, `step` threads, the first of them `from`.
+  auto put_queries = [&](const Portion& q, int from, int step, int parity) {
+    constexpr int kBatch = KV == kKv16 ? 4 : 2;
+    const int total = q.rows * CPR, G = p.G;
+    const T* src = reinterpret_cast<const T*>(p.q) + ((int64_t)p.cu_q[q.b] * p.Hq + q.kvh * G) * D;
+    for (int c0 = from;; c0 += kBatch * step) {
+      uint4 x[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int c = c0 + k * step;
+        if (c < total) {
+          const int gr = c / CPR, R = q.r0 + gr, t = R / G;
+          x[k] = *reinterpret_cast<const uint4*>(src + ((int64_t)t * p.Hq + (R - t * G)) * D + (c - gr * CPR) * 8);
         }
       }
-    }
-  } else if (warp == kMmaWarp) {
-    // ---------------- products, issued by one lane
-    if (lane == 0) {
-      constexpr uint32_t kIdS = tc::idesc_f16(kBf16, false, false, kTreeTile, kTreeTile);
-      constexpr uint32_t kIdO = tc::idesc_f16(kBf16, false, true, kTreeTile, D);
-      const uint32_t q0 = dev::smem_addr(smem), slot0 = dev::smem_addr(slots);
-      uint32_t base = 0, q_phase = 0, p_phase[2] = {0, 0};
-      while (cur.next(p, o)) {
-        const int jobs = o.jobs();
-        wait(q_ready, q_phase & 1);
-        ++q_phase;
-        tc::fence_after_sync();
-        auto scores = [&](int j) {
-          const int w = j & 1, t = o.tile_of(j);
-          const uint32_t i = base + o.seq_k(t), slot = i % nslot;
-          wait(op_full0 + 8 * slot, (i / nslot) & 1);
-          tc::fence_after_sync();
-          const uint32_t qa = q0 + (o.two ? w * kOperand : 0), ka = slot0 + slot * kOperand;
+      // Portions but the first: the last products with Q's old rows are done.  (Threads without a chunk wait too.)
+      if (c0 == from && parity >= 0) wait(q_empty, parity & 1);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_f16_ss(tmem + w * kTmemS, tc::smem_desc(qa + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024, tc::kSwizzle128B),
-                           tc::smem_desc(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024, tc::kSwizzle128B), kIdS, kk > 0);
-          tc::commit(s_full0 + 8 * w);
-          if (!o.two || w == 1) tc::commit(op_empty0 + 8 * slot);
-        };
-        scores(0);
-        if (jobs > 1) scores(1);
-        for (int j = 0; j < jobs; ++j) {
-          const int w = j & 1, t = o.tile_of(j);
-          const uint32_t i = base + o.seq_v(t), slot = i % nslot;
-          wait(p_ready0 + 8 * w, p_phase[w] & 1);
-          ++p_phase[w];
-          wait(op_full0 + 8 * slot, (i / nslot) & 1);
-          tc::fence_after_sync();
-          const uint32_t va = slot0 + slot * kOperand, ps = tmem + w * kTmemS, od = tmem + kTmemO + w * kTmemS;
+      for (int k = 0; k < kBatch; ++k) {
+        const int c = c0 + k * step;
+        if (c < total) {
+          const int gr = c / CPR, ch = c - gr * CPR;
+          if constexpr (kScaledQ) {
+            // bf16 into fp16 by a power of two for each row that brings its largest value below 2^15.
+            float f[8];
+            dev::unpack8<T>(x[k], f);
+            float m = 0.f;
 #pragma unroll
-          for (int kk = 0; kk < kTreeTile / 16; ++kk) {
-            const uint64_t vd = tc::smem_desc(va + kk * 2048, kHalf, 1024, tc::kSwizzle128B);
-            mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8, vd, kIdO, j > 1 || kk > 0);
-            if (kBf16) mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8 + 16, vd, kIdO, 1u);
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+            const uint32_t lanes_here = __activemask();       // whole rows: CPR divides every bound
+#pragma unroll
+            for (int off = 1; off < CPR; off <<= 1) m = fmaxf(m, __shfl_xor_sync(lanes_here, m, off));
+            const int e = (int)(__float_as_uint(m) >> 23);    // 2^(e - 127) <= m
+            const int up = e == 0 || e == 255 ? 0 : min(max(141 - e, -100), 100);
+            const float s = __int_as_float((127 + up) << 23);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= s;
+            x[k] = make_uint4(dev::pack2<__half>(f[0], f[1]), dev::pack2<__half>(f[2], f[3]),
+                              dev::pack2<__half>(f[4], f[5]), dev::pack2<__half>(f[6], f[7]));
+            if (ch == 0) q_exp[((parity + 1) & 1) * kTreeRows + gr] = (int8_t)-up;
           }
-          if (!o.two || w == 1) tc::commit(op_empty0 + 8 * slot);
-          if (j + 2 >= jobs) tc::commit(o_full0 + 8 * w);
-          else scores(j + 2);
+          const int tile = q.two && gr >= q.row_tile ? 1 : 0, r = gr - tile * q.row_tile;
+          *reinterpret_cast<uint4*>(smem + tile * kOperand + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x[k];
         }
-        base += 2 * o.nt;
       }
+      if (c0 + kBatch * step >= total) break;
     }
-    __syncwarp();
-  } else if (warp < kMmaWarp) {
+    tc::fence_proxy_async_smem();
+  };
+
+  if (warp < kMmaWarp) {
+    regs_inc<softmax_regs(KV)>();
     // ---------------- softmax
     const int w = warp >> 2, wl = tid & 127;             // group, and thread in it: the row in its tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + w * kTmemS, to = tmem + lanes + kTmemO + w * kTmemS;
+    const uint32_t ts = lanes + w * kTmemS, to = lanes + kTmemO + w * kTmemS;
     uint32_t base = 0, s_phase = 0, o_phase[2] = {0, 0};
-    while (cur.next(p, o)) {
+    // The first item's queries, for which everybody waits, are brought in by all.
+    put_queries(said[0], tid, 256 + 32 * kQueryWarps, -1);
+    tc::named_sync(2, 256 + 32 * kQueryWarps);
+    for (uint32_t nth = 0;; ++nth) {
+      const Portion o = said[nth % 3];
+      if (o.nt == 0 || *(volatile int*)dead) break;
       const int jobs = o.jobs(), G = p.G;
-      // Q: the rows of the item's tokens and heads, rows past the last one left as they are (they meet nobody).
-      for (int c = tid; c < o.rows * CPR; c += 256) {
-        const int gr = c / CPR, ch = c - gr * CPR, R = o.r0 + gr, t = R / G;
-        uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.q) +
-                      ((int64_t)(p.cu_q[o.b] + t) * p.Hq + o.kvh * G + (R - t * G)) * D + ch * 8);
-        if constexpr (kScaledQ) {
-          // bf16 into fp16 by a power of two for each row that brings its largest value below 2^15.
-          float f[8];
-          dev::unpack8<T>(x, f);
-          float m = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
-#pragma unroll
-          for (int off = 1; off < CPR; off <<= 1) m = fmaxf(m, __shfl_xor_sync(__activemask(), m, off));
-          const int e = (int)(__float_as_uint(m) >> 23);        // 2^(e - 127) <= m
-          const int up = e == 0 || e == 255 ? 0 : min(max(141 - e, -100), 100);
-          const float s = __int_as_float((127 + up) << 23);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] *= s;
-          x = make_uint4(dev::pack2<__half>(f[0], f[1]), dev::pack2<__half>(f[2], f[3]), dev::pack2<__half>(f[4], f[5]),
-                         dev::pack2<__half>(f[6], f[7]));
-          if (ch == 0) q_scale[gr] = __int_as_float((127 - up) << 23);
-        }
-        const int tile = o.two && gr >= o.row_tile ? 1 : 0, r = gr - tile * o.row_tile;
-        *reinterpret_cast<uint4*>(smem + tile * kOperand + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
-      }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(q_ready);
-      if (kScaledQ) tc::named_sync(1, 256);
-
       const int gr = (o.two ? w * o.row_tile : 0) + wl;   // row of the item
       const int rows_here = o.two ? (w ? o.rows - o.row_tile : min(o.rows, o.row_tile)) : o.rows;
       const bool mine = wl < rows_here;
@@ -379,7 +357,8 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       if (mine) mask = p.mask != nullptr ? p.mask[p.cu_q[o.b] + t] & nodes : all_nodes(t + 1);
       uint64_t any = nodes;
       if (KV == kKv16) any = seen_by_any(p, o.b, o.n);
-      const float scale = kScaledQ && mine ? p.scale_log2 * q_scale[gr] : p.scale_log2;
+      float scale = p.scale_log2;
+      if (kScaledQ && mine) scale *= __int_as_float((127 + q_exp[(nth & 1) * kTreeRows + gr]) << 23);
       float m = -INFINITY, l = 0.f;
       for (int j = w; j < jobs; j += 2) {
         const int tile = o.tile_of(j), off = o.L - o.n - (o.tile0 + tile) * kTreeTile;  // columns before the drafted rows
@@ -455,17 +434,19 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
           // V rows that no token sees (behind the sequence, of padding nodes) become 0: a weight of 0 times what they
           // hold could be NaN.
           const uint32_t i = base + o.seq_v(tile), slot = i % nslot;
-          wait(op_full0 + 8 * slot, (i / nslot) & 1);
-          uint8_t* vs = slots + slot * kOperand;
+          uint32_t gone[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t gone = ~seen(any, off, c);
-            for (; gone != 0; gone &= gone - 1) {
-              const int row = 32 * c + __ffs(gone) - 1;
-              if (wl < CPR) *reinterpret_cast<uint4*>(vs + (wl >> 3) * kHalf + row * 128 + (wl & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
+          for (int c = 0; c < 4; ++c) gone[c] = ~seen(any, off, c);
+          if (gone[0] | gone[1] | gone[2] | gone[3]) {
+            wait(op_full0 + 8 * slot, (i / nslot) & 1);
+            const int ch = wl % CPR;
+            uint8_t* vs = slots + slot * kOperand + (ch >> 3) * kHalf + (ch & 7) * 16;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              for (int row = wl / CPR; row < 32; row += 128 / CPR)
+                if (gone[c] >> row & 1) *reinterpret_cast<uint4*>(vs + (32 * c + row) * 128) = make_uint4(0u, 0u, 0u, 0u);
+            tc::fence_proxy_async_smem();
           }
-          tc::fence_proxy_async_smem();
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -473,6 +454,8 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       }
 
       // The item's end (or this CTA's share of it).
+      const bool both = !o.two && jobs > 1;
+      if (!o.two) *reinterpret_cast<float2*>(ml + 256 * w + 2 * wl) = make_float2(m, l);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (k < jobs) {
@@ -481,80 +464,188 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
         }
       tc::fence_after_sync();
       float c0 = 1.f, c1 = 0.f;
-      int col0 = 0, col1 = D;
       if (!o.two) {
         // The groups' results of alternate tiles: each takes half the columns of both.
-        float* ml = reinterpret_cast<float*>(smem);       // in Q's place: its products are done
-        ml[w * 256 + 2 * wl] = m;
-        ml[w * 256 + 2 * wl + 1] = l;
         tc::named_sync(1, 256);
-        const float m0 = ml[2 * wl], l0 = ml[2 * wl + 1], m1 = ml[256 + 2 * wl], l1 = ml[256 + 2 * wl + 1];
-        m = fmaxf(m0, m1);
-        c0 = m0 == -INFINITY ? 0.f : dev::ex2(m0 - m);
-        c1 = m1 == -INFINITY ? 0.f : dev::ex2(m1 - m);
-        l = c0 * l0 + c1 * l1;
-        col0 = w * (D / 2);
-        col1 = col0 + D / 2;
+        const float2 a = *reinterpret_cast<const float2*>(ml + 2 * wl), b = *reinterpret_cast<const float2*>(ml + 256 + 2 * wl);
+        m = fmaxf(a.x, b.x);
+        c0 = a.x == -INFINITY ? 0.f : dev::ex2(a.x - m);
+        c1 = b.x == -INFINITY ? 0.f : dev::ex2(b.x - m);
+        l = c0 * a.y + c1 * b.y;
       }
       if (busy) {
-        const uint32_t o0 = tmem + lanes + kTmemO + (o.two ? w * kTmemS : 0), o1 = tmem + lanes + kTmemO + kTmemS;
-        const bool both = !o.two && jobs > 1;
+        // All of the thread's columns at once: one row tile: D / 2 of either group's; two: all D of its own group's.
+        uint32_t y[D];
+        const uint32_t oc = lanes + kTmemO + (o.two ? w * kTmemS : w * (D / 2));
+#pragma unroll
+        for (int c = 0; c < D; c += 32) ld32(oc + (o.two ? c : c < D / 2 ? c : c - D / 2 + kTmemS), y + c);
+        tc::wait_ld();
         float* rec = p.part + (int64_t)(2 * blockIdx.x + o.slot) * tree_record_floats(D, p.rec_rows);
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const int64_t out_row = (int64_t)(p.cu_q[o.b] + t) * p.Hq + o.kvh * G + (R - t * G);
-#pragma unroll 1
-        for (int c = col0; c < col1; c += 32) {
-          uint32_t y[32];
-          float f[32];
-          ld32(o0 + c, y);
-          tc::wait_ld();
+        const int col0 = o.two ? 0 : w * (D / 2);
+        if (!o.two) {
+          // A coefficient of 0 takes no part: the group had no tile, or no token that the row sees.
 #pragma unroll
-          for (int k = 0; k < 32; ++k) f[k] = c0 != 0.f || o.two ? __uint_as_float(y[k]) * c0 : 0.f;
-          if (both) {
-            ld32(o1 + c, y);
-            tc::wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) f[k] = c1 != 0.f ? fmaf(__uint_as_float(y[k]), c1, f[k]) : f[k];
-          }
-          if (!mine) continue;
-          if (o.whole) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint4 v;
-              v.x = dev::pack2<T>(f[k] * inv, f[k + 1] * inv);
-              v.y = dev::pack2<T>(f[k + 2] * inv, f[k + 3] * inv);
-              v.z = dev::pack2<T>(f[k + 4] * inv, f[k + 5] * inv);
-              v.w = dev::pack2<T>(f[k + 6] * inv, f[k + 7] * inv);
-              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + out_row * D + c + k) = v;
-            }
-          } else {
-            // Column by column: the rows of a warp lie together.
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              __stcg(reinterpret_cast<float4*>(rec + 2 * p.rec_rows) + (int64_t)((c + k) / 4) * p.rec_rows + gr,
-                     make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]));
+          for (int k = 0; k < D / 2; ++k) {
+            float f = c0 != 0.f ? __uint_as_float(y[k]) * c0 : 0.f;
+            if (both && c1 != 0.f) f = fmaf(__uint_as_float(y[k + D / 2]), c1, f);
+            y[k] = __float_as_uint(f);
           }
         }
-        if (mine && col0 == 0) {
-          if (!o.whole) {
-            __stcg(rec + gr, m);
-            __stcg(rec + p.rec_rows + gr, l);
-          } else if (p.lse != nullptr) {
-            p.lse[out_row] = l > 0.f ? fmaf(m, dev::kLn2, logf(l)) : l == 0.f ? -INFINITY : l;
+        if (mine) {
+#pragma unroll
+          for (int k = 0; k < D; k += 8) {
+            if (k >= D / 2 && !o.two) break;
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(y[k + i]);
+            if (o.whole) {
+              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + out_row * D + col0 + k) =
+                  make_uint4(dev::pack2<T>(f[0] * inv, f[1] * inv), dev::pack2<T>(f[2] * inv, f[3] * inv),
+                             dev::pack2<T>(f[4] * inv, f[5] * inv), dev::pack2<T>(f[6] * inv, f[7] * inv));
+            } else {
+              // Column by column: the rows of a warp lie together.
+              float4* at = reinterpret_cast<float4*>(rec + 2 * p.rec_rows) + (int64_t)((col0 + k) / 4) * p.rec_rows + gr;
+              __stcg(at, make_float4(f[0], f[1], f[2], f[3]));
+              __stcg(at + p.rec_rows, make_float4(f[4], f[5], f[6], f[7]));
+            }
+          }
+          if (col0 == 0) {
+            if (!o.whole) {
+              __stcg(rec + gr, m);
+              __stcg(rec + p.rec_rows + gr, l);
+            } else if (p.lse != nullptr) {
+              p.lse[out_row] = l > 0.f ? fmaf(m, dev::kLn2, logf(l)) : l == 0.f ? -INFINITY : l;
+            }
           }
         }
       }
       tc::fence_before_sync();
-      tc::named_sync(1, 256);  // O and the exchanged sums are read; Q may be written
+      wait(q_full0 + 8 * ((nth + 1) & 1), ((nth + 1) >> 1) & 1);  // the next portion is said, its queries are there
+      tc::named_sync(1, 256);                                 // O and the exchanged sums are read
       base += 2 * o.nt;
     }
+  } else if (warp < kConvertWarp) {
+    regs_dec<other_regs(KV)>();
+    if (warp == kLoadWarp) {
+    // ---------------- loads: a lane issues a box (a page's rows, or half the columns)
+    const uint64_t policy = dev::l2_evict_first_policy();
+    constexpr int NBOX = KV == kKv16 ? D / 64 : 1;
+    constexpr int kUnit = KV == kKvE2m1 ? kBlockTokens : 1;
+    constexpr int kLoadBytes = KV == kKv16 ? kOperand : kRaw;
+    constexpr int kBoxRow = KV == kKv16 ? 128 : kRaw / kTreeTile;  // bytes of a token's row in a box
+    const int pieces = kTreeTile / p.box_rows, boxes = pieces * NBOX;
+    const int piece = lane / NBOX, bx = lane - piece * NBOX, r = piece * p.box_rows;
+    int i = 0;
+    for (; more; more = cur.next(p, o)) {
+      for (int s = 0; s < 2 * o.nt; ++s, ++i) {
+        const int slot = i % nload;
+        const int t0 = (o.tile0 + o.load_tile(s)) * kTreeTile;
+        int row = 0;
+        if (lane < boxes) {
+          if (p.block_table == nullptr) {
+            row = p.base[o.b] + t0;
+          } else {
+            // Boxes past the end of the sequence reload its last page; an index outside the pool reads zeros.
+            const int pg = min((t0 + r) >> p.page_shift, (o.L - 1) >> p.page_shift);
+            const uint32_t page = (uint32_t)p.block_table[(int64_t)o.b * p.bt_stride + pg];
+            row = page < (uint32_t)p.num_pages ? (int)(page << p.page_shift) + ((t0 + r) & ((1 << p.page_shift) - 1))
+                                               : p.num_pages << p.page_shift;
+          }
+        }
+        if (i >= nload) wait(empty0 + 8 * slot, (i / nload - 1) & 1);
+        if (*(volatile int*)dead) continue;
+        if (lane == 0) dev::mbar_arrive_expect_tx(full0 + 8 * slot, kLoadBytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const uint32_t dst = dev::smem_addr(KV == kKv16 ? slots + slot * kOperand : raws + slot * kRaw);
+          dev::tma_load_3d(dst + bx * kHalf + r * kBoxRow, o.is_v(s) ? &p.tm_v : &p.tm_k, bx * 64, o.kvh, row / kUnit,
+                           full0 + 8 * slot, policy);
+        }
+      }
+    }
+    } else if (warp == kMmaWarp) {
+    // ---------------- products: the whole warp keeps track, so that addresses are uniform; one lane issues
+    constexpr uint32_t kIdS = tc::idesc_f16(kBf16, false, false, kTreeTile, kTreeTile);
+    constexpr uint32_t kIdO = tc::idesc_f16(kBf16, false, true, kTreeTile, D);
+    const uint32_t q0 = dev::smem_addr(smem), slot0 = dev::smem_addr(slots);
+    const bool leader = elect_one();
+    uint32_t base = 0, p_phase[2] = {0, 0};
+    for (uint32_t k = 0;; ++k) {
+      wait(q_full0 + 8 * (k & 1), (k >> 1) & 1);
+      const Portion o = said[k % 3];
+      if (o.nt == 0 || *(volatile int*)dead) break;
+      const int jobs = o.jobs();
+      tc::fence_after_sync();
+      auto scores = [&](int j) {
+        const int w = j & 1, t = o.tile_of(j);
+        const uint32_t i = base + o.seq_k(t), slot = i % nslot;
+        wait(op_full0 + 8 * slot, (i / nslot) & 1);
+        tc::fence_after_sync();
+        const uint32_t qa = q0 + (o.two ? w * kOperand : 0), ka = slot0 + slot * kOperand;
+        const uint64_t qd = tc::smem_desc(qa, 16, 1024, tc::kSwizzle128B), kd = tc::smem_desc(ka, 16, 1024, tc::kSwizzle128B);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_f16_ss(w * kTmemS, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                           kIdS, kk > 0);
+          tc::commit(s_full0 + 8 * w);
+          if (!o.two || w == 1) tc::commit(op_empty0 + 8 * slot);
+          if (j == jobs - 1) tc::commit(q_empty);
+        }
+        __syncwarp();
+      };
+      scores(0);
+      if (jobs > 1) scores(1);
+      for (int j = 0; j < jobs; ++j) {
+        const int w = j & 1, t = o.tile_of(j);
+        const uint32_t i = base + o.seq_v(t), slot = i % nslot;
+        wait(op_full0 + 8 * slot, (i / nslot) & 1);
+        wait(p_ready0 + 8 * w, p_phase[w] & 1);
+        ++p_phase[w];
+        tc::fence_after_sync();
+        const uint32_t va = slot0 + slot * kOperand, ps = w * kTmemS, od = kTmemO + w * kTmemS;
+        const uint64_t vd = tc::smem_desc(va, kHalf, 1024, tc::kSwizzle128B);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kTreeTile / 16; ++kk) {
+            mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8, vd + (kk * 2048 >> 4), kIdO, j > 1 || kk > 0);
+            if (kBf16) mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8 + 16, vd + (kk * 2048 >> 4), kIdO, 1u);
+          }
+          if (!o.two || w == 1) tc::commit(op_empty0 + 8 * slot);
+          if (j + 2 >= jobs) tc::commit(o_full0 + 8 * w);
+        }
+        __syncwarp();
+        if (j + 2 < jobs) scores(j + 2);
+      }
+      base += 2 * o.nt;
+    }
+    } else {
+    // ---------------- queries of the items behind the first
+    // Portion k is said and its queries are written once portion k - 1's products with Q are done; the softmax groups
+    // wait for that at the end of k - 1, so neither of the two barriers nor the three places are ever overrun.
+    put_queries(o, tid - 64, 256 + 32 * kQueryWarps, -1);
+    tc::named_sync(2, 256 + 32 * kQueryWarps);
+    if (lane == 0) dev::mbar_arrive(q_full0);
+    for (uint32_t k = 1; more; ++k) {
+      more = cur.next(p, o);
+      if (more) put_queries(o, tid - 32 * kQueryWarp, 32 * kQueryWarps, (int)k - 1);
+      else wait(q_empty, (k - 1) & 1);
+      if (!more) o.nt = 0;
+      if (warp == kQueryWarp && lane == 0) said[k % 3] = o;
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(q_full0 + 8 * (k & 1));
+    }
+    }
   } else {
+    if constexpr (KV != kKv16) regs_dec<kConvertRegs>();
     // ---------------- widening of 8- and 4-bit rows
     if constexpr (KV != kKv16) {
       constexpr int NC = 32 * convert_warps(KV);
       const int ct = tid - 32 * kConvertWarp;
       uint32_t i = 0;
-      while (cur.next(p, o)) {
+      for (; more; more = cur.next(p, o)) {
         const uint64_t any = seen_by_any(p, o.b, o.n);
         for (int s = 0; s < 2 * o.nt; ++s, ++i) {
           const uint32_t raw = i % nraw, slot = i % nslot;
@@ -631,7 +722,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
   }
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, kTmemAll);
+    tc::tmem_dealloc(0, kTmemAll);
   }
 }
 

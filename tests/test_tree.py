@@ -185,6 +185,15 @@ def test_work_cut_anywhere(fd, dtype, num_sms):
     c.check(*c.run(c.tree(num_sms=num_sms)))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16_e2m1kv"])
+def test_many_small_sequences(fd, dtype):
+    """CTAs that go through many sequences of one tile and one query row."""
+    for n in (1, 3):
+        c = Case(fd, dtype, 64, 1, 40, [3 + 7 * b for b in range(18)], [n] * 18, seed=n)
+        c.check(*c.run())
+        c.check(*c.run(c.tree(num_sms=3)))
+
+
 @pytest.mark.parametrize("dtype", ALL)
 def test_chains_and_many_heads(fd, dtype):
     c = Case(fd, dtype, 128, 16, 3, [700, 64, 2000], [64, 64, 31], trees="chain", seed=3)
