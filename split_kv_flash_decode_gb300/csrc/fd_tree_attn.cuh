@@ -29,8 +29,8 @@ FD_HD constexpr int threads(int kv) { return 32 * (kConvertWarp + convert_warps(
 // Registers per thread: at launch (what the compiler takes for that many threads), then softmax, warps 8-11, and
 // converters.  A softmax thread holds a row's 128 scores.
 FD_HD constexpr int launch_regs(int kv) { return kv == kKv16 ? 168 : 96; }
-FD_HD constexpr int softmax_regs(int kv) { return kv == kKv16 ? 200 : 168; }
-FD_HD constexpr int other_regs(int kv) { return kv == kKv16 ? 104 : 56; }
+FD_HD constexpr int softmax_regs(int kv) { return kv == kKv16 ? 208 : 168; }
+FD_HD constexpr int other_regs(int kv) { return kv == kKv16 ? 88 : 56; }
 constexpr int kConvertRegs = 40;
 FD_HD constexpr bool regs_fit(int kv) {
   return 256 * softmax_regs(kv) + 128 * other_regs(kv) + 32 * convert_warps(kv) * kConvertRegs <= threads(kv) * launch_regs(kv);
@@ -90,6 +90,43 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// Two fp32 values in one register pair.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// A place in a ring of slots, and the parity of its barriers' phase.
+struct Place {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void advance(uint32_t by, uint32_t slots) {
+    slot += by;
+    if (slot >= slots) {
+      slot -= slots;
+      parity ^= 1;
+    }
+  }
+};
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t yes;
@@ -241,11 +278,11 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
   if (tid == 0) {
     for (int s = 0; s < nload; ++s) {
       dev::mbar_init(full0 + 8 * s, 1);
-      dev::mbar_init(empty0 + 8 * s, KV == kKv16 ? 1 : convert_warps(KV));
+      dev::mbar_init(empty0 + 8 * s, KV == kKv16 ? 1 : convert_warps(KV) / 2);
     }
     if (KV != kKv16)
       for (int s = 0; s < nslot; ++s) {
-        dev::mbar_init(op_full0 + 8 * s, convert_warps(KV));
+        dev::mbar_init(op_full0 + 8 * s, convert_warps(KV) / 2);
         dev::mbar_init(op_empty0 + 8 * s, 1);
       }
     for (int w = 0; w < 2; ++w) {
@@ -384,9 +421,8 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
 #pragma unroll
           for (int k = 0; k < 128; k += 8)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(x[k + 2 * c]), __uint_as_float(x[k + 2 * c + 1])));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+            for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(x[k + 2 * c]), __uint_as_float(x[k + 2 * c + 1]));
+          const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale;
           // A row's maximum in use moves only when it grew by more than 2^8, which is rare.
           const bool grew = mine && top > m + dev::kRescaleThreshold;
           if (__any_sync(0xffffffffu, grew)) {
@@ -406,28 +442,32 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
             }
           }
           const float mm = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t scale2 = pair(scale, scale), minus2 = pair(-mm, -mm);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t y[32];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               // Product, then difference: the largest score minus the maximum in use is then exact.
-              const float a = dev::ex2(__fmul_rn(__uint_as_float(x[32 * c + 2 * k]), scale) - mm);
-              const float b = dev::ex2(__fmul_rn(__uint_as_float(x[32 * c + 2 * k + 1]), scale) - mm);
-              sum[(2 * k) & 3] += a;
-              sum[(2 * k + 1) & 3] += b;
-              y[k] = dev::pack2<Op>(a, b);
+              const float2 e = unpair(add_pair(
+                  mul_pair(pair(__uint_as_float(x[32 * c + 2 * k]), __uint_as_float(x[32 * c + 2 * k + 1])), scale2), minus2));
+              const float f = dev::ex2(e.x), g = dev::ex2(e.y);
+              const uint64_t fg = pair(f, g);
+              sum[k & 1] = add_pair(sum[k & 1], fg);
+              y[k] = dev::pack2<Op>(f, g);
               if constexpr (kBf16) {
                 const float2 h = dev::Elem<Op>::to_f2(y[k]);
-                y[16 + k] = dev::pack2<Op>(a - h.x, b - h.y);
+                const float2 rest = unpair(add_pair(fg, pair(-h.x, -h.y)));
+                y[16 + k] = dev::pack2<Op>(rest.x, rest.y);
               }
             }
             // The weights lie where their scores lay: the scores are all read.
             if constexpr (kBf16) st32(ts + 32 * c, y);
             else st16(ts + 32 * c, y);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float2 s2 = unpair(add_pair(sum[0], sum[1]));
+          l += s2.x + s2.y;
           tc::wait_st();
         }
         if (KV == kKv16 && edge) {
@@ -474,43 +514,48 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
         l = c0 * a.y + c1 * b.y;
       }
       if (busy) {
-        // All of the thread's columns at once: one row tile: D / 2 of either group's; two: all D of its own group's.
-        uint32_t y[D];
-        const uint32_t oc = lanes + kTmemO + (o.two ? w * kTmemS : w * (D / 2));
-#pragma unroll
-        for (int c = 0; c < D; c += 32) ld32(oc + (o.two ? c : c < D / 2 ? c : c - D / 2 + kTmemS), y + c);
-        tc::wait_ld();
+        // 64 values at a time: one row tile: 32 columns of both groups; two: 64 of the group's own.
         float* rec = p.part + (int64_t)(2 * blockIdx.x + o.slot) * tree_record_floats(D, p.rec_rows);
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const int64_t out_row = (int64_t)(p.cu_q[o.b] + t) * p.Hq + o.kvh * G + (R - t * G);
         const int col0 = o.two ? 0 : w * (D / 2);
-        if (!o.two) {
-          // A coefficient of 0 takes no part: the group had no tile, or no token that the row sees.
+        const uint32_t oc = lanes + kTmemO + (o.two ? w * kTmemS : col0);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          uint32_t y[64];
+          const int col = col0 + (o.two ? c : c / 2);
+          ld32(oc + (o.two ? c : c / 2), y);
+          ld32(oc + (o.two ? c + 32 : c / 2 + kTmemS), y + 32);
+          tc::wait_ld();
+          if (!o.two) {
+            // A coefficient of 0 takes no part: the group had no tile, or no token that the row sees.
 #pragma unroll
-          for (int k = 0; k < D / 2; ++k) {
-            float f = c0 != 0.f ? __uint_as_float(y[k]) * c0 : 0.f;
-            if (both && c1 != 0.f) f = fmaf(__uint_as_float(y[k + D / 2]), c1, f);
-            y[k] = __float_as_uint(f);
+            for (int k = 0; k < 32; ++k) {
+              float f = c0 != 0.f ? __uint_as_float(y[k]) * c0 : 0.f;
+              if (both && c1 != 0.f) f = fmaf(__uint_as_float(y[k + 32]), c1, f);
+              y[k] = __float_as_uint(f);
+            }
           }
-        }
-        if (mine) {
+          if (!mine) continue;
 #pragma unroll
-          for (int k = 0; k < D; k += 8) {
-            if (k >= D / 2 && !o.two) break;
+          for (int k = 0; k < 64; k += 8) {
+            if (k >= 32 && !o.two) break;
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(y[k + i]);
             if (o.whole) {
-              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + out_row * D + col0 + k) =
+              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + out_row * D + col + k) =
                   make_uint4(dev::pack2<T>(f[0] * inv, f[1] * inv), dev::pack2<T>(f[2] * inv, f[3] * inv),
                              dev::pack2<T>(f[4] * inv, f[5] * inv), dev::pack2<T>(f[6] * inv, f[7] * inv));
             } else {
               // Column by column: the rows of a warp lie together.
-              float4* at = reinterpret_cast<float4*>(rec + 2 * p.rec_rows) + (int64_t)((col0 + k) / 4) * p.rec_rows + gr;
+              float4* at = reinterpret_cast<float4*>(rec + 2 * p.rec_rows) + (int64_t)((col + k) / 4) * p.rec_rows + gr;
               __stcg(at, make_float4(f[0], f[1], f[2], f[3]));
               __stcg(at + p.rec_rows, make_float4(f[4], f[5], f[6], f[7]));
             }
           }
+        }
+        if (mine) {
           if (col0 == 0) {
             if (!o.whole) {
               __stcg(rec + gr, m);
@@ -537,10 +582,12 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     constexpr int kBoxRow = KV == kKv16 ? 128 : kRaw / kTreeTile;  // bytes of a token's row in a box
     const int pieces = kTreeTile / p.box_rows, boxes = pieces * NBOX;
     const int piece = lane / NBOX, bx = lane - piece * NBOX, r = piece * p.box_rows;
-    int i = 0;
+    Place at;
+    at.parity = 1;  // a slot that was never used is free
     for (; more; more = cur.next(p, o)) {
-      for (int s = 0; s < 2 * o.nt; ++s, ++i) {
-        const int slot = i % nload;
+      for (int s = 0; s < 2 * o.nt; ++s) {
+        const uint32_t slot = at.slot, parity = at.parity;
+        at.advance(1, nload);
         const int t0 = (o.tile0 + o.load_tile(s)) * kTreeTile;
         int row = 0;
         if (lane < boxes) {
@@ -554,7 +601,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
                                                : p.num_pages << p.page_shift;
           }
         }
-        if (i >= nload) wait(empty0 + 8 * slot, (i / nload - 1) & 1);
+        wait(empty0 + 8 * slot, parity);
         if (*(volatile int*)dead) continue;
         if (lane == 0) dev::mbar_arrive_expect_tx(full0 + 8 * slot, kLoadBytes);
         __syncwarp();
@@ -571,19 +618,25 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     constexpr uint32_t kIdO = tc::idesc_f16(kBf16, false, true, kTreeTile, D);
     const uint32_t q0 = dev::smem_addr(smem), slot0 = dev::smem_addr(slots);
     const bool leader = elect_one();
-    uint32_t base = 0, p_phase[2] = {0, 0};
+    Place first;  // of the portion's loads
+    uint32_t p_parity[2] = {0, 0};
     for (uint32_t k = 0;; ++k) {
       wait(q_full0 + 8 * (k & 1), (k >> 1) & 1);
       const Portion o = said[k % 3];
       if (o.nt == 0 || *(volatile int*)dead) break;
       const int jobs = o.jobs();
       tc::fence_after_sync();
+      const bool two = o.two;
+      const int nt = o.nt;
+      Place kp = first, vp = first;
+      vp.advance(two || nt == 1 ? 1 : 2, nslot);
       auto scores = [&](int j) {
-        const int w = j & 1, t = o.tile_of(j);
-        const uint32_t i = base + o.seq_k(t), slot = i % nslot;
-        wait(op_full0 + 8 * slot, (i / nslot) & 1);
+        const int w = j & 1;
+        const uint32_t slot = kp.slot;
+        wait(op_full0 + 8 * slot, kp.parity);
+        if (!two || w == 1) kp.advance(two || j > 0 ? 2 : 1, nslot);
         tc::fence_after_sync();
-        const uint32_t qa = q0 + (o.two ? w * kOperand : 0), ka = slot0 + slot * kOperand;
+        const uint32_t qa = q0 + (two ? w * kOperand : 0), ka = slot0 + slot * kOperand;
         const uint64_t qd = tc::smem_desc(qa, 16, 1024, tc::kSwizzle128B), kd = tc::smem_desc(ka, 16, 1024, tc::kSwizzle128B);
         if (leader) {
 #pragma unroll
@@ -591,7 +644,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
             tc::mma_f16_ss(w * kTmemS, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
                            kIdS, kk > 0);
           tc::commit(s_full0 + 8 * w);
-          if (!o.two || w == 1) tc::commit(op_empty0 + 8 * slot);
+          if (!two || w == 1) tc::commit(op_empty0 + 8 * slot);
           if (j == jobs - 1) tc::commit(q_empty);
         }
         __syncwarp();
@@ -599,11 +652,14 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       scores(0);
       if (jobs > 1) scores(1);
       for (int j = 0; j < jobs; ++j) {
-        const int w = j & 1, t = o.tile_of(j);
-        const uint32_t i = base + o.seq_v(t), slot = i % nslot;
-        wait(op_full0 + 8 * slot, (i / nslot) & 1);
-        wait(p_ready0 + 8 * w, p_phase[w] & 1);
-        ++p_phase[w];
+        const int w = j & 1;
+        const uint32_t slot = vp.slot;
+        wait(op_full0 + 8 * slot, vp.parity);
+        wait(p_ready0 + 8 * w, p_parity[w]);
+        p_parity[w] ^= 1;
+        // The last V, of one row tile, follows the one before it; behind it begins the next portion.
+        const int left = nt - 1 - (two ? j >> 1 : j);
+        if (!two || w == 1) vp.advance(left == 0 || (left == 1 && !two) ? 1 : 2, nslot);
         tc::fence_after_sync();
         const uint32_t va = slot0 + slot * kOperand, ps = w * kTmemS, od = kTmemO + w * kTmemS;
         const uint64_t vd = tc::smem_desc(va, kHalf, 1024, tc::kSwizzle128B);
@@ -613,13 +669,13 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
             mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8, vd + (kk * 2048 >> 4), kIdO, j > 1 || kk > 0);
             if (kBf16) mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8 + 16, vd + (kk * 2048 >> 4), kIdO, 1u);
           }
-          if (!o.two || w == 1) tc::commit(op_empty0 + 8 * slot);
+          if (!two || w == 1) tc::commit(op_empty0 + 8 * slot);
           if (j + 2 >= jobs) tc::commit(o_full0 + 8 * w);
         }
         __syncwarp();
         if (j + 2 < jobs) scores(j + 2);
       }
-      base += 2 * o.nt;
+      first = vp;
     }
     } else {
     // ---------------- queries of the items behind the first
@@ -642,41 +698,42 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     if constexpr (KV != kKv16) regs_dec<kConvertRegs>();
     // ---------------- widening of 8- and 4-bit rows
     if constexpr (KV != kKv16) {
-      constexpr int NC = 32 * convert_warps(KV);
-      const int ct = tid - 32 * kConvertWarp;
-      uint32_t i = 0;
+      // Two teams of four warps take alternate operands.  In a step of 128 threads a thread's row within 8 and its
+      // place in the row stay, so that a step is a constant offset on both sides.
+      const int ct = tid & 127, team = (warp - kConvertWarp) >> 2;
+      constexpr int kSteps = kTreeTile * CPR / 128, kBatch = 8;
+      constexpr int kBlock = kRaw / 8;                    // bytes of a 4-bit block in the ring
+      // K (and E4M3): neighbouring lanes along a row; V of 4 bits: along the tokens, whose codes lie together.
+      const int krow = ct / CPR, kch = ct % CPR, vrow = ct & 15, vch = ct >> 4;
+      const int k_to = (kch >> 3) * kHalf + krow * 128 + (((kch & 7) ^ (krow & 7)) << 4);
+      const int v_to = vrow * 128 + (((vch & 7) ^ (vrow & 7)) << 4);
+      const int vg = 8 * vch / (D / 8), swap = ((D == 128 ? vg : vg >> 1) & 1) << 2;
+      const int v_from = vg * D + ((vrow >> 1) ^ swap) * (D / 8) + (vrow & 1) * (D / 16) + (8 * vch % (D / 8)) / 2;
+      Place raw, op;
+      raw.slot = op.slot = team;
       for (; more; more = cur.next(p, o)) {
         const uint64_t any = seen_by_any(p, o.b, o.n);
-        for (int s = 0; s < 2 * o.nt; ++s, ++i) {
-          const uint32_t raw = i % nraw, slot = i % nslot;
+        for (int s = team; s < 2 * o.nt; s += 2) {
           const bool is_v = o.is_v(s);
-          const int off = o.L - o.n - (o.tile0 + o.load_tile(s)) * kTreeTile;
-          const bool edge = is_v && off < kTreeTile;      // V rows that no token sees become 0
-          wait(full0 + 8 * raw, (i / nraw) & 1);
-          if (i >= (uint32_t)nslot) wait(op_empty0 + 8 * slot, (i / nslot - 1) & 1);
-          const uint8_t* src = raws + raw * kRaw;
-          uint8_t* dst = slots + slot * kOperand;
-          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-          if (edge)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) vis[c] = seen(any, off, c);
-          auto put = [&](int row, int ch, uint4 y) {
-            const uint32_t v = row < 64 ? (row < 32 ? vis[0] : vis[1]) : (row < 96 ? vis[2] : vis[3]);
-            if (!(v >> (row & 31) & 1)) y = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(dst + (ch >> 3) * kHalf + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = y;
-          };
+          wait(full0 + 8 * raw.slot, raw.parity);
+          wait(op_empty0 + 8 * op.slot, op.parity ^ 1);
+          const uint8_t* src = raws + raw.slot * kRaw;
+          uint8_t* dst = slots + op.slot * kOperand;
           if constexpr (KV == kKvE4m3) {
-#pragma unroll 4
-            for (int c = ct; c < kTreeTile * CPR; c += NC) {
-              const int row = c / CPR, ch = c - row * CPR;
-              const uint2 x = *reinterpret_cast<const uint2*>(src + row * D + 8 * ch);
-              uint4 y;
-              dev::e4m3x4_to_f16x4(x.x, y.x, y.y);
-              dev::e4m3x4_to_f16x4(x.y, y.z, y.w);
-              put(row, ch, y);
+#pragma unroll
+            for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
+              uint2 x[kBatch];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const uint2*>(src + 8 * ct + (i0 + i) * 1024);
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                uint4 y;
+                dev::e4m3x4_to_f16x4(x[i].x, y.x, y.y);
+                dev::e4m3x4_to_f16x4(x[i].y, y.z, y.w);
+                *reinterpret_cast<uint4*>(dst + k_to + (i0 + i) * (128 / CPR) * 128) = y;
+              }
             }
           } else {
-            constexpr int kBlock = kRaw / 8;              // bytes of a block in the ring
             // Eight elements of one scale.
             auto widen = [&](uint32_t codes, uint32_t scale) {
               const uint32_t z = dev::e4m3x2_to_f16x2(scale), s2 = __byte_perm(z, z, 0x1010);
@@ -684,31 +741,53 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
               dev::e2m1x8_to_f16x8(codes, f);
               return make_uint4(dev::hmul2(f[0], s2), dev::hmul2(f[1], s2), dev::hmul2(f[2], s2), dev::hmul2(f[3], s2));
             };
-            if (!is_v) {
-#pragma unroll 4
-              for (int c = ct; c < kTreeTile * CPR; c += NC) {
-                const int row = c / CPR, ch = c - row * CPR, r = row & 15;
-                const uint8_t* blk = src + (row >> 4) * kBlock;
-                put(row, ch, widen(*reinterpret_cast<const uint32_t*>(blk + r * (D / 2) + 4 * ch), blk[8 * D + r * (D / 16) + (ch >> 1)]));
+            // A step goes 128 / CPR rows on (K), or 128 / CPR / 16 blocks, or half a row of them (V).
+            constexpr int kHalves = D / 64;               // steps per block
+#pragma unroll
+            for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
+              uint32_t x[kBatch], z[kBatch];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                const int blk = (i0 + i) / kHalves, half = (i0 + i) % kHalves;
+                const uint8_t* at = src + blk * kBlock;
+                if (is_v) {
+                  x[i] = *reinterpret_cast<const uint32_t*>(at + v_from + half * 4 * D);
+                  z[i] = at[8 * D + 16 * (vch >> 1) + vrow + half * 64];
+                } else {
+                  x[i] = *reinterpret_cast<const uint32_t*>(at + krow * (D / 2) + 4 * kch + half * 4 * D);
+                  z[i] = at[8 * D + krow * (D / 16) + (kch >> 1) + half * (D / 2)];
+                }
               }
-            } else {
-              // Tokens in neighbouring lanes: a group's 16 rows lie together.
-#pragma unroll 4
-              for (int c = ct; c < kTreeTile * CPR; c += NC) {
-                const int r = c & 15, rest = c >> 4, ch = rest % CPR, row = (rest / CPR) * 16 + r;
-                const uint8_t* blk = src + (row >> 4) * kBlock;
-                const int e = 8 * ch, g = e / (D / 8), swap = ((D == 128 ? g : g >> 1) & 1) << 2;
-                put(row, ch, widen(*reinterpret_cast<const uint32_t*>(blk + g * D + ((r >> 1) ^ swap) * (D / 8) + (r & 1) * (D / 16) + (e % (D / 8)) / 2),
-                                   blk[8 * D + 16 * (ch >> 1) + r]));
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                const int blk = (i0 + i) / kHalves, half = (i0 + i) % kHalves;
+                *reinterpret_cast<uint4*>(dst + blk * 2048 + (is_v ? v_to + half * kHalf : k_to + half * 1024)) = widen(x[i], z[i]);
               }
+            }
+          }
+          const int off = o.L - o.n - (o.tile0 + o.load_tile(s)) * kTreeTile;
+          if (is_v && off < kTreeTile) {
+            // V rows that no token sees become 0.
+            uint32_t gone[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) gone[c] = ~seen(any, off, c);
+            if (gone[0] | gone[1] | gone[2] | gone[3]) {
+              tc::named_sync(3 + team, 128);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                for (int row = krow; row < 32; row += 128 / CPR)
+                  if (gone[c] >> row & 1)
+                    *reinterpret_cast<uint4*>(dst + (kch >> 3) * kHalf + (32 * c + row) * 128 + (kch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            dev::mbar_arrive(op_full0 + 8 * slot);
-            dev::mbar_arrive(empty0 + 8 * raw);
+            dev::mbar_arrive(op_full0 + 8 * op.slot);
+            dev::mbar_arrive(empty0 + 8 * raw.slot);
           }
+          raw.advance(2, nraw);
+          op.advance(2, nslot);
         }
       }
     }
