@@ -30,8 +30,12 @@ struct VerifyParams {
 };
 
 __device__ __forceinline__ float weight(float x) { return x > 0.f ? fminf(x, 2.f) : 0.f; }
-// A weight in units of 2^-60.
-__device__ __forceinline__ uint64_t fixed(float x) { return __float2ull_rn(weight(x) * 0x1p60f); }
+// A weight in units of 2^-60 (below 2^-37 its last bits are cut): the significand, shifted by what the exponent says.
+// (The conversion instruction to 64 bits runs at the rate of fp64: 64 rows of 131072 of both took 41 us with it.)
+__device__ __forceinline__ uint64_t fixed(float x) {
+  const uint32_t b = __float_as_uint(weight(x));
+  return (uint64_t)((b << 6 & 0x1fffffc0u) | 0x20000000u) << 32 >> min(128 - (b >> 23), 63u);
+}
 __device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? a - b : 0; }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
