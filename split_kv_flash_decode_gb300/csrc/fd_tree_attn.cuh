@@ -47,6 +47,7 @@ __device__ __forceinline__ void regs_dec() {
 // Tensor memory, all of it (so that its addresses begin at 0): S (and P in its place) of the two groups, then their O.
 constexpr uint32_t kTmemAll = 512, kTmemS = 128, kTmemO = 256;
 constexpr int kMaxOperandSlots = 4;  // of 8- and 4-bit caches
+constexpr int kPrefetch = 4;         // operand tiles that a CTA brings into L2 ahead of its turn
 
 // ------------------------------------------------------------------ primitives
 
@@ -208,15 +209,18 @@ __device__ __forceinline__ uint32_t seen(uint64_t mask, int off, int k) {
   else if (lim > 0 && lim < 32) v |= (uint32_t)(mask << lim);
   return v;
 }
-// The nodes that any token of the sequence sees, by a whole warp.
-__device__ __forceinline__ uint64_t seen_by_any(const TreeParams& p, int b, int n) {
+// The nodes that any token of the sequence sees: what a lane of a whole warp looks at, and all of them together.
+__device__ __forceinline__ uint64_t seen_by_lane(const TreeParams& p, int b, int n) {
   if (p.mask == nullptr) return all_nodes(n);
   const int lane = threadIdx.x & 31;
   uint64_t m = lane < n ? p.mask[p.cu_q[b] + lane] : 0;
   if (lane + 32 < n) m |= p.mask[p.cu_q[b] + lane + 32];
+  return m & all_nodes(n);
+}
+__device__ __forceinline__ uint64_t seen_by_any(uint64_t m) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m |= __shfl_xor_sync(0xffffffffu, m, off);
-  return m & all_nodes(n);
+  return m;
 }
 
 // Waits for a barrier's phase.  Where that takes over a second the CTA is given up: the status word says so, and
@@ -317,7 +321,6 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  dev::pdl_wait();
   const Waiter wait{dead, p.status};
 
   // Writes query rows of portion q: chunks of 16 bytes, `step` threads, the first of them `from`.
@@ -327,14 +330,16 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     const T* src = reinterpret_cast<const T*>(p.q) + ((int64_t)p.cu_q[q.b] * p.Hq + q.kvh * G) * D;
     for (int c0 = from;; c0 += kBatch * step) {
       uint4 x[kBatch];
+      int64_t at[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int c = c0 + k * step;
-        if (c < total) {
-          const int gr = c / CPR, R = q.r0 + gr, t = R / G;
-          x[k] = *reinterpret_cast<const uint4*>(src + ((int64_t)t * p.Hq + (R - t * G)) * D + (c - gr * CPR) * 8);
-        }
+        const int c = c0 + k * step, gr = c / CPR, R = q.r0 + gr, t = R / G;
+        at[k] = ((int64_t)t * p.Hq + (R - t * G)) * D + (c - gr * CPR) * 8;
       }
+      if (c0 == from && parity < 0) dev::pdl_wait();
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (c0 + k * step < total) x[k] = *reinterpret_cast<const uint4*>(src + at[k]);
       // Portions but the first: the last products with Q's old rows are done.  (Threads without a chunk wait too.)
       if (c0 == from && parity >= 0) wait(q_empty, parity & 1);
 #pragma unroll
@@ -392,8 +397,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       const uint64_t nodes = all_nodes(o.n);
       uint64_t mask = 0;
       if (mine) mask = p.mask != nullptr ? p.mask[p.cu_q[o.b] + t] & nodes : all_nodes(t + 1);
-      uint64_t any = nodes;
-      if (KV == kKv16) any = seen_by_any(p, o.b, o.n);
+      const uint64_t some = KV == kKv16 ? seen_by_lane(p, o.b, o.n) : 0;
       float scale = p.scale_log2;
       if (kScaledQ && mine) scale *= __int_as_float((127 + q_exp[(nth & 1) * kTreeRows + gr]) << 23);
       float m = -INFINITY, l = 0.f;
@@ -473,11 +477,12 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
         if (KV == kKv16 && edge) {
           // V rows that no token sees (behind the sequence, of padding nodes) become 0: a weight of 0 times what they
           // hold could be NaN.
-          const uint32_t i = base + o.seq_v(tile), slot = i % nslot;
+          const uint64_t any = seen_by_any(some);
           uint32_t gone[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) gone[c] = ~seen(any, off, c);
           if (gone[0] | gone[1] | gone[2] | gone[3]) {
+            const uint32_t i = base + o.seq_v(tile), slot = i % nslot;
             wait(op_full0 + 8 * slot, (i / nslot) & 1);
             const int ch = wl % CPR;
             uint8_t* vs = slots + slot * kOperand + (ch >> 3) * kHalf + (ch & 7) * 16;
@@ -582,25 +587,27 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     constexpr int kBoxRow = KV == kKv16 ? 128 : kRaw / kTreeTile;  // bytes of a token's row in a box
     const int pieces = kTreeTile / p.box_rows, boxes = pieces * NBOX;
     const int piece = lane / NBOX, bx = lane - piece * NBOX, r = piece * p.box_rows;
+    auto row_of = [&](int t0) {
+      if (p.block_table == nullptr) return p.base[o.b] + t0;
+      // Boxes past the end of the sequence reload its last page; an index outside the pool reads zeros.
+      const int pg = min((t0 + r) >> p.page_shift, (o.L - 1) >> p.page_shift);
+      const uint32_t page = (uint32_t)p.block_table[(int64_t)o.b * p.bt_stride + pg];
+      return page < (uint32_t)p.num_pages ? (int)(page << p.page_shift) + ((t0 + r) & ((1 << p.page_shift) - 1))
+                                          : p.num_pages << p.page_shift;
+    };
+    // The first tiles into L2 while the kernels before still run.  That hands no data over, so it cannot show what they
+    // are still writing.  (A page table may itself be on its way.)
+    if (p.block_table == nullptr && lane < NBOX)
+      for (int s = 0; s < min(2 * o.nt, kPrefetch); ++s)
+        dev::tma_prefetch_l2_3d(o.is_v(s) ? &p.tm_v : &p.tm_k, bx * 64, o.kvh, row_of((o.tile0 + o.load_tile(s)) * kTreeTile) / kUnit);
+    dev::pdl_wait();
     Place at;
     at.parity = 1;  // a slot that was never used is free
     for (; more; more = cur.next(p, o)) {
       for (int s = 0; s < 2 * o.nt; ++s) {
         const uint32_t slot = at.slot, parity = at.parity;
         at.advance(1, nload);
-        const int t0 = (o.tile0 + o.load_tile(s)) * kTreeTile;
-        int row = 0;
-        if (lane < boxes) {
-          if (p.block_table == nullptr) {
-            row = p.base[o.b] + t0;
-          } else {
-            // Boxes past the end of the sequence reload its last page; an index outside the pool reads zeros.
-            const int pg = min((t0 + r) >> p.page_shift, (o.L - 1) >> p.page_shift);
-            const uint32_t page = (uint32_t)p.block_table[(int64_t)o.b * p.bt_stride + pg];
-            row = page < (uint32_t)p.num_pages ? (int)(page << p.page_shift) + ((t0 + r) & ((1 << p.page_shift) - 1))
-                                               : p.num_pages << p.page_shift;
-          }
-        }
+        const int row = lane < boxes ? row_of((o.tile0 + o.load_tile(s)) * kTreeTile) : 0;
         wait(empty0 + 8 * slot, parity);
         if (*(volatile int*)dead) continue;
         if (lane == 0) dev::mbar_arrive_expect_tx(full0 + 8 * slot, kLoadBytes);
@@ -711,8 +718,9 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       const int v_from = vg * D + ((vrow >> 1) ^ swap) * (D / 8) + (vrow & 1) * (D / 16) + (8 * vch % (D / 8)) / 2;
       Place raw, op;
       raw.slot = op.slot = team;
+      dev::pdl_wait();
       for (; more; more = cur.next(p, o)) {
-        const uint64_t any = seen_by_any(p, o.b, o.n);
+        const uint64_t some = seen_by_lane(p, o.b, o.n);
         for (int s = team; s < 2 * o.nt; s += 2) {
           const bool is_v = o.is_v(s);
           wait(full0 + 8 * raw.slot, raw.parity);
@@ -768,6 +776,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
           const int off = o.L - o.n - (o.tile0 + o.load_tile(s)) * kTreeTile;
           if (is_v && off < kTreeTile) {
             // V rows that no token sees become 0.
+            const uint64_t any = seen_by_any(some);
             uint32_t gone[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) gone[c] = ~seen(any, off, c);

@@ -57,6 +57,7 @@ class TreeDecoder(CacheCalls):
         self._q_shape, self._lse_shape = (self.tokens, self.Hq, self.d), (self.tokens, self.Hq)
         self._path_shape = (self.Bsz, self.max_drafts)
         self._cache_shape = cache_shape(self.dtype, self.Hkv, self.d, self.seqlens, 0, self.page_size)
+        self._like = {}
 
     def _launch(self, name, call, args, stream):
         index = self.device.index
@@ -66,10 +67,17 @@ class TreeDecoder(CacheCalls):
 
     def _out(self, name, t, shape, dtype, stream):
         """(tensor, address) of an output, allocated if missing."""
-        if t is None:
+        if t is not None:
+            return t, self._whole(name, t, shape, dtype)
+        if stream is None:
+            # Like one of its shape and type that is kept for this: half of torch.empty's time.
+            like = self._like.get(name)
+            if like is None:
+                like = self._like[name] = torch.empty(shape, dtype=dtype, device=self.device)
+            t = torch.empty_like(like)
+        else:
             t = empty(stream, shape, dtype, self.device)
-            return t, t.data_ptr()
-        return t, self._whole(name, t, shape, dtype)
+        return t, t.data_ptr()
 
     def __call__(self, q, k_cache, v_cache, mask=None, *, block_table=None, out=None, lse=None, status=None,
                  stream=None):
@@ -85,10 +93,14 @@ class TreeDecoder(CacheCalls):
         lse, lse_ptr = self._out("lse", lse, self._lse_shape, torch.float32, stream)
         state = self._status(status)
         if self.tokens:  # no tokens: empty tensors have null addresses
-            work = empty(stream, (self._workspace_bytes,), torch.uint8, self.device) if self._workspace_bytes else None
+            work, work_ptr = None, 0
+            if self._workspace_bytes:
+                # Of its stream's pool, and of this call alone: another call in flight cannot meet it.
+                work = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=self.device) if stream is None else \
+                    empty(stream, (self._workspace_bytes,), torch.uint8, self.device)
+                work_ptr = work.data_ptr()
             self._launch("fd_tree_decode", self._decode,
-                         (q_ptr, k, v, num_pages, table, stride, bits, out_ptr, lse_ptr,
-                          work.data_ptr() if work is not None else 0, state), stream)
+                         (q_ptr, k, v, num_pages, table, stride, bits, out_ptr, lse_ptr, work_ptr, state), stream)
         return out, lse
 
     def _rows_of(self, name, t, vocab):
