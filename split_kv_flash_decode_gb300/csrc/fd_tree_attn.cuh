@@ -112,10 +112,22 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+// Whether a barrier's phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
 }
 // A place in a ring of slots, and the parity of its barriers' phase.
 struct Place {
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
         if (KV == kKv16 && edge) {
           // V rows that no token sees (behind the sequence, of padding nodes) become 0: a weight of 0 times what they
           // hold could be NaN.
-          const uint64_t any = seen_by_any(some);
+          const uint64_t any = p.mask != nullptr ? seen_by_any(some) : nodes;
           uint32_t gone[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) gone[c] = ~seen(any, off, c);
@@ -521,42 +533,40 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       if (busy) {
         // 64 values at a time: one row tile: 32 columns of both groups; two: 64 of the group's own.
         float* rec = p.part + (int64_t)(2 * blockIdx.x + o.slot) * tree_record_floats(D, p.rec_rows);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = o.whole ? l > 0.f ? 1.f / l : 0.f : 1.f;
+        const uint64_t f0 = pair(c0 * inv, c0 * inv), f1 = pair(c1 * inv, c1 * inv);
         const int64_t out_row = (int64_t)(p.cu_q[o.b] + t) * p.Hq + o.kvh * G + (R - t * G);
         const int col0 = o.two ? 0 : w * (D / 2);
         const uint32_t oc = lanes + kTmemO + (o.two ? w * kTmemS : col0);
 #pragma unroll 1
         for (int c = 0; c < D; c += 64) {
           uint32_t y[64];
-          const int col = col0 + (o.two ? c : c / 2);
+          uint64_t f[32];
+          const int col = col0 + (o.two ? c : c / 2), pairs = o.two ? 32 : 16;
           ld32(oc + (o.two ? c : c / 2), y);
           ld32(oc + (o.two ? c + 32 : c / 2 + kTmemS), y + 32);
           tc::wait_ld();
-          if (!o.two) {
-            // A coefficient of 0 takes no part: the group had no tile, or no token that the row sees.
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float f = c0 != 0.f ? __uint_as_float(y[k]) * c0 : 0.f;
-              if (both && c1 != 0.f) f = fmaf(__uint_as_float(y[k + 32]), c1, f);
-              y[k] = __float_as_uint(f);
-            }
+          for (int k = 0; k < 32; ++k)
+            f[k] = mul_pair(pair(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), f0);
+          if (both) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              f[k] = fma_pair(pair(__uint_as_float(y[2 * k + 32]), __uint_as_float(y[2 * k + 33])), f1, f[k]);
           }
           if (!mine) continue;
 #pragma unroll
-          for (int k = 0; k < 64; k += 8) {
-            if (k >= 32 && !o.two) break;
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(y[k + i]);
+          for (int k = 0; k < 32; k += 4) {
+            if (k >= pairs) break;
+            const float2 a = unpair(f[k]), b = unpair(f[k + 1]), d = unpair(f[k + 2]), e = unpair(f[k + 3]);
             if (o.whole) {
-              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + out_row * D + col + k) =
-                  make_uint4(dev::pack2<T>(f[0] * inv, f[1] * inv), dev::pack2<T>(f[2] * inv, f[3] * inv),
-                             dev::pack2<T>(f[4] * inv, f[5] * inv), dev::pack2<T>(f[6] * inv, f[7] * inv));
+              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + out_row * D + col + 2 * k) =
+                  make_uint4(dev::pack2<T>(a.x, a.y), dev::pack2<T>(b.x, b.y), dev::pack2<T>(d.x, d.y), dev::pack2<T>(e.x, e.y));
             } else {
               // Column by column: the rows of a warp lie together.
-              float4* at = reinterpret_cast<float4*>(rec + 2 * p.rec_rows) + (int64_t)((col + k) / 4) * p.rec_rows + gr;
-              __stcg(at, make_float4(f[0], f[1], f[2], f[3]));
-              __stcg(at + p.rec_rows, make_float4(f[4], f[5], f[6], f[7]));
+              float4* at = reinterpret_cast<float4*>(rec + 2 * p.rec_rows) + (int64_t)((col + 2 * k) / 4) * p.rec_rows + gr;
+              __stcg(at, make_float4(a.x, a.y, b.x, b.y));
+              __stcg(at + p.rec_rows, make_float4(d.x, d.y, e.x, e.y));
             }
           }
         }
@@ -637,50 +647,60 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       const int nt = o.nt;
       Place kp = first, vp = first;
       vp.advance(two || nt == 1 ? 1 : 2, nslot);
-      auto scores = [&](int j) {
+      // S of job j, whose K is there: issued by the leader.
+      auto scores = [&](int j, uint32_t slot) {
         const int w = j & 1;
-        const uint32_t slot = kp.slot;
-        wait(op_full0 + 8 * slot, kp.parity);
-        if (!two || w == 1) kp.advance(two || j > 0 ? 2 : 1, nslot);
-        tc::fence_after_sync();
-        const uint32_t qa = q0 + (two ? w * kOperand : 0), ka = slot0 + slot * kOperand;
-        const uint64_t qd = tc::smem_desc(qa, 16, 1024, tc::kSwizzle128B), kd = tc::smem_desc(ka, 16, 1024, tc::kSwizzle128B);
-        if (leader) {
+        const uint32_t at = ((two ? w * kOperand : 0) + q0), ka = slot0 + slot * kOperand;
+        const uint64_t qd = tc::smem_desc(at, 16, 1024, tc::kSwizzle128B), kd = tc::smem_desc(ka, 16, 1024, tc::kSwizzle128B);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_f16_ss(w * kTmemS, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
-                           kIdS, kk > 0);
-          tc::commit(s_full0 + 8 * w);
-          if (!two || w == 1) tc::commit(op_empty0 + 8 * slot);
-          if (j == jobs - 1) tc::commit(q_empty);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_f16_ss(w * kTmemS, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                         kIdS, kk > 0);
+        tc::commit(s_full0 + 8 * w);
+        if (!two || w == 1) tc::commit(op_empty0 + 8 * slot);
+        if (j == jobs - 1) tc::commit(q_empty);
       };
-      scores(0);
-      if (jobs > 1) scores(1);
+      auto next_k = [&](int j) { if (!two || (j & 1)) kp.advance(two || j > 0 ? 2 : 1, nslot); };
+      for (int j = 0; j < min(jobs, 2); ++j) {
+        wait(op_full0 + 8 * kp.slot, kp.parity);
+        tc::fence_after_sync();
+        if (leader) scores(j, kp.slot);
+        __syncwarp();
+        next_k(j);
+      }
       for (int j = 0; j < jobs; ++j) {
         const int w = j & 1;
         const uint32_t slot = vp.slot;
+        const bool again = j + 2 < jobs;
         wait(op_full0 + 8 * slot, vp.parity);
         wait(p_ready0 + 8 * w, p_parity[w]);
-        p_parity[w] ^= 1;
-        // The last V, of one row tile, follows the one before it; behind it begins the next portion.
-        const int left = nt - 1 - (two ? j >> 1 : j);
-        if (!two || w == 1) vp.advance(left == 0 || (left == 1 && !two) ? 1 : 2, nslot);
+        // If the next K is there too, its product goes out with P.V: nothing comes between them.
+        const bool both = again && __all_sync(0xffffffffu, mbar_test(op_full0 + 8 * kp.slot, kp.parity));
         tc::fence_after_sync();
-        const uint32_t va = slot0 + slot * kOperand, ps = w * kTmemS, od = kTmemO + w * kTmemS;
-        const uint64_t vd = tc::smem_desc(va, kHalf, 1024, tc::kSwizzle128B);
+        const uint64_t vd = tc::smem_desc(slot0 + slot * kOperand, kHalf, 1024, tc::kSwizzle128B);
         if (leader) {
+          const uint32_t ps = w * kTmemS, od = kTmemO + w * kTmemS;
 #pragma unroll
           for (int kk = 0; kk < kTreeTile / 16; ++kk) {
             mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8, vd + (kk * 2048 >> 4), kIdO, j > 1 || kk > 0);
             if (kBf16) mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8 + 16, vd + (kk * 2048 >> 4), kIdO, 1u);
           }
           if (!two || w == 1) tc::commit(op_empty0 + 8 * slot);
-          if (j + 2 >= jobs) tc::commit(o_full0 + 8 * w);
+          if (!again) tc::commit(o_full0 + 8 * w);
+          if (both) scores(j + 2, kp.slot);
         }
         __syncwarp();
-        if (j + 2 < jobs) scores(j + 2);
+        if (again && !both) {
+          wait(op_full0 + 8 * kp.slot, kp.parity);
+          tc::fence_after_sync();
+          if (leader) scores(j + 2, kp.slot);
+          __syncwarp();
+        }
+        if (again) next_k(j + 2);
+        p_parity[w] ^= 1;
+        // The last V, of one row tile, follows the one before it; behind it begins the next portion.
+        const int left = nt - 1 - (two ? j >> 1 : j);
+        if (!two || w == 1) vp.advance(left == 0 || (left == 1 && !two) ? 1 : 2, nslot);
       }
       first = vp;
     }
