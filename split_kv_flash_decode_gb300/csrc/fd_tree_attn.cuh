@@ -24,14 +24,14 @@ namespace fd {
 namespace tree {
 
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kQueryWarp = 10, kQueryWarps = 2, kConvertWarp = 12;
-FD_HD constexpr int convert_warps(int kv) { return kv == kKv16 ? 0 : 8; }
+FD_HD constexpr int convert_warps(int kv) { return kv == kKv16 ? 0 : 4; }
 FD_HD constexpr int threads(int kv) { return 32 * (kConvertWarp + convert_warps(kv)); }
 // Registers per thread: at launch (what the compiler takes for that many threads), then softmax, warps 8-11, and
 // converters.  A softmax thread holds a row's 128 scores.
-FD_HD constexpr int launch_regs(int kv) { return kv == kKv16 ? 168 : 96; }
-FD_HD constexpr int softmax_regs(int kv) { return kv == kKv16 ? 208 : 168; }
-FD_HD constexpr int other_regs(int kv) { return kv == kKv16 ? 88 : 56; }
-constexpr int kConvertRegs = 40;
+FD_HD constexpr int launch_regs(int kv) { return kv == kKv16 ? 168 : 128; }
+FD_HD constexpr int softmax_regs(int kv) { return kv == kKv16 ? 216 : 192; }
+FD_HD constexpr int other_regs(int kv) { return kv == kKv16 ? 72 : 56; }
+constexpr int kConvertRegs = 72;
 FD_HD constexpr bool regs_fit(int kv) {
   return 256 * softmax_regs(kv) + 128 * other_regs(kv) + 32 * convert_warps(kv) * kConvertRegs <= threads(kv) * launch_regs(kv);
 }
@@ -725,17 +725,25 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     if constexpr (KV != kKv16) regs_dec<kConvertRegs>();
     // ---------------- widening of 8- and 4-bit rows
     if constexpr (KV != kKv16) {
-      // Two teams of four warps take alternate operands.  In a step of 128 threads a thread's row within 8 and its
-      // place in the row stay, so that a step is a constant offset on both sides.
-      const int ct = tid & 127, team = (warp - kConvertWarp) >> 2;
+      // Two teams of two warps take alternate operands.  A step takes 64 chunks twice over, as 128 threads would: from
+      // one to the next a chunk's row within 8 and its place in the row stay, a constant offset on both sides.
+      const int team = (warp - kConvertWarp) >> 1;
       constexpr int kSteps = kTreeTile * CPR / 128, kBatch = 8;
       constexpr int kBlock = kRaw / 8;                    // bytes of a 4-bit block in the ring
       // K (and E4M3): neighbouring lanes along a row; V of 4 bits: along the tokens, whose codes lie together.
-      const int krow = ct / CPR, kch = ct % CPR, vrow = ct & 15, vch = ct >> 4;
-      const int k_to = (kch >> 3) * kHalf + krow * 128 + (((kch & 7) ^ (krow & 7)) << 4);
-      const int v_to = vrow * 128 + (((vch & 7) ^ (vrow & 7)) << 4);
-      const int vg = 8 * vch / (D / 8), swap = ((D == 128 ? vg : vg >> 1) & 1) << 2;
-      const int v_from = vg * D + ((vrow >> 1) ^ swap) * (D / 8) + (vrow & 1) * (D / 16) + (8 * vch % (D / 8)) / 2;
+      int krow[2], kch, vrow, vch[2], k_to[2], v_to[2], v_from[2];
+      kch = (tid & 63) % CPR;
+      vrow = tid & 15;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int ct = (tid & 63) + 64 * v;
+        krow[v] = ct / CPR;
+        vch[v] = ct >> 4;
+        k_to[v] = (kch >> 3) * kHalf + krow[v] * 128 + (((kch & 7) ^ (krow[v] & 7)) << 4);
+        v_to[v] = vrow * 128 + (((vch[v] & 7) ^ (vrow & 7)) << 4);
+        const int g = 8 * vch[v] / (D / 8), swap = ((D == 128 ? g : g >> 1) & 1) << 2;
+        v_from[v] = g * D + ((vrow >> 1) ^ swap) * (D / 8) + (vrow & 1) * (D / 16) + (8 * vch[v] % (D / 8)) / 2;
+      }
       Place raw, op;
       raw.slot = op.slot = team;
       dev::pdl_wait();
@@ -750,15 +758,16 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
           if constexpr (KV == kKvE4m3) {
 #pragma unroll
             for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
-              uint2 x[kBatch];
+              uint2 x[2 * kBatch];
 #pragma unroll
-              for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const uint2*>(src + 8 * ct + (i0 + i) * 1024);
+              for (int i = 0; i < 2 * kBatch; ++i)
+                x[i] = *reinterpret_cast<const uint2*>(src + 8 * (tid & 63) + (i & 1) * 512 + (i0 + i / 2) * 1024);
 #pragma unroll
-              for (int i = 0; i < kBatch; ++i) {
+              for (int i = 0; i < 2 * kBatch; ++i) {
                 uint4 y;
                 dev::e4m3x4_to_f16x4(x[i].x, y.x, y.y);
                 dev::e4m3x4_to_f16x4(x[i].y, y.z, y.w);
-                *reinterpret_cast<uint4*>(dst + k_to + (i0 + i) * (128 / CPR) * 128) = y;
+                *reinterpret_cast<uint4*>(dst + k_to[i & 1] + (i0 + i / 2) * (128 / CPR) * 128) = y;
               }
             }
           } else {
@@ -773,23 +782,23 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
             constexpr int kHalves = D / 64;               // steps per block
 #pragma unroll
             for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
-              uint32_t x[kBatch], z[kBatch];
+              uint32_t x[2 * kBatch], z[2 * kBatch];
 #pragma unroll
-              for (int i = 0; i < kBatch; ++i) {
-                const int blk = (i0 + i) / kHalves, half = (i0 + i) % kHalves;
+              for (int i = 0; i < 2 * kBatch; ++i) {
+                const int v = i & 1, blk = (i0 + i / 2) / kHalves, half = (i0 + i / 2) % kHalves;
                 const uint8_t* at = src + blk * kBlock;
                 if (is_v) {
-                  x[i] = *reinterpret_cast<const uint32_t*>(at + v_from + half * 4 * D);
-                  z[i] = at[8 * D + 16 * (vch >> 1) + vrow + half * 64];
+                  x[i] = *reinterpret_cast<const uint32_t*>(at + v_from[v] + half * 4 * D);
+                  z[i] = at[8 * D + 16 * (vch[v] >> 1) + vrow + half * 64];
                 } else {
-                  x[i] = *reinterpret_cast<const uint32_t*>(at + krow * (D / 2) + 4 * kch + half * 4 * D);
-                  z[i] = at[8 * D + krow * (D / 16) + (kch >> 1) + half * (D / 2)];
+                  x[i] = *reinterpret_cast<const uint32_t*>(at + krow[v] * (D / 2) + 4 * kch + half * 4 * D);
+                  z[i] = at[8 * D + krow[v] * (D / 16) + (kch >> 1) + half * (D / 2)];
                 }
               }
 #pragma unroll
-              for (int i = 0; i < kBatch; ++i) {
-                const int blk = (i0 + i) / kHalves, half = (i0 + i) % kHalves;
-                *reinterpret_cast<uint4*>(dst + blk * 2048 + (is_v ? v_to + half * kHalf : k_to + half * 1024)) = widen(x[i], z[i]);
+              for (int i = 0; i < 2 * kBatch; ++i) {
+                const int v = i & 1, blk = (i0 + i / 2) / kHalves, half = (i0 + i / 2) % kHalves;
+                *reinterpret_cast<uint4*>(dst + blk * 2048 + (is_v ? v_to[v] + half * kHalf : k_to[v] + half * 1024)) = widen(x[i], z[i]);
               }
             }
           }
@@ -801,10 +810,10 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
 #pragma unroll
             for (int c = 0; c < 4; ++c) gone[c] = ~seen(any, off, c);
             if (gone[0] | gone[1] | gone[2] | gone[3]) {
-              tc::named_sync(3 + team, 128);
+              tc::named_sync(3 + team, 64);
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                for (int row = krow; row < 32; row += 128 / CPR)
+                for (int row = krow[0]; row < 32; row += 64 / CPR)
                   if (gone[c] >> row & 1)
                     *reinterpret_cast<uint4*>(dst + (kch >> 3) * kHalf + (32 * c + row) * 128 + (kch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
