@@ -416,7 +416,10 @@ int encode_cache(CUtensorMap* map, const fd_tree_s* t, const void* cache, int nu
                     : is_bf16(t->dtype) ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                     cache, dims, strides, box, kind == kKv16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                    kind == kKvE2m1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+                    // A head's row: its neighbours are other heads', which other CTAs read at other times.
+                    row >= 256 && kind != kKvE2m1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                    : row >= 128                  ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                  : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
 }
 // Whether an output overlaps an input or another output.
 template <size_t N, size_t M>

@@ -19,23 +19,16 @@ FD_HD constexpr int tree_operand_bytes(int d) { return kTreeTile * d * 2; }
 FD_HD constexpr int tree_raw_bytes(int kv, int d) {
   return kv == kKvE2m1 ? kTreeTile * ring_row_bytes(kPathMmaKv4, d) : kTreeTile * d;
 }
-// Whether items of at most 64 query rows spread each row over several lanes ("Copies" in fd_tree_attn.cuh): where the
-// softmax would be slower than a tile's bytes, so not over 16-bit caches with d = 128; in plans of one row tile.
-FD_HD constexpr bool tree_spreads(int kv, int d) { return kv != kKv16 || d == 64; }
-constexpr int kTreeScratch = 16 * 1024;  // the copies' sums
 constexpr int kTreeSmemTiles = 224 * 1024;
-FD_HD constexpr int tree_tile_bytes(int kv, int d, int q_tiles) {
-  return kTreeSmemTiles - (tree_spreads(kv, d) && q_tiles == 1 ? kTreeScratch : 0);
-}
 constexpr int kTreeMaxSlots = 14;
 FD_HD constexpr int tree_slots(int kv, int d, int q_tiles) {
-  return kv == kKv16 ? tree_tile_bytes(kv, d, q_tiles) / tree_operand_bytes(d) - q_tiles : d == 128 ? 3 : 4;
+  return kv == kKv16 ? kTreeSmemTiles / tree_operand_bytes(d) - q_tiles : d == 128 ? 5 - q_tiles : 4;
 }
 // An even number: the two converter teams take alternate loads, so each slot is one team's alone.  (With an odd one a
 // team could wait for a slot's next phase before the other's load, which may land later, has ended the phase before; a
 // parity does not tell the two apart.)
 FD_HD constexpr int tree_raw_slots(int kv, int d, int q_tiles) {
-  const int room = tree_tile_bytes(kv, d, q_tiles) - (q_tiles + tree_slots(kv, d, q_tiles)) * tree_operand_bytes(d);
+  const int room = kTreeSmemTiles - (q_tiles + tree_slots(kv, d, q_tiles)) * tree_operand_bytes(d);
   const int n = room / tree_raw_bytes(kv, d) / 2 * 2;
   return kv == kKv16 ? 0 : n > 12 ? 12 : n;
 }

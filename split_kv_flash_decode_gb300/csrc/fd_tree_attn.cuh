@@ -47,7 +47,6 @@ __device__ __forceinline__ void regs_dec() {
 // Tensor memory, all of it (so that its addresses begin at 0): S (and P in its place) of the two groups, then their O.
 constexpr uint32_t kTmemAll = 512, kTmemS = 128, kTmemO = 256;
 constexpr int kMaxOperandSlots = 4;  // of 8- and 4-bit caches
-constexpr int kCopyTiles = 2;        // tiles from which a row is spread over copies
 constexpr int kPrefetch = 4;         // operand tiles that a CTA brings into L2 ahead of its turn
 
 // ------------------------------------------------------------------ primitives
@@ -123,13 +122,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Whether a barrier's phase is over, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
 // A place in a ring of slots, and the parity of its barriers' phase.
 struct Place {
   uint32_t slot = 0, parity = 0;
@@ -157,7 +149,6 @@ struct Portion {
   bool two;    // two row tiles; else one, and the groups take alternate tiles of tokens
   bool whole;  // all tiles of the item
   bool slot;   // the CTA's record: 0 of the item it goes on with, 1 of the item it leaves unfinished
-  int8_t copies;  // lanes of a query row (one row tile): 1, 2 or 4
   __device__ __forceinline__ int jobs() const { return two ? 2 * nt : nt; }
   __device__ __forceinline__ int tile_of(int job) const { return two ? job >> 1 : job; }
   // Places of a tile's K and V among the portion's 2 nt loads: in the order in which the products want them.
@@ -184,7 +175,6 @@ struct Cursor {
     }
     b = lo;
   }
-  template <bool SPREAD>
   __device__ __forceinline__ bool next(const TreeParams& p, Portion& o) {
     while (u < u1) {
       while (p.unit_base[b + 1] <= u) ++b;
@@ -207,7 +197,6 @@ struct Cursor {
       o.nt = hi - lo;
       o.whole = lo == 0 && hi == tiles;
       o.slot = lo == 0;
-      o.copies = !SPREAD || p.q_tiles == 2 || o.nt < kCopyTiles || o.rows > 64 ? 1 : o.rows > 32 ? 2 : 4;
       return true;
     }
     return false;
@@ -264,30 +253,19 @@ struct Waiter {
 
 // ------------------------------------------------------------------ softmax
 
-// A row's weights of one tile: the NCH chunks of 32 columns from `chunk0` on (all of them, or a copy's share; its other
-// weights are then 0).  ts, to: its lane's S and O; first: O holds nothing yet.
-template <int NCH, int D, typename Op>
-__device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, int chunk0, bool edge, uint64_t mask, int off, float scale,
-                                      bool mine, bool first, float& m, float& l) {
+// A row's weights of one tile.  ts, to: its lane's S (which its weights replace) and O; first: O holds nothing yet.
+template <int D, typename Op>
+__device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint64_t mask, int off, float scale, bool mine,
+                                      bool first, float& m, float& l) {
   constexpr bool kBf16 = std::is_same<Op, __nv_bfloat16>::value;
-  if constexpr (NCH < 4) {
-    uint32_t zero[32] = {};
+  uint32_t x[128];
 #pragma unroll
-    for (int c = NCH; c < 4; ++c) {
-      // Not before the chunk's scores could be read: nobody reads them.
-      if constexpr (kBf16) st32(ts + 32 * ((chunk0 + c) & 3), zero);
-      else st16(ts + 32 * ((chunk0 + c) & 3), zero);
-    }
-    ts += 32 * chunk0;
-  }
-  uint32_t x[32 * NCH];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) ld32(ts + 32 * c, x + 32 * c);
+  for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, x + 32 * c);
   tc::wait_ld();
   if (edge) {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const uint32_t v = seen(mask, off, chunk0 + c);
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t v = seen(mask, off, c);
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         if (!(v >> k & 1)) x[32 * c + k] = 0xff800000u;
@@ -295,7 +273,7 @@ __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, int chunk0, bool
   }
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int k = 0; k < 32 * NCH; k += 8)
+  for (int k = 0; k < 128; k += 8)
 #pragma unroll
     for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(x[k + 2 * c]), __uint_as_float(x[k + 2 * c + 1]));
   const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale;
@@ -321,7 +299,7 @@ __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, int chunk0, bool
   const uint64_t scale2 = pair(scale, scale), minus2 = pair(-mm, -mm);
   uint64_t sum[2] = {0, 0};
 #pragma unroll
-  for (int c = 0; c < NCH; ++c) {
+  for (int c = 0; c < 4; ++c) {
     uint32_t y[32];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -356,7 +334,6 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
   constexpr bool kScaledQ = std::is_same<T, __nv_bfloat16>::value && !kBf16;
   constexpr int kOperand = tree_operand_bytes(D), kRaw = tree_raw_bytes(KV, D), kHalf = kTreeTile * 128;
   constexpr int CPR = D / 8;  // 16-byte chunks of a row
-  constexpr bool kSpread = tree_spreads(KV, D);
   extern __shared__ __align__(1024) uint8_t smem[];
   const int q_tiles = p.q_tiles, nslot = tree_slots(KV, D, q_tiles), nraw = tree_raw_slots(KV, D, q_tiles);
   uint8_t* slots = smem + q_tiles * kOperand;
@@ -415,7 +392,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
   bool more = false;
   if (warp >= kLoadWarp) {
     cur = Cursor(p, blockIdx.x);
-    more = cur.template next<kSpread>(p, o);
+    more = cur.next(p, o);
     if (!more) o = Portion{};  // a run may lie within what an item costs beyond its tiles
     if (warp == kQueryWarp && lane == 0) said[0] = o;
   }
@@ -468,10 +445,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
             if (ch == 0) q_exp[((parity + 1) & 1) * kTreeRows + gr] = (int8_t)-up;
           }
           const int tile = q.two && gr >= q.row_tile ? 1 : 0, r = gr - tile * q.row_tile;
-          uint8_t* to = smem + tile * kOperand + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(to) = x[k];
-          if constexpr (kSpread)
-            for (int i = 1; i < q.copies; ++i) *reinterpret_cast<uint4*>(to + i * (kTreeTile * 128) / q.copies) = x[k];
+          *reinterpret_cast<uint4*>(smem + tile * kOperand + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x[k];
         }
       }
       if (c0 + kBatch * step >= total) break;
@@ -493,12 +467,10 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       const Portion o = said[nth % 3];
       if (o.nt == 0) break;
       const int jobs = o.jobs(), G = p.G;
-      const int per_copy = kSpread ? kTreeTile / o.copies : kTreeTile;
-      const int copy = kSpread ? wl / per_copy : 0, row = wl - copy * per_copy;  // place in the row tile
-      const int gr = (o.two ? w * o.row_tile : 0) + row;  // row of the item
+      const int gr = (o.two ? w * o.row_tile : 0) + wl;   // row of the item
       const int rows_here = o.two ? (w ? o.rows - o.row_tile : min(o.rows, o.row_tile)) : o.rows;
-      const bool mine = row < rows_here;
-      const bool busy = (row & ~31) < rows_here;          // this warp has rows
+      const bool mine = wl < rows_here;
+      const bool busy = (wl & ~31) < rows_here;           // this warp has rows
       const int R = o.r0 + gr, t = mine ? R / G : 0;
       const uint64_t nodes = all_nodes(o.n);
       uint64_t mask = 0;
@@ -515,10 +487,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
         __syncwarp();
         tc::fence_after_sync();
         if (busy) {
-          const bool first = j <= 1;
-          if (!kSpread || o.copies == 1) weigh<4, D, Op>(ts, to, 0, edge, mask, off, scale, mine, first, m, l);
-          else if (o.copies == 2) weigh<2, D, Op>(ts, to, 2 * copy, edge, mask, off, scale, mine, first, m, l);
-          else weigh<1, D, Op>(ts, to, copy, edge, mask, off, scale, mine, first, m, l);
+          weigh<D, Op>(ts, to, edge, mask, off, scale, mine, j <= 1, m, l);
           tc::wait_st();
         }
         if (KV == kKv16 && edge) {
@@ -558,32 +527,19 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       tc::fence_after_sync();
       float c0 = 1.f, c1 = 0.f;
       if (!o.two) {
-        // The groups' results of alternate tiles (and the copies' of their columns).
+        // The groups' results of alternate tiles: each takes half the columns of both.
         tc::named_sync(1, 256);
-        const float m0 = ml[2 * wl], m1 = ml[256 + 2 * wl];
-        m = fmaxf(m0, m1);
-        if constexpr (kSpread) {
-          for (int i = 1; i < o.copies; ++i) {
-            const int at = (wl + i * per_copy) & (kTreeTile - 1);
-            m = max3(m, ml[2 * at], ml[256 + 2 * at]);
-          }
-        }
-        c0 = m0 == -INFINITY ? 0.f : dev::ex2(m0 - m);
-        c1 = m1 == -INFINITY ? 0.f : dev::ex2(m1 - m);
-        l = c0 * ml[2 * wl + 1] + c1 * ml[256 + 2 * wl + 1];
-        if constexpr (kSpread) {
-          for (int i = 1; i < o.copies; ++i) {
-            const int at = (wl + i * per_copy) & (kTreeTile - 1);
-            const float2 a = *reinterpret_cast<const float2*>(ml + 2 * at), b = *reinterpret_cast<const float2*>(ml + 256 + 2 * at);
-            l += (a.x == -INFINITY ? 0.f : dev::ex2(a.x - m) * a.y) + (b.x == -INFINITY ? 0.f : dev::ex2(b.x - m) * b.y);
-          }
-        }
+        const float2 a = *reinterpret_cast<const float2*>(ml + 2 * wl), b = *reinterpret_cast<const float2*>(ml + 256 + 2 * wl);
+        m = fmaxf(a.x, b.x);
+        c0 = a.x == -INFINITY ? 0.f : dev::ex2(a.x - m);
+        c1 = b.x == -INFINITY ? 0.f : dev::ex2(b.x - m);
+        l = c0 * a.y + c1 * b.y;
       }
       float* rec = p.part + (int64_t)(2 * blockIdx.x + o.slot) * tree_record_floats(D, p.rec_rows);
       const float inv = o.whole ? l > 0.f ? 1.f / l : 0.f : 1.f;
       const uint64_t f0 = pair(c0 * inv, c0 * inv), f1 = pair(c1 * inv, c1 * inv);
       const int64_t out_row = (int64_t)(p.cu_q[o.b] + t) * p.Hq + o.kvh * G + (R - t * G);
-      if (mine && (o.two || w == 0) && copy == 0) {
+      if (mine && (o.two || w == 0)) {
         if (!o.whole) {
           __stcg(rec + gr, m);
           __stcg(rec + p.rec_rows + gr, l);
@@ -592,47 +548,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
         }
       }
       __syncwarp();
-      if (kSpread && o.copies > 1) {
-        // Copies lie in lanes of different warps: 16 columns at a time go through shared memory, [4][128 lanes] of 16
-        // bytes, where a thread adds up the copies of one row.  Each group takes half the columns, of both groups.
-        float4* sums = reinterpret_cast<float4*>(smem + tree_tile_bytes(KV, D, 1)) + w * 512;
-        const int srow = wl & (per_copy - 1), sR = o.r0 + srow, st = sR / G;
-        const int64_t s_out = (int64_t)(p.cu_q[o.b] + st) * p.Hq + o.kvh * G + (sR - st * G);
-#pragma unroll 1
-        for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 16) {
-          float y0[16], y1[16];
-          tc::ld16(lanes + kTmemO + c, y0);
-          if (both) tc::ld16(lanes + kTmemO + kTmemS + c, y1);
-          tc::wait_ld();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint64_t a = mul_pair(pair(y0[4 * k], y0[4 * k + 1]), f0), b = mul_pair(pair(y0[4 * k + 2], y0[4 * k + 3]), f0);
-            if (both) {
-              a = fma_pair(pair(y1[4 * k], y1[4 * k + 1]), f1, a);
-              b = fma_pair(pair(y1[4 * k + 2], y1[4 * k + 3]), f1, b);
-            }
-            const float2 x = unpair(a), z = unpair(b);
-            sums[k * 128 + wl] = make_float4(x.x, x.y, z.x, z.y);
-          }
-          tc::named_sync(5 + w, 128);
-          for (int k = wl / per_copy; k < 4; k += o.copies) {
-            float4 s = sums[k * 128 + srow];
-            for (int i = 1; i < o.copies; ++i) {
-              const float4 x = sums[k * 128 + i * per_copy + srow];
-              s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-            }
-            if (srow < o.rows) {
-              if (o.whole)
-                *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + s_out * D + c + 4 * k) =
-                    make_uint2(dev::pack2<T>(s.x, s.y), dev::pack2<T>(s.z, s.w));
-              else
-                __stcg(reinterpret_cast<float4*>(rec + 2 * p.rec_rows) + (int64_t)(c / 4 + k) * p.rec_rows + srow, s);
-            }
-          }
-          __syncwarp();
-          tc::named_sync(5 + w, 128);
-        }
-      } else if (busy) {
+      if (busy) {
         // 64 values at a time: one row tile: 32 columns of both groups; two: 64 of the group's own.
         const int col0 = o.two ? 0 : w * (D / 2);
         const uint32_t oc = lanes + kTmemO + (o.two ? w * kTmemS : col0);
@@ -686,8 +602,10 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     constexpr int kBoxRow = KV == kKv16 ? 128 : kRaw / kTreeTile;  // bytes of a token's row in a box
     const int pieces = kTreeTile / p.box_rows, boxes = pieces * NBOX;
     const int piece = lane / NBOX, bx = lane - piece * NBOX, r = piece * p.box_rows;
+    const bool paged = p.block_table != nullptr;
+    // Cache row of a tile, or of this lane's piece of it.
     auto row_of = [&](int t0) {
-      if (p.block_table == nullptr) return p.base[o.b] + t0;
+      if (!paged) return p.base[o.b] + t0;
       // Boxes past the end of the sequence reload its last page; an index outside the pool reads zeros.
       const int pg = min((t0 + r) >> p.page_shift, (o.L - 1) >> p.page_shift);
       const uint32_t page = (uint32_t)p.block_table[(int64_t)o.b * p.bt_stride + pg];
@@ -696,26 +614,47 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     };
     // The first tiles into L2 while the kernels before still run.  That hands no data over, so it cannot show what they
     // are still writing.  (A page table may itself be on its way.)
-    if (p.block_table == nullptr && lane < NBOX)
+    if (!paged && lane < NBOX)
       for (int s = 0; s < min(2 * o.nt, kPrefetch); ++s)
         dev::tma_prefetch_l2_3d(o.is_v(s) ? &p.tm_v : &p.tm_k, bx * 64, o.kvh, row_of((o.tile0 + o.load_tile(s)) * kTreeTile) / kUnit);
     dev::pdl_wait();
+    const uint32_t ring = dev::smem_addr(KV == kKv16 ? slots : raws);
     Place at;
     at.parity = 1;  // a slot that was never used is free
-    for (; more; more = cur.template next<kSpread>(p, o)) {
-      for (int s = 0; s < 2 * o.nt; ++s) {
-        const uint32_t slot = at.slot, parity = at.parity;
-        at.advance(1, nload);
-        const int row = lane < boxes ? row_of((o.tile0 + o.load_tile(s)) * kTreeTile) : 0;
-        wait(empty0 + 8 * slot, parity);
-        if (__any_sync(0xffffffffu, *(volatile int*)dead)) continue;
-        if (lane == 0) dev::mbar_arrive_expect_tx(full0 + 8 * slot, kLoadBytes);
-        __syncwarp();
-        if (lane < boxes) {
-          const uint32_t dst = dev::smem_addr(KV == kKv16 ? slots + slot * kOperand : raws + slot * kRaw);
-          dev::tma_load_3d(dst + bx * kHalf + r * kBoxRow, o.is_v(s) ? &p.tm_v : &p.tm_k, bx * 64, o.kvh, row / kUnit,
-                           full0 + 8 * slot, policy);
+    for (; more; more = cur.next(p, o)) {
+      const int loads = 2 * o.nt, kvh = o.kvh;
+      const bool two = o.two;
+      int next_t[2] = {o.tile0 * kTreeTile, o.tile0 * kTreeTile};  // of K, of V
+      bool v = false;
+      for (int s = 0; s < loads; ++s) {
+        const int t0 = next_t[v];
+        const uint32_t bar = full0 + 8 * at.slot, dst = ring + at.slot * (KV == kKv16 ? kOperand : kRaw);
+        const CUtensorMap* map = v ? &p.tm_v : &p.tm_k;
+        if (pieces == 1) {
+          // One lane: all columns of a tile (of a page, where one holds it).
+          if (lane == 0) {
+            const int row = row_of(t0) / kUnit;
+            wait(empty0 + 8 * at.slot, at.parity);
+            if (!*(volatile int*)dead) {
+              dev::mbar_arrive_expect_tx(bar, kLoadBytes);
+#pragma unroll
+              for (int i = 0; i < NBOX; ++i) dev::tma_load_3d(dst + i * kHalf, map, i * 64, kvh, row, bar, policy);
+            }
+          }
+        } else {
+          const int row = lane < boxes ? row_of(t0) / kUnit : 0;
+          wait(empty0 + 8 * at.slot, at.parity);
+          if (!__any_sync(0xffffffffu, *(volatile int*)dead)) {
+            if (lane == 0) dev::mbar_arrive_expect_tx(bar, kLoadBytes);
+            __syncwarp();
+            if (lane < boxes) dev::tma_load_3d(dst + bx * kHalf + r * kBoxRow, map, bx * 64, kvh, row, bar, policy);
+          }
         }
+        at.advance(1, nload);
+        next_t[v] = t0 + kTreeTile;
+        // K and V in turn, but of one row tile the second K comes ahead of the first V.
+        v = two || s > 0 || loads == 2 ? !v : false;
+        if (s == loads - 2) v = true;
       }
     }
     } else if (warp == kMmaWarp) {
@@ -751,23 +690,22 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       };
       auto next_k = [&](int j) { if (!two || (j & 1)) kp.advance(two || j > 0 ? 2 : 1, nslot); };
       for (int j = 0; j < min(jobs, 2); ++j) {
-        wait(op_full0 + 8 * kp.slot, kp.parity);
-        tc::fence_after_sync();
-        if (leader) scores(j, kp.slot);
-        __syncwarp();
+        if (leader) {
+          wait(op_full0 + 8 * kp.slot, kp.parity);
+          tc::fence_after_sync();
+          scores(j, kp.slot);
+        }
         next_k(j);
       }
       for (int j = 0; j < jobs; ++j) {
         const int w = j & 1;
         const uint32_t slot = vp.slot;
         const bool again = j + 2 < jobs;
-        wait(op_full0 + 8 * slot, vp.parity);
-        wait(p_ready0 + 8 * w, p_parity[w]);
-        // If the next K is there too, its product goes out with P.V: nothing comes between them.
-        const bool both = again && __all_sync(0xffffffffu, mbar_test(op_full0 + 8 * kp.slot, kp.parity));
-        tc::fence_after_sync();
-        const uint64_t vd = tc::smem_desc(slot0 + slot * kOperand, kHalf, 1024, tc::kSwizzle128B);
         if (leader) {
+          wait(op_full0 + 8 * slot, vp.parity);
+          wait(p_ready0 + 8 * w, p_parity[w]);
+          tc::fence_after_sync();
+          const uint64_t vd = tc::smem_desc(slot0 + slot * kOperand, kHalf, 1024, tc::kSwizzle128B);
           const uint32_t ps = w * kTmemS, od = kTmemO + w * kTmemS;
 #pragma unroll
           for (int kk = 0; kk < kTreeTile / 16; ++kk) {
@@ -775,15 +713,13 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
             if (kBf16) mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8 + 16, vd + (kk * 2048 >> 4), kIdO, 1u);
           }
           if (!two || w == 1) tc::commit(op_empty0 + 8 * slot);
-          if (!again) tc::commit(o_full0 + 8 * w);
-          if (both) scores(j + 2, kp.slot);
-        }
-        __syncwarp();
-        if (again && !both) {
-          wait(op_full0 + 8 * kp.slot, kp.parity);
-          tc::fence_after_sync();
-          if (leader) scores(j + 2, kp.slot);
-          __syncwarp();
+          if (!again) {
+            tc::commit(o_full0 + 8 * w);
+          } else {
+            wait(op_full0 + 8 * kp.slot, kp.parity);
+            tc::fence_after_sync();
+            scores(j + 2, kp.slot);
+          }
         }
         if (again) next_k(j + 2);
         p_parity[w] ^= 1;
@@ -801,7 +737,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     tc::named_sync(2, 256 + 32 * kQueryWarps);
     if (lane == 0) dev::mbar_arrive(q_full0);
     for (uint32_t k = 1; more; ++k) {
-      more = cur.template next<kSpread>(p, o);
+      more = cur.next(p, o);
       if (more) put_queries(o, tid - 32 * kQueryWarp, 32 * kQueryWarps, (int)k - 1);
       else wait(q_empty, (k - 1) & 1);
       if (!more) o.nt = 0;
@@ -836,7 +772,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       Place raw, op;
       raw.slot = op.slot = team;
       dev::pdl_wait();
-      for (; more; more = cur.template next<kSpread>(p, o)) {
+      for (; more; more = cur.next(p, o)) {
         const uint64_t some = seen_by_lane(p, o.b, o.n);
         for (int s = team; s < 2 * o.nt; s += 2) {
           const bool is_v = o.is_v(s);
