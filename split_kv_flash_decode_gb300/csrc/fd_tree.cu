@@ -477,13 +477,15 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
   }
   // Units of work: the tiles of every item, and what an item costs beyond them.
   const int G = Hq / Hkv;
-  int64_t units = 0, tiles = 0;
-  int rows = 0;
+  int64_t units = 0, tiles = 0, all_items = 0;
+  int rows = 0, longest = 0;
   for (int b = 0; b < B; ++b) {
     if (!drafts[b]) continue;
     const int64_t items = (int64_t)Hkv * fd::tree_groups(drafts[b] * G);
     units += items * (fd::tree_tiles(seqlens[b]) + fd::kTreeItemUnits);
     tiles += items * fd::tree_tiles(seqlens[b]);
+    all_items += items;
+    longest = std::max(longest, fd::tree_tiles(seqlens[b]));
     rows = std::max(rows, drafts[b] * G);
   }
   if (units >= limit) return FD_ERR_UNSUPPORTED;
@@ -499,6 +501,8 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
   p.box_rows = page_size ? std::min(fd::kTreeTile, page_size) : fd::kTreeTile;
   p.q_tiles = rows > fd::kTreeTile ? 2 : 1;
   p.rec_rows = fd::kTreeTile * p.q_tiles;
+  p.whole_items = longest <= fd::kTreeWholeTiles && all_items <= std::min(num_sms, fd::kTreeMaxCtas);
+  if (p.whole_items) units = tiles = all_items;
   p.ctas = (int)std::min<int64_t>({tiles, (int64_t)num_sms, (int64_t)fd::kTreeMaxCtas});
   if (p.ctas) {
     p.run_len = (int32_t)(units / p.ctas);
@@ -515,11 +519,11 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
     base += four ? ((int64_t)seqlens[b] + fd::kBlockTokens - 1) / fd::kBlockTokens * fd::kBlockTokens : seqlens[b];
     if (!drafts[b]) continue;
     // The runs that begin behind an item's first tile: the first of them combines the item's records.
-    const int items = Hkv * fd::tree_groups(drafts[b] * G), per = fd::tree_tiles(seqlens[b]) + fd::kTreeItemUnits;
+    const int items = Hkv * fd::tree_groups(drafts[b] * G), per = fd::tree_item_units(p, fd::tree_tiles(seqlens[b]));
     int last = -1;
     for (; cta < p.ctas && fd::tree_run_begin(p, cta) < unit + items * per; ++cta) {
       const int at = fd::tree_run_begin(p, cta) - unit, item = at / per;
-      if (at - item * per <= fd::kTreeItemUnits || item == last) continue;
+      if (p.whole_items || at - item * per <= fd::kTreeItemUnits || item == last) continue;
       p.split[t->splits++] = (uint16_t)cta;
       last = item;
     }

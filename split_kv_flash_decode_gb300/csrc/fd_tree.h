@@ -12,6 +12,8 @@ constexpr int kTreeRows = 256;    // query rows that stream the cache together: 
 constexpr int kTreeMaxCtas = 512;
 // What an item (a sequence's KV head and up to kTreeRows of its query rows) costs a CTA beyond its tiles, in tiles.
 constexpr int kTreeItemUnits = 2;
+// Items of at most this many tiles, no more of them than SMs, are each one CTA's: combining records would take longer.
+constexpr int kTreeWholeTiles = 3;
 
 // One CTA: operand tiles in the 16-bit swizzled layout (Q, then K and V in a ring of slots); over 8- and 4-bit
 // caches a second ring of the rows as they are stored, which converter warps widen into the operand slots.
@@ -57,16 +59,18 @@ struct TreeParams {
   int32_t q_tiles;         // 1 or 2 tiles of query rows at most in an item
   int32_t rec_rows;        // kTreeTile x q_tiles
   int32_t ctas, run_len, run_extra;  // units per CTA; the first run_extra CTAs take one more
+  int32_t whole_items;     // 1: a unit is an item, one for each CTA; else a tile
   float scale_log2;        // log2(e) / sqrt(d)
   int32_t cu_q[FD_MAX_BATCH + 1];
   int32_t len[FD_MAX_BATCH];
   int32_t base[FD_MAX_BATCH];           // contiguous caches: cache row (in tokens) of the sequence's row 0
-  int32_t unit_base[FD_MAX_BATCH + 1];  // prefix sums of units: items x (tiles + kTreeItemUnits)
+  int32_t unit_base[FD_MAX_BATCH + 1];  // prefix sums of units: items x (tiles + kTreeItemUnits), or items
   uint16_t split[kTreeMaxCtas];         // CTAs whose run begins within an item, the first one of each item
 };
 
 FD_HD int tree_groups(int rows) { return (rows + kTreeRows - 1) / kTreeRows; }
 FD_HD int tree_tiles(int L) { return (int)(((int64_t)L + kTreeTile - 1) / kTreeTile); }
+FD_HD int tree_item_units(const TreeParams& p, int tiles) { return p.whole_items ? 1 : tiles + kTreeItemUnits; }
 FD_HD int tree_run_begin(const TreeParams& p, int cta) {
   return cta * p.run_len + (cta < p.run_extra ? cta : p.run_extra);
 }

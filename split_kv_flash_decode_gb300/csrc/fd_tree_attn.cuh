@@ -181,11 +181,12 @@ struct Cursor {
       o.b = b;
       o.L = p.len[b];
       o.n = p.cu_q[b + 1] - p.cu_q[b];
-      const int tiles = tree_tiles(o.L), per = tiles + kTreeItemUnits, rows = o.n * p.G, groups = tree_groups(rows);
+      const int tiles = tree_tiles(o.L), per = tree_item_units(p, tiles), rows = o.n * p.G, groups = tree_groups(rows);
       const int at = u - p.unit_base[b], item = at / per, off = at - item * per;
       const int end = min(u1 - u + off, per);
       u += end - off;
-      const int lo = max(0, off - kTreeItemUnits), hi = max(0, end - kTreeItemUnits);
+      const int lo = p.whole_items ? 0 : max(0, off - kTreeItemUnits);
+      const int hi = p.whole_items ? tiles : max(0, end - kTreeItemUnits);
       if (hi <= lo) continue;
       o.kvh = item / groups;
       o.r0 = (item - o.kvh * groups) * kTreeRows;
