@@ -568,7 +568,7 @@ int fd_tree_decode(fd_tree_t tree, const void* q, const void* k, const void* v, 
  * other); weights without a sum are replaced by the target's, and if that has none the token is -1.
  *
  *   target         device float [T, vocab], rows target_stride elements apart (>= vocab); probabilities:
- *                  NaN and negative values count as 0, values over 2 as 2
+ *                  NaN and negative values count as 0, values over 1 as 1
  *   draft          device float [T, vocab], rows draft_stride apart, or NULL
  *   vocab          1 .. FD_MAX_VOCAB
  *   tokens         device int32 [T]; a token outside [0, vocab) never stands
@@ -580,8 +580,8 @@ int fd_tree_decode(fd_tree_t tree, const void* q, const void* k, const void* v, 
  *                  token, then -1 (so count tokens)
  *   count          device int32 [B], written: nodes that stand (0 for a sequence without drafted tokens)
  *
- * The products and differences of probabilities are exact or in 64 bits; sums of weights are in units of 2^-60,
- * so that they do not depend on an order (a row's sum must stay below 8).
+ * Products and differences of probabilities are exact or in 64 bits, sums of weights hold 2^-40 of a row's sum
+ * (which must stay below 8).
  * FD_ERR_INVALID: a missing pointer, a short stride, an output that overlaps an input or another output;
  * FD_ERR_UNSUPPORTED: draft with parents, vocab; FD_ERR_ALIGN: a pointer not 4-byte aligned.  T = 0 still
  * writes count (and max_drafts = 0: nothing else).

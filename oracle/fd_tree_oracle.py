@@ -41,8 +41,8 @@ def tree_reference(q, k, v, seqlens, sees):
 
 
 def weights(p):
-    """Probabilities as they count: NaN and negative values 0, at most 2."""
-    return np.clip(np.nan_to_num(np.asarray(p, dtype=np.float64), nan=0.0, posinf=2.0, neginf=0.0), 0.0, 2.0)
+    """Probabilities as they count: NaN and negative values 0, at most 1."""
+    return np.clip(np.nan_to_num(np.asarray(p, dtype=np.float64), nan=0.0, posinf=1.0, neginf=0.0), 0.0, 1.0)
 
 
 def verify_walk(target, tokens, uniform, parents=None, draft=None):

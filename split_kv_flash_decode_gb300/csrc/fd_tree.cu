@@ -29,13 +29,62 @@ struct VerifyParams {
   int32_t cu[FD_MAX_BATCH + 1];
 };
 
-__device__ __forceinline__ float weight(float x) { return x > 0.f ? fminf(x, 2.f) : 0.f; }
-// A weight in units of 2^-60 (below 2^-37 its last bits are cut): the significand, shifted by what the exponent says.
-// (The conversion instruction to 64 bits runs at the rate of fp64: 64 rows of 131072 of both took 41 us with it.)
-__device__ __forceinline__ uint64_t fixed(float x) {
-  const uint32_t b = __float_as_uint(weight(x));
-  return (uint64_t)((b << 6 & 0x1fffffc0u) | 0x20000000u) << 32 >> min(128 - (b >> 23), 63u);
+// A probability as it counts: NaN as 0.
+__device__ __forceinline__ float weight(float x) { return __saturatef(x); }
+// A value in [0, 16) in units of 2^-57 (below 2^-34 its last bits are cut): the significand, shifted by what the
+// exponent says.  (The conversion instruction to 64 bits runs at the rate of fp64.)
+__device__ __forceinline__ uint64_t fixed_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return (uint64_t)((b << 5 & 0x0fffffe0u) | 0x10000000u) << 32 >> min(130 - (b >> 23), 63u);
 }
+__device__ __forceinline__ uint64_t fixed(float x) { return fixed_of(weight(x)); }
+// A thread's sum of weights: two running sums (of the even and the odd ones) with what their additions and differences
+// rounded away beside them, so that some dozens of weights are off by 2^-46 of their sum.  All on the fp32 pipe, two
+// values an instruction; in 64-bit integers the sums took longer than the rows' bytes (64 rows of 131072 of both: 25 us).
+struct Sum {
+  uint64_t high = 0, low = 0;
+  static __device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+  }
+  static __device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+  }
+  static __device__ __forceinline__ uint64_t minus(uint64_t a, uint64_t b) {  // a - b, rounded once
+    uint64_t r;
+    asm("{\n\t.reg .b64 m;\n\tmov.b64 m, 0xbf800000bf800000;\n\tfma.rn.f32x2 %0, %2, m, %1;\n\t}" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+  }
+  // The sum and its rounding error (Knuth).
+  __device__ __forceinline__ void accumulate(uint64_t w, uint64_t e) {
+    const uint64_t s = plus(high, w), z = minus(s, high);
+    low = plus(low, plus(plus(minus(high, minus(s, z)), minus(w, z)), e));
+    high = s;
+  }
+  __device__ __forceinline__ void add(float a, float b) { accumulate(pair(weight(a), weight(b)), 0); }
+  // max(a - qa, 0) and max(b - qb, 0): the difference and its rounding error, or neither.
+  __device__ __forceinline__ void add_left(float a, float qa, float b, float qb) {
+    const uint64_t x = pair(weight(a), weight(b)), y = pair(weight(qa), weight(qb));
+    const uint64_t s = minus(x, y), v = minus(s, x);
+    const float2 d = unpair(s), e = unpair(minus(minus(x, minus(s, v)), plus(y, v)));
+    accumulate(pair(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f)), pair(d.x > 0.f ? e.x : 0.f, d.y > 0.f ? e.y : 0.f));
+  }
+  // In units of 2^-57.
+  __device__ __forceinline__ uint64_t fixed_sum() const {
+    const float2 h = unpair(high), l = unpair(low);
+    const float rest = l.x + l.y;
+    const uint64_t sum = fixed_of(h.x) + fixed_of(h.y), r = fixed_of(fabsf(rest));
+    return rest >= 0.f ? sum + r : sum > r ? sum - r : 0;
+  }
+};
 __device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? a - b : 0; }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -62,6 +111,7 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
   __shared__ uint64_t warp_sum[2][kVerifyWarps];
   __shared__ uint64_t slice_sum[2][kVerifyCluster];
   __shared__ uint64_t stands_s, tried_s;
+  __shared__ int last_s;
   dev::pdl_launch_dependents();
   dev::pdl_wait();
   const int b = blockIdx.x / kVerifyCluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -156,9 +206,9 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
   const float u0 = p.uniform[first];
   const float* target = p.target + (first + node) * p.target_stride;
   // The slice of this CTA, and this warp's part of it.
-  const int per_cta = (V + kVerifyCluster - 1) / kVerifyCluster;
-  const int c0 = min((int)rank * per_cta, V), c1 = min(c0 + per_cta, V);
-  const int per_warp = (c1 - c0 + kVerifyWarps - 1) / kVerifyWarps;
+  constexpr int kParts = kVerifyCluster * kVerifyWarps, kStep = 128;
+  const int per_warp = ((V + kParts - 1) / kParts + kStep - 1) / kStep * kStep;
+  const int c0 = min((int)rank * kVerifyWarps * per_warp, V), c1 = min(c0 + kVerifyWarps * per_warp, V);
   const int w0 = min(c0 + warp * per_warp, c1), w1 = min(w0 + per_warp, c1);
 
   for (int attempt = 0;; ++attempt) {
@@ -166,24 +216,46 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
     const bool rest = attempt == 0 && tried != 0;
     const float* draft = rest && p.draft != nullptr ? p.draft + (first + __ffsll((long long)tried) - 1) * p.draft_stride : nullptr;
     const uint64_t gone = rest && p.draft == nullptr ? tried : 0;
-    uint64_t sum = 0;
-    if (draft != nullptr) {
-#pragma unroll 8
-      for (int i = w0 + lane; i < w1; i += 32) sum += less(fixed(target[i]), fixed(draft[i]));
-    } else {
-#pragma unroll 16
-      for (int i = w0 + lane; i < w1; i += 32) sum += fixed(target[i]);
+    Sum part;
+    int at0 = w0 + lane;
+    // 16 bytes at a time where both rows allow it.
+    if (((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) & 15) == 0) {
+      const int whole = w1 & ~3;
+      if (draft != nullptr) {
+#pragma unroll 4
+        for (int i = w0 + 4 * lane; i < whole; i += kStep) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(target + i)), b = __ldg(reinterpret_cast<const float4*>(draft + i));
+          part.add_left(a.x, b.x, a.y, b.y);
+          part.add_left(a.z, b.z, a.w, b.w);
+        }
+      } else {
+#pragma unroll 4
+        for (int i = w0 + 4 * lane; i < whole; i += kStep) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(target + i));
+          part.add(a.x, a.y);
+          part.add(a.z, a.w);
+        }
+      }
+      at0 = max(w0, whole) + lane;
     }
+#pragma unroll 4
+    for (int i = at0; i < w1; i += 64) {
+      const int j = min(i + 32, w1 - 1);                 // past the end: weighs nothing
+      const float a = target[i], b = i + 32 < w1 ? target[j] : 0.f;
+      if (draft != nullptr) part.add_left(a, draft[i], b, i + 32 < w1 ? draft[j] : 0.f);
+      else part.add(a, b);
+    }
+    uint64_t sum = part.fixed_sum();
     // Tokens that were tried weigh nothing; one that was tried twice goes once.
     for (uint64_t m = gone; m != 0; m &= m - 1) {
       const int i = __ffsll((long long)m) - 1, t = tokens[i];
       bool again = false;
       for (uint64_t e = gone & ((1ull << i) - 1); e != 0; e &= e - 1) again |= tokens[__ffsll((long long)e) - 1] == t;
-      if (t >= w0 && t < w1 && ((t - w0) & 31) == lane && !again) sum -= fixed(target[t]);
+      if (t >= w0 && t < w1 && lane == 0 && !again) sum -= fixed(target[t]);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) warp_sum[attempt][warp] = sum;
+    if (lane == 0) warp_sum[attempt][warp] = (int64_t)sum > 0 ? sum : 0;
     __syncthreads();
     if (tid < kVerifyCluster) {
       uint64_t all = 0;
@@ -208,6 +280,8 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
     int w = 0;
     while (at >= before + warp_sum[attempt][w]) before += warp_sum[attempt][w++];
     const int s0 = min(c0 + w * per_warp, c1), s1 = min(s0 + per_warp, c1);
+    int heavy = -1;  // this thread's last token with a weight
+    if (tid == 0) last_s = -1;
     // All threads look through that warp's part: eight tokens each.
     for (int at0 = s0; at0 < s1; at0 += 8 * kVerifyThreads) {
       uint64_t x[8], mine = 0;
@@ -225,7 +299,10 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
           if (t == k) x[k] = 0;
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mine += x[k];
+      for (int k = 0; k < 8; ++k) {
+        mine += x[k];
+        if (x[k] != 0) heavy = i0 + k;
+      }
       uint64_t upto = mine;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -254,6 +331,10 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
       }
       if (at < before) return;  // the same in every thread
     }
+    // The weights one by one came to less than their sum by 2^-46 of it: the last of them.
+    if (heavy >= 0) atomicMax(&last_s, heavy);
+    __syncthreads();
+    if (tid == 0) p.emitted[(int64_t)b * p.max_drafts + __popcll(stands) - 1] = last_s;
     return;
   }
 }
