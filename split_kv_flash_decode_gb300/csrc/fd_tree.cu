@@ -558,18 +558,17 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
   }
   // Units of work: the tiles of every item, and what an item costs beyond them.
   const int G = Hq / Hkv;
-  int64_t units = 0, tiles = 0, all_items = 0;
+  int64_t tiles = 0, all_items = 0;
   int rows = 0, longest = 0;
   for (int b = 0; b < B; ++b) {
     if (!drafts[b]) continue;
     const int64_t items = (int64_t)Hkv * fd::tree_groups(drafts[b] * G);
-    units += items * (fd::tree_tiles(seqlens[b]) + fd::kTreeItemUnits);
     tiles += items * fd::tree_tiles(seqlens[b]);
     all_items += items;
     longest = std::max(longest, fd::tree_tiles(seqlens[b]));
     rows = std::max(rows, drafts[b] * G);
   }
-  if (units >= limit) return FD_ERR_UNSUPPORTED;
+  if (tiles + all_items * fd::kTreeMaxItemUnits >= limit) return FD_ERR_UNSUPPORTED;
   fd_tree_s* t = new (std::nothrow) fd_tree_s();
   if (!t) return FD_ERR_NOMEM;
   t->B = B; t->Hq = Hq; t->Hkv = Hkv; t->d = d; t->dtype = dtype; t->page_size = page_size;
@@ -583,8 +582,10 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
   p.q_tiles = rows > fd::kTreeTile ? 2 : 1;
   p.rec_rows = fd::kTreeTile * p.q_tiles;
   p.whole_items = longest <= fd::kTreeWholeTiles && all_items <= std::min(num_sms, fd::kTreeMaxCtas);
-  if (p.whole_items) units = tiles = all_items;
+  if (p.whole_items) tiles = all_items;
   p.ctas = (int)std::min<int64_t>({tiles, (int64_t)num_sms, (int64_t)fd::kTreeMaxCtas});
+  p.item_units = p.ctas ? (int)std::clamp<int64_t>(tiles * 3 / 4 / p.ctas, fd::kTreeMinItemUnits, fd::kTreeMaxItemUnits) : 0;
+  const int64_t units = p.whole_items ? all_items : tiles + all_items * p.item_units;
   if (p.ctas) {
     p.run_len = (int32_t)(units / p.ctas);
     p.run_extra = (int32_t)(units % p.ctas);
@@ -604,7 +605,7 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
     int last = -1;
     for (; cta < p.ctas && fd::tree_run_begin(p, cta) < unit + items * per; ++cta) {
       const int at = fd::tree_run_begin(p, cta) - unit, item = at / per;
-      if (p.whole_items || at - item * per <= fd::kTreeItemUnits || item == last) continue;
+      if (p.whole_items || at - item * per <= p.item_units || item == last) continue;
       p.split[t->splits++] = (uint16_t)cta;
       last = item;
     }

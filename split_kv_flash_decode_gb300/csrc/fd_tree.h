@@ -10,8 +10,11 @@ namespace fd {
 constexpr int kTreeTile = 128;    // tokens of a tile, and query rows of one
 constexpr int kTreeRows = 256;    // query rows that stream the cache together: two tiles
 constexpr int kTreeMaxCtas = 512;
-// What an item (a sequence's KV head and up to kTreeRows of its query rows) costs a CTA beyond its tiles, in tiles.
-constexpr int kTreeItemUnits = 2;
+// What an item (a sequence's KV head and up to kTreeRows of its query rows) costs a CTA beyond its tiles, in tiles: up to
+// 10, as much as its records and its end take, so that few items are cut in two; 3/4 of a CTA's tiles where it has few, so
+// that small work still spreads.  (With 2, 6, 10 and 17: 32K tokens with a tree of 16: 30.8, 28.3, 26.9, 26.9 us; a ragged
+// batch of 17: 56.6, 30.2, 29.4, 31.3; 517 tokens: 7.3, 7.8, 8.6, 8.9.)
+constexpr int kTreeMinItemUnits = 2, kTreeMaxItemUnits = 10;
 // Items of at most this many tiles, no more of them than SMs, are each one CTA's: combining records would take longer.
 constexpr int kTreeWholeTiles = 3;
 
@@ -60,17 +63,18 @@ struct TreeParams {
   int32_t rec_rows;        // kTreeTile x q_tiles
   int32_t ctas, run_len, run_extra;  // units per CTA; the first run_extra CTAs take one more
   int32_t whole_items;     // 1: a unit is an item, one for each CTA; else a tile
+  int32_t item_units;      // units of an item beyond its tiles
   float scale_log2;        // log2(e) / sqrt(d)
   int32_t cu_q[FD_MAX_BATCH + 1];
   int32_t len[FD_MAX_BATCH];
   int32_t base[FD_MAX_BATCH];           // contiguous caches: cache row (in tokens) of the sequence's row 0
-  int32_t unit_base[FD_MAX_BATCH + 1];  // prefix sums of units: items x (tiles + kTreeItemUnits), or items
+  int32_t unit_base[FD_MAX_BATCH + 1];  // prefix sums of units: items x (tiles + item_units), or items
   uint16_t split[kTreeMaxCtas];         // CTAs whose run begins within an item, the first one of each item
 };
 
 FD_HD int tree_groups(int rows) { return (rows + kTreeRows - 1) / kTreeRows; }
 FD_HD int tree_tiles(int L) { return (int)(((int64_t)L + kTreeTile - 1) / kTreeTile); }
-FD_HD int tree_item_units(const TreeParams& p, int tiles) { return p.whole_items ? 1 : tiles + kTreeItemUnits; }
+FD_HD int tree_item_units(const TreeParams& p, int tiles) { return p.whole_items ? 1 : tiles + p.item_units; }
 FD_HD int tree_run_begin(const TreeParams& p, int cta) {
   return cta * p.run_len + (cta < p.run_extra ? cta : p.run_extra);
 }

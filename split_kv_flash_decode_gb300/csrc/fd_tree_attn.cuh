@@ -185,8 +185,8 @@ struct Cursor {
       const int at = u - p.unit_base[b], item = at / per, off = at - item * per;
       const int end = min(u1 - u + off, per);
       u += end - off;
-      const int lo = p.whole_items ? 0 : max(0, off - kTreeItemUnits);
-      const int hi = p.whole_items ? tiles : max(0, end - kTreeItemUnits);
+      const int lo = p.whole_items ? 0 : max(0, off - p.item_units);
+      const int hi = p.whole_items ? tiles : max(0, end - p.item_units);
       if (hi <= lo) continue;
       o.kvh = item / groups;
       o.r0 = (item - o.kvh * groups) * kTreeRows;
@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(kCombineThreads) fd_tree_combine_kernel(const 
     if (p.unit_base[mid] <= u) b = mid; else hi = mid;
   }
   const int n = p.cu_q[b + 1] - p.cu_q[b], all = n * p.G, groups = tree_groups(all);
-  const int per = tree_tiles(p.len[b]) + kTreeItemUnits, item = (u - p.unit_base[b]) / per;
+  const int per = tree_item_units(p, tree_tiles(p.len[b])), item = (u - p.unit_base[b]) / per;
   const int end = p.unit_base[b] + (item + 1) * per;
   const int kvh = item / groups, r0 = (item - kvh * groups) * kTreeRows, rows = min(all - r0, kTreeRows);
   const int gr = rb * 32 + lane;
