@@ -656,3 +656,27 @@ def test_wrapper_checks(fd):
     none = fd.TreeDecoder(4, 2, 64, [5, 6], [0, 0])
     path, emitted, count = none.verify(p[:0], tok[:0], u[:0])
     assert path.shape == (2, 0) and count.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f16_e4m3kv", "f16_e2m1kv", "bf16_e2m1kv"])
+def test_one_drafted_token_is_a_decode(fd, dtype):
+    """A chain of one over many long sequences, each CTA through several of them, against the decode of the same cache."""
+    import torch
+    B, L, Hq, Hkv, d = 24, 5000, 32, 8, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    t16 = torch.bfloat16 if dtype.startswith("bf16") else torch.float16
+    x = torch.randn((B * L, Hq + 2 * Hkv, d), device="cuda", generator=g).to(t16)
+    caches = [torch.empty(fd.cache_shape(dtype, Hkv, d, [L] * B), dtype=torch.uint8 if "kv" in dtype else t16, device="cuda")
+              for _ in "kv"]
+    fd.KVRows(Hq, Hkv, d, [L] * B, dtype=dtype).append(None, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], *caches)
+    q = x[L - 1::L, :Hq].contiguous()
+    tree = fd.TreeDecoder(Hq, Hkv, d, [L] * B, [1] * B, dtype)
+    want = fd.Decoder(Hq, Hkv, d, [L] * B, [4] * B, dtype)(q, *caches)
+    for _ in range(20):
+        got = tree(q, *caches)
+        # Two roundings of the output and two of the weights (each 2^-11 of at most max |V| < 6); lse as for decodes.
+        eps = 2.0 ** -8 if dtype.startswith("bf16") else 2.0 ** -11
+        assert (np.abs(f64(got[0]) - f64(want[0])) <= 2 * eps * np.abs(f64(want[0])) + 2.0 ** -9 * 6).all()
+        assert np.abs(f64(got[1]) - f64(want[1])).max() <= 2 * LSE_TOL
+    # Their 2-norms are nearer: rounding errors do not line up.
+    assert np.linalg.norm(f64(got[0]) - f64(want[0])) <= 2 * eps * np.linalg.norm(f64(want[0]))
