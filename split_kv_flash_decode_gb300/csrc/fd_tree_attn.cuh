@@ -871,18 +871,19 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
 
 // ------------------------------------------------------------------ combination
 
-// 32 query rows (lanes) by 16 columns of one item that several CTAs share: the warps take its records in turn, then
-// add up.  Bound by the latency of the records' loads from L2: four independent 16-byte loads of each record.
-constexpr int kCombineThreads = 256, kCombineCols = 16;
-template <typename T, int D>
-__global__ void __launch_bounds__(kCombineThreads) fd_tree_combine_kernel(const __grid_constant__ TreeParams p) {
-  constexpr int NW = kCombineThreads / 32, NC = D / kCombineCols;
-  __shared__ float sm_m[NW][32], sm_l[NW][32];
-  __shared__ float4 sm_o[NW][kCombineCols / 4][32];
+// 32 query rows (lanes) of one item that several CTAs share: a warp takes an eighth of the columns and every GROUPS-th
+// record, then the groups meet in shared memory.  Bound by the latency of the records' loads from L2: more groups where
+// records are many or blocks few.  (Always 8: 64 heads x 64 drafts over 32K tokens 81.6 us instead of 77; always 2: 4K
+// tokens, with 19 records an item, 16.5 us instead of 11.3.)
+FD_HD constexpr int combine_parts(int groups) { return groups == 2 ? 8 : groups == 4 ? 4 : 1; }  // eighths of a block
+template <typename T, int D, int GROUPS>
+__global__ void __launch_bounds__(32 * GROUPS * combine_parts(GROUPS)) fd_tree_combine_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int NQ = D / 32, PARTS = combine_parts(GROUPS);  // NQ: groups of four columns of a warp
+  __shared__ float sm_m[GROUPS - 1][PARTS][32], sm_l[GROUPS - 1][PARTS][32];
+  __shared__ float4 sm_o[GROUPS - 1][PARTS][NQ][32];
   dev::pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = p.split[blockIdx.y];
-  const int rb = blockIdx.x / NC, col = (blockIdx.x - rb * NC) * kCombineCols;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, place = warp % PARTS, group = warp / PARTS;
+  const int cta = p.split[blockIdx.y], rb = blockIdx.x, part = blockIdx.z * PARTS + place, col = part * (D / 8);
   // The item that CTA `cta` goes on with; CTA cta - 1 began it.
   const int u = tree_run_begin(p, cta);
   int b = 0, hi = p.B;
@@ -898,22 +899,23 @@ __global__ void __launch_bounds__(kCombineThreads) fd_tree_combine_kernel(const 
   if (rb * 32 >= rows) return;
   int records = 1;
   while (cta + records - 1 < p.ctas && tree_run_begin(p, cta + records - 1) < end) ++records;
-  dev::pdl_wait();
   const int64_t size = tree_record_floats(D, p.rec_rows);
   auto record = [&](int i) { return p.part + (int64_t)(2 * (cta - 1 + i) + (i == 0)) * size; };
+  dev::pdl_wait();
   float m = -INFINITY, l = 0.f;
-  for (int i = warp; i < records; i += NW) m = fmaxf(m, __ldcg(record(i) + gr));
-  float4 acc[kCombineCols / 4];
+#pragma unroll 4
+  for (int i = group; i < records; i += GROUPS) m = fmaxf(m, __ldcg(record(i) + gr));
+  float4 acc[NQ];
 #pragma unroll
-  for (int k = 0; k < kCombineCols / 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int i = warp; i < records; i += NW) {
+  for (int k = 0; k < NQ; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = group; i < records; i += GROUPS) {
     const float* rec = record(i);
     const float mi = __ldcg(rec + gr), li = __ldcg(rec + p.rec_rows + gr);
     const float c = mi == -INFINITY ? 0.f : dev::ex2(mi - m);
     l = fmaf(c, li, l);
 #pragma unroll
-    for (int k = 0; k < kCombineCols / 4; ++k) {
+    for (int k = 0; k < NQ; ++k) {
       const float4 x = __ldcg(reinterpret_cast<const float4*>(rec + 2 * p.rec_rows) + (int64_t)(col / 4 + k) * p.rec_rows + gr);
       acc[k].x = fmaf(c, x.x, acc[k].x);
       acc[k].y = fmaf(c, x.y, acc[k].y);
@@ -921,33 +923,43 @@ __global__ void __launch_bounds__(kCombineThreads) fd_tree_combine_kernel(const 
       acc[k].w = fmaf(c, x.w, acc[k].w);
     }
   }
-  sm_m[warp][lane] = m;
-  sm_l[warp][lane] = l;
+  if (group > 0) {
+    sm_m[group - 1][place][lane] = m;
+    sm_l[group - 1][place][lane] = l;
 #pragma unroll
-  for (int k = 0; k < kCombineCols / 4; ++k) sm_o[warp][k][lane] = acc[k];
-  __syncthreads();
-  if (warp >= kCombineCols / 4 || gr >= rows) return;
-  float M = -INFINITY, Lsum = 0.f;
-#pragma unroll
-  for (int i = 0; i < NW; ++i) M = fmaxf(M, sm_m[i][lane]);
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    const float c = sm_m[i][lane] == -INFINITY ? 0.f : dev::ex2(sm_m[i][lane] - M);
-    const float4 x = sm_o[i][warp][lane];
-    Lsum = fmaf(c, sm_l[i][lane], Lsum);
-    a.x = fmaf(c, x.x, a.x);
-    a.y = fmaf(c, x.y, a.y);
-    a.z = fmaf(c, x.z, a.z);
-    a.w = fmaf(c, x.w, a.w);
+    for (int k = 0; k < NQ; ++k) sm_o[group - 1][place][k][lane] = acc[k];
   }
-  const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
+  __syncthreads();
+  if (group > 0 || gr >= rows) return;
+  float top = m;
+#pragma unroll
+  for (int g = 0; g < GROUPS - 1; ++g) top = fmaxf(top, sm_m[g][place][lane]);
+  const float c0 = m == -INFINITY ? 0.f : dev::ex2(m - top);
+  l *= c0;
+#pragma unroll
+  for (int k = 0; k < NQ; ++k) acc[k] = make_float4(acc[k].x * c0, acc[k].y * c0, acc[k].z * c0, acc[k].w * c0);
+#pragma unroll
+  for (int g = 0; g < GROUPS - 1; ++g) {
+    const float mg = sm_m[g][place][lane], c = mg == -INFINITY ? 0.f : dev::ex2(mg - top);
+    l = fmaf(c, sm_l[g][place][lane], l);
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) {
+      const float4 x = sm_o[g][place][k][lane];
+      acc[k].x = fmaf(c, x.x, acc[k].x);
+      acc[k].y = fmaf(c, x.y, acc[k].y);
+      acc[k].z = fmaf(c, x.z, acc[k].z);
+      acc[k].w = fmaf(c, x.w, acc[k].w);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
   const int R = r0 + gr, t = R / p.G;
   const int64_t out_row = (int64_t)(p.cu_q[b] + t) * p.Hq + kvh * p.G + (R - t * p.G);
-  *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + out_row * D + col + 4 * warp) =
-      make_uint2(dev::pack2<T>(a.x * inv, a.y * inv), dev::pack2<T>(a.z * inv, a.w * inv));
-  if (warp == 0 && col == 0 && p.lse != nullptr)
-    p.lse[out_row] = Lsum > 0.f ? fmaf(M, dev::kLn2, logf(Lsum)) : Lsum == 0.f ? -INFINITY : Lsum;
+#pragma unroll
+  for (int k = 0; k < NQ; k += 2)
+    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + out_row * D + col + 4 * k) =
+        make_uint4(dev::pack2<T>(acc[k].x * inv, acc[k].y * inv), dev::pack2<T>(acc[k].z * inv, acc[k].w * inv),
+                   dev::pack2<T>(acc[k + 1].x * inv, acc[k + 1].y * inv), dev::pack2<T>(acc[k + 1].z * inv, acc[k + 1].w * inv));
+  if (part == 0 && p.lse != nullptr) p.lse[out_row] = l > 0.f ? fmaf(top, dev::kLn2, logf(l)) : l == 0.f ? -INFINITY : l;
 }
 
 // ------------------------------------------------------------------ launch
@@ -978,10 +990,15 @@ cudaError_t launch(const TreeParams& p, int splits, cudaStream_t stream) {
   void* args[] = {const_cast<TreeParams*>(&p)};
   err = cudaLaunchKernelExC(&cfg, fn, args);
   if (err != cudaSuccess || splits == 0) return err;
-  cfg.gridDim = dim3(p.rec_rows / 32 * (D / kCombineCols), splits);
-  cfg.blockDim = dim3(kCombineThreads);
+  const int blocks = p.rec_rows / 32 * splits;
+  const int groups = p.ctas / splits < 3 ? 2 : blocks >= 128 ? 4 : 8;  // ctas / splits + 1: records of an item
+  cfg.gridDim = dim3(p.rec_rows / 32, splits, 8 / combine_parts(groups));
+  cfg.blockDim = dim3(32 * groups * combine_parts(groups));
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&fd_tree_combine_kernel<T, D>), args);
+  const void* combine = groups == 2   ? reinterpret_cast<const void*>(&fd_tree_combine_kernel<T, D, 2>)
+                        : groups == 4 ? reinterpret_cast<const void*>(&fd_tree_combine_kernel<T, D, 4>)
+                                      : reinterpret_cast<const void*>(&fd_tree_combine_kernel<T, D, 8>);
+  return cudaLaunchKernelExC(&cfg, combine, args);
 }
 
 }  // namespace tree
