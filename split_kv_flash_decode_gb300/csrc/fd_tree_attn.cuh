@@ -254,7 +254,7 @@ struct Waiter {
 
 // ------------------------------------------------------------------ softmax
 
-// A row's weights of one tile.  ts, to: its lane's S (which its weights replace) and O; first: O holds nothing yet.
+// A row's weights of one tile; m is a score, without the scale.  ts, to: its lane's S (which its weights replace) and O; first: O holds nothing yet.
 template <int D, typename Op>
 __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint64_t mask, int off, float scale, bool mine,
                                       bool first, float& m, float& l) {
@@ -277,11 +277,11 @@ __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint6
   for (int k = 0; k < 128; k += 8)
 #pragma unroll
     for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(x[k + 2 * c]), __uint_as_float(x[k + 2 * c + 1]));
-  const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale;
-  // A row's maximum in use moves only when it grew by more than 2^8, which is rare.
-  const bool grew = mine && top > m + dev::kRescaleThreshold;
+  const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+  // A row's maximum in use moves only when its weight grew by more than 2^8, which is rare.
+  const bool grew = mine && (top - m) * scale > dev::kRescaleThreshold;
   if (__any_sync(0xffffffffu, grew)) {
-    const float coef = !grew ? 1.f : m == -INFINITY ? 0.f : dev::ex2(m - top);
+    const float coef = !grew ? 1.f : m == -INFINITY ? 0.f : dev::ex2((m - top) * scale);
     if (grew) m = top;
     l *= coef;
     if (!first) {  // the group's earlier products are done: this tile's scores were committed behind them
@@ -304,9 +304,10 @@ __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint6
     uint32_t y[32];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      // Product, then difference: the largest score minus the maximum in use is then exact.
-      const float2 e = unpair(add_pair(
-          mul_pair(pair(__uint_as_float(x[32 * c + 2 * k]), __uint_as_float(x[32 * c + 2 * k + 1])), scale2), minus2));
+      // Difference, then product: the largest score minus the maximum in use is then exact, however large both are.  (A
+      // product and a difference behind it become one instruction, rounding modes or not, which rounds m alone.)
+      const float2 e = unpair(mul_pair(
+          add_pair(pair(__uint_as_float(x[32 * c + 2 * k]), __uint_as_float(x[32 * c + 2 * k + 1])), minus2), scale2));
       const float f = dev::ex2(e.x), g = dev::ex2(e.y);
       const uint64_t fg = pair(f, g);
       sum[k & 1] = add_pair(sum[k & 1], fg);
@@ -433,11 +434,11 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
             float m = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-            const uint32_t lanes_here = __activemask();       // whole rows: CPR divides every bound
+            const uint32_t lanes_here = ((1u << CPR) - 1) << (lane & ~(CPR - 1));  // a row's: CPR divides every bound
 #pragma unroll
             for (int off = 1; off < CPR; off <<= 1) m = fmaxf(m, __shfl_xor_sync(lanes_here, m, off));
             const int e = (int)(__float_as_uint(m) >> 23);    // 2^(e - 127) <= m
-            const int up = e == 0 || e == 255 ? 0 : min(max(141 - e, -100), 100);
+            const int up = e == 0 || e == 255 ? 0 : min(141 - e, 100);
             const float s = __int_as_float((127 + up) << 23);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] *= s;
@@ -516,6 +517,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       }
 
       // The item's end (or this CTA's share of it).
+      m *= scale;
       const bool both = !o.two && jobs > 1;
       if (!o.two) *reinterpret_cast<float2*>(ml + 256 * w + 2 * wl) = make_float2(m, l);
 #pragma unroll

@@ -211,6 +211,19 @@ def test_query_sizes(fd, dtype):
         c.check(*c.run(), lse_tol=1e-3 if size > 1 else LSE_TOL)
 
 
+@pytest.mark.parametrize("power", [40, 80, 118])
+@pytest.mark.parametrize("dtype", ["bf16", "bf16_e2m1kv"])
+def test_largest_queries(fd, dtype, power):
+    """Scores whose last bit is far over 1: one token takes all, with a weight of 1."""
+    c = Case(fd, dtype, 64, 4, 2, [300, 40], [9, 3], seed=12, q_size=2.0 ** power)
+    c.q[0, 0] = 0.0
+    out, lse = c.run()
+    want, want_lse = c.reference()
+    assert np.isfinite(lse).all() and np.isfinite(out).all()
+    # A score is a sum of 64 terms whose sizes add up to less than 2^4 times the largest of them, off by 2^-23 of that.
+    assert (np.abs(lse - want_lse) <= 2.0 ** -18 * np.abs(want_lse) + LSE_TOL).all()
+
+
 def test_scores_that_overflow(fd):
     """Rows whose visible scores are all -inf in fp32 weigh nothing, as rows without any."""
     import torch
