@@ -580,8 +580,9 @@ int fd_tree_decode(fd_tree_t tree, const void* q, const void* k, const void* v, 
  *                  token, then -1 (so count tokens)
  *   count          device int32 [B], written: nodes that stand (0 for a sequence without drafted tokens)
  *
- * Products and differences of probabilities are exact or in 64 bits, sums of weights hold 2^-40 of a row's sum
- * (which must stay below 8).
+ * Products and differences of probabilities are exact or in 64 bits, sums of weights hold 2^-40 of a row's sum, or of 1
+ * where that is less.  A row whose sum is 8 or more (no probabilities) still gives a token of it, with no distribution
+ * promised.
  * FD_ERR_INVALID: a missing pointer, a short stride, an output that overlaps an input or another output;
  * FD_ERR_UNSUPPORTED: draft with parents, vocab; FD_ERR_ALIGN: a pointer not 4-byte aligned.  T = 0 still
  * writes count (and max_drafts = 0: nothing else).

@@ -38,6 +38,10 @@ __device__ __forceinline__ uint64_t fixed_of(float x) {
   return (uint64_t)((b << 5 & 0x0fffffe0u) | 0x10000000u) << 32 >> min(130 - (b >> 23), 63u);
 }
 __device__ __forceinline__ uint64_t fixed(float x) { return fixed_of(weight(x)); }
+// Sums of rows that are no probabilities (logits, say) stop here, so that none of them wraps around: 64 warps' sums, and
+// what the search adds to one of them, stay within 64 bits.
+constexpr uint64_t kMost = (1ull << 60) - 1;
+__device__ __forceinline__ uint64_t plus_most(uint64_t a, uint64_t b) { return min(a + b, kMost); }
 // A thread's sum of weights: two running sums (of the even and the odd ones) with what their additions and differences
 // rounded away beside them, so that some dozens of weights are off by 2^-46 of their sum.  All on the fp32 pipe, two
 // values an instruction; in 64-bit integers the sums took longer than the rows' bytes (64 rows of 131072 of both: 25 us).
@@ -80,9 +84,9 @@ struct Sum {
   // In units of 2^-57.
   __device__ __forceinline__ uint64_t fixed_sum() const {
     const float2 h = unpair(high), l = unpair(low);
-    const float rest = l.x + l.y;
-    const uint64_t sum = fixed_of(h.x) + fixed_of(h.y), r = fixed_of(fabsf(rest));
-    return rest >= 0.f ? sum + r : sum > r ? sum - r : 0;
+    const float rest = fminf(fmaxf(l.x + l.y, -8.f), 8.f);
+    const uint64_t sum = fixed_of(fminf(h.x, 8.f)) + fixed_of(fminf(h.y, 8.f)), r = fixed_of(fabsf(rest));
+    return min(rest >= 0.f ? sum + r : sum > r ? sum - r : 0, kMost);
   }
 };
 __device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? a - b : 0; }
@@ -92,9 +96,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Store into the shared memory of CTA `rank` of the cluster.
 __device__ __forceinline__ void store_cluster_u64(uint32_t addr, uint32_t rank, uint64_t v) {
   asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
@@ -125,6 +128,7 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
     }
     return;
   }
+  cluster_arrive();  // this CTA runs, so that others may write its shared memory
   if (warp == 0) {
     int up[2], tok[2];
     float u[2], pt[2], qt[2];
@@ -245,24 +249,29 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
       if (draft != nullptr) part.add_left(a, draft[i], b, i + 32 < w1 ? draft[j] : 0.f);
       else part.add(a, b);
     }
-    uint64_t sum = part.fixed_sum();
+    uint64_t sum = part.fixed_sum(), away = 0;
     // Tokens that were tried weigh nothing; one that was tried twice goes once.
     for (uint64_t m = gone; m != 0; m &= m - 1) {
       const int i = __ffsll((long long)m) - 1, t = tokens[i];
       bool again = false;
       for (uint64_t e = gone & ((1ull << i) - 1); e != 0; e &= e - 1) again |= tokens[__ffsll((long long)e) - 1] == t;
-      if (t >= w0 && t < w1 && lane == 0 && !again) sum -= fixed(target[t]);
+      if (t >= w0 && t < w1 && !again) away += fixed(target[t]);
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) warp_sum[attempt][warp] = (int64_t)sum > 0 ? sum : 0;
+    for (int off = 16; off > 0; off >>= 1) sum = plus_most(sum, __shfl_xor_sync(0xffffffffu, sum, off));
+    // What the tried tokens leave must be more than the roundings of both sums (3 units a lane, one a token, 2^-46 of
+    // the whole): else nothing is left, and nothing could be found.
+    if (lane == 0) warp_sum[attempt][warp] = gone == 0 ? sum : sum > away + (sum >> 44) + 256 ? sum - away : 0;
     __syncthreads();
+    if (attempt == 0) cluster_wait();
     if (tid < kVerifyCluster) {
       uint64_t all = 0;
-      for (int w = 0; w < kVerifyWarps; ++w) all += warp_sum[attempt][w];
+      for (int w = 0; w < kVerifyWarps; ++w) all = plus_most(all, warp_sum[attempt][w]);
       store_cluster_u64(dev::smem_addr(&slice_sum[attempt][rank]), tid, all);
     }
-    cluster_sync();
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
     uint64_t total = 0, before = 0;
     for (int r = 0; r < kVerifyCluster; ++r) {
       before += r < (int)rank ? slice_sum[attempt][r] : 0;
@@ -285,29 +294,32 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
     // All threads look through that warp's part: eight tokens each.
     for (int at0 = s0; at0 < s1; at0 += 8 * kVerifyThreads) {
       uint64_t x[8], mine = 0;
+      uint32_t weighs = 0;
       const int i0 = at0 + 8 * tid;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int i = i0 + k;
-        x[k] = i < s1 ? fixed(target[i]) : 0;
-        if (draft != nullptr && i < s1) x[k] = less(x[k], fixed(draft[i]));
+        const float a = i < s1 ? weight(target[i]) : 0.f, b = draft != nullptr && i < s1 ? weight(draft[i]) : 0.f;
+        x[k] = less(fixed_of(a), fixed_of(b));
+        if (a > b) weighs |= 1u << k;
       }
       for (uint64_t m = gone; m != 0; m &= m - 1) {
         const int t = tokens[__ffsll((long long)m) - 1] - i0;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (t == k) x[k] = 0;
+          if (t == k) {
+            x[k] = 0;
+            weighs &= ~(1u << k);
+          }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        mine += x[k];
-        if (x[k] != 0) heavy = i0 + k;
-      }
-      uint64_t upto = mine;
+      for (int k = 0; k < 8; ++k) mine += x[k];
+      if (weighs != 0) heavy = i0 + 31 - __clz(weighs);
+      uint64_t upto = min(mine, kMost);
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const uint64_t o = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += o;
+        if (lane >= off) upto = plus_most(upto, o);
       }
       __syncthreads();  // the sums of the last round are read
       if (lane == 31) warp_sum[attempt ^ 1][warp] = upto;
@@ -317,8 +329,9 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
         if (k < warp) sum0 += warp_sum[attempt ^ 1][k];
         before += warp_sum[attempt ^ 1][k];
       }
-      sum0 += upto - mine;
-      if (at >= sum0 && at < sum0 + mine) {
+      const uint64_t end = sum0 + upto, left = __shfl_up_sync(0xffffffffu, upto, 1);
+      sum0 += lane > 0 ? left : 0;
+      if (at >= sum0 && at < end) {
         int k = 0;
 #pragma unroll
         for (int j = 0; j < 7; ++j) {
@@ -331,7 +344,7 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
       }
       if (at < before) return;  // the same in every thread
     }
-    // The weights one by one came to less than their sum by 2^-46 of it: the last of them.
+    // The weights one by one came to less than their sum (by 2^-46 of it, or units that each of them lacks): the last.
     if (heavy >= 0) atomicMax(&last_s, heavy);
     __syncthreads();
     if (tid == 0) p.emitted[(int64_t)b * p.max_drafts + __popcll(stands) - 1] = last_s;

@@ -460,6 +460,54 @@ def test_verify_odd_rows(fd):
         by_hand(fd, [[0.0, 0.3, 0.0, 0.7, 0.0]], [0], [u])
 
 
+@pytest.mark.parametrize("draft", [False, True])
+@pytest.mark.parametrize("V", [40, 5000, 131072, 1 << 20])
+def test_verify_rows_that_are_no_probabilities(fd, V, draft):
+    """Logits, say: sums far beyond 8.  A token of the row comes out, the same one every time."""
+    import torch
+    g = torch.Generator().manual_seed(V)
+    target = (torch.randn((6, V), generator=g) * 4).cuda()
+    tokens = torch.randint(0, V, (6,), generator=g).int().cuda()
+    uniform = torch.tensor([0.999999, 0.5, 0.1, 0.99, 0.7, 0.2]).cuda()
+    t = fd.TreeDecoder(4, 2, 64, [3, 2, 1], [3, 2, 1])
+    kw = dict(draft=torch.ones((6, V)).cuda() * 0.5) if draft else {}
+    first = [x.cpu() for x in t.verify(target, tokens, uniform, **kw)]
+    path, emitted, count = first
+    weights = target.clamp(0, 1).cpu()
+    for b, (at, n) in enumerate([(0, 3), (3, 2), (5, 1)]):
+        k = int(count[b])
+        assert 1 <= k <= n and path[b, :k].tolist() == list(range(k))
+        last = int(emitted[b, k - 1])
+        assert 0 <= last < V and weights[at + k - 1, last] > 0
+    for x, y in zip(first, t.verify(target, tokens, uniform, **kw)):
+        assert torch.equal(x, y.cpu())
+
+
+def test_verify_tried_tokens_leave_nothing(fd):
+    """The tried tokens are all that has weight, and so little that a sum of both is not the sum of each one's units."""
+    a = (2 ** 23 + 40) * 2.0 ** -63  # 0.625 units beyond a whole number of 2^-57
+    for V, places in ((128, (5, 7)), (128, (5, 6)), (4000, (5, 2005)), (40, (3, 35))):
+        row = [0.0] * V
+        for x in places:
+            row[x] = a
+        for u, left in ((0.25, places[0]), (0.75, places[1])):
+            assert by_hand(fd, [row] * 3, [0, *places], [u, 0.9, 0.9], [-1, 0, 0]) == ([0], [left])
+
+
+def test_verify_differences_below_a_unit(fd):
+    """What the target has over the draft is less than the sums' unit at every token, more at all together."""
+    import torch
+    V = 1 << 16
+    q = torch.full((2, V), 2.0 ** -36)
+    p = q + 2.0 ** -59  # an ulp
+    q[:, 9] = 1.0
+    t = fd.TreeDecoder(4, 2, 64, [2], [2])
+    path, emitted, count = (x.cpu() for x in t.verify(p.cuda(), torch.tensor([0, 9], dtype=torch.int32).cuda(),
+                                                      torch.tensor([0.5, 0.5]).cuda(), draft=q.cuda()))
+    assert int(count) == 1 and path[0].tolist() == [0, -1]
+    assert 0 <= int(emitted[0, 0]) < V and int(emitted[0, 0]) != 9
+
+
 @pytest.mark.parametrize("u", [1.0, 5.0, -2.0, float("nan"), float("inf"), -float("inf")])
 def test_verify_uniforms_out_of_range_stay_in_the_vocabulary(fd, u):
     import torch
