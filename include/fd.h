@@ -483,8 +483,8 @@ int fd_gather(fd_rows_t rows, const void* k_cache, const void* v_cache, int num_
  *
  * fd_tree_plan -- plan a step (host only; no CUDA call unless num_sms == 0).
  *
- *   B, Hq, Hkv, d, dtype   as for fd_plan, with any group Hq / Hkv and with d = 64 as well for
- *                          FD_F16_E4M3KV
+ *   B, Hq, Hkv, d, dtype   as for fd_plan, with any group Hq / Hkv, Hq <= 4096, and with d = 64 as well
+ *                          for FD_F16_E4M3KV
  *   seqlens    host array [B]: the lengths L_b that the cache is laid out for, the drafted tokens included
  *   drafts     host array [B]: 0 <= n_b <= min(L_b, FD_MAX_DRAFTS)
  *   page_size  0: contiguous cache (rows packed as for fd_decode); else as fd_plan_paged
@@ -604,7 +604,8 @@ int fd_tree_verify(fd_tree_t tree, const float* target, int64_t target_stride, c
  *   status  device word or NULL
  *
  * Where a path does not ascend, or leaves [0, n_b), that entry and those behind it move nothing
- * (FD_TREE_BAD_PATH); a row from or to a page outside the pool is not moved (FD_TREE_BAD_PAGE).
+ * (FD_TREE_BAD_PATH); a row from or to a page outside the pool is not moved (FD_TREE_BAD_PAGE).  Two
+ * sequences whose drafted rows the block table sends to one place leave either's values there.
  * Errors as for fd_append; path, count, block_table and status 4-byte aligned.
  */
 int fd_tree_keep(fd_tree_t tree, void* k_cache, void* v_cache, int num_pages,

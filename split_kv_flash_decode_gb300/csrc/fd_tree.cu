@@ -108,6 +108,12 @@ __device__ __forceinline__ void store_cluster_u64(uint32_t addr, uint32_t rank, 
 // probability of their tokens (all gathered at once: the walk's chain is one load long), and a ballot finds
 // the children of a node.  Then each CTA sums a slice of the last node's row, the cluster adds the slices up,
 // and the CTA in whose slice the draw falls looks for it there.
+//
+// Bound by latency but for many sequences: a launch, the walk's gather, one batch of loads per thread, a cluster
+// barrier, the search.  One tree over 32768 tokens 5.4 us, 17 over 50021 (whose
+// rows begin at odd places) 9.2; 64 chains of 131072 tokens with both rows
+// 19.0 us, 3.5 TB/s.  There each cluster reads one row after its walk, in one wave; 512 threads a CTA, loads that pass
+// the L1 and 64-bit integer sums (25 us) were not faster.
 __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluster, 1, 1)
     fd_verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ int32_t tokens[FD_MAX_DRAFTS];
@@ -384,7 +390,8 @@ __device__ __forceinline__ void move_rows(uint8_t* cache, const int64_t* from, c
 
 // One thread: one piece of K (even blocks of a sequence) or V of a row, through all rows of its sequence
 // that move: nothing is shared between threads, so the move needs no order among them.  Pieces are 16
-// bytes; of a 4-bit block, whose rows lie in parts, 4 bytes, and single bytes for V's scales.
+// bytes; of a 4-bit block, whose rows lie in parts, 4 bytes, and single bytes for V's scales.  Bound by the
+// launch and two loads in series (the page's index, then the rows): 2.4 us for one sequence, 4.8 for 64 of E4M3.
 template <int KV>
 __global__ void __launch_bounds__(kKeepThreads) fd_keep_kernel(const __grid_constant__ KeepParams p) {
   __shared__ int64_t from[FD_MAX_DRAFTS], to[FD_MAX_DRAFTS];
@@ -545,7 +552,7 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
     return FD_ERR_UNSUPPORTED;
   if (B > FD_MAX_BATCH || (d != 64 && d != 128)) return FD_ERR_UNSUPPORTED;
   const int64_t limit = (int64_t)1 << 31;
-  // Token x head offsets of q and the heads of a grid stay within 32 bits.
+  // Query rows of a sequence (64 x Hq / Hkv) and pieces of a row stay far within 32 bits.
   if (Hq > 4096) return FD_ERR_UNSUPPORTED;
   const bool four = fd::kv_kind(dtype) == fd::kKvE2m1;
   int64_t T = 0, tokens = 0, blocks = 0, read = 0;

@@ -13,6 +13,15 @@
 // several CTAs share leaves fp32 records (m, l, O), which a second launch combines: no CTA waits for
 // another.  (The records of an item that one CTA had alone are never written.)
 //
+// What bounds it, at 8 KV heads of 128 elements: 16-bit caches and one row tile HBM (64 x 8192 tokens, 16 drafts, groups
+// of 4: 334 us, 6.47 TB/s; 32768 tokens 26.7 us, with the first loads, the records and their combination around 20 us of
+// stream).  Two row tiles: the products and the shared memory that feeds them (32768 tokens, 64 drafts, groups of 8: 80
+// us, 861 TFLOP/s).  8- and 4-bit caches: the way of a tile through a converter team, about 1800 clocks from its load's
+// arrival to its operand's (4 bits, 131072 tokens, 24 drafts, groups of 8: 127 us, 811 TFLOP/s), and over pages of 16
+// tokens the issue of the loads, 70 to 100 ns a box (E4M3, 64 x 4096 tokens, 5 drafts, groups of 4: 174 us; 131 without
+// pages).  Tiles whose tokens the two
+// groups split (S twice in tensor memory): equal over 16 bits, 10 to 22 % slower over the others.
+//
 // Warps: 0-3 and 4-7 softmax, 8 issues the products, 9 the TMA loads, 10 and 11 bring the next item's queries in, and
 // over 8- and 4-bit caches 12 on widen the stored rows to fp16 in the layout that the products read.
 #pragma once
@@ -151,8 +160,7 @@ struct Portion {
   bool slot;   // the CTA's record: 0 of the item it goes on with, 1 of the item it leaves unfinished
   __device__ __forceinline__ int jobs() const { return two ? 2 * nt : nt; }
   __device__ __forceinline__ int tile_of(int job) const { return two ? job >> 1 : job; }
-  // Places of a tile's K and V among the portion's 2 nt loads: in the order in which the products want them.
-  __device__ __forceinline__ int seq_k(int t) const { return two ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
+  // Place of a tile's V among the portion's 2 nt loads, which come in the order in which the products want them.
   __device__ __forceinline__ int seq_v(int t) const { return two || t == nt - 1 ? 2 * t + 1 : 2 * t + 2; }
   // The tile and kind of load s.
   __device__ __forceinline__ bool is_v(int s) const { return two || s == 2 * nt - 1 ? s & 1 : s != 0 && !(s & 1); }
