@@ -41,7 +41,7 @@ static_assert(tree_raw_slots(kKvE4m3, 128, 1) >= 4 && tree_raw_slots(kKvE4m3, 12
                   tree_raw_slots(kKvE2m1, 128, 1) >= 6 && tree_raw_slots(kKvE2m1, 128, 2) >= 6,
               "loads in flight");
 // After the tiles: barriers, flags, the query rows' scales, sums that the softmax groups exchange.
-constexpr int kTreeMetaBytes = 3072;
+constexpr int kTreeMetaBytes = 3 * 1024;
 constexpr int kTreeSmemBytes = kTreeSmemTiles + kTreeMetaBytes;
 
 // Floats of a CTA's partial record of `rows` query rows: m, l, then O as [d / 4][rows][4].

@@ -120,7 +120,7 @@ class TreeDecoder(CacheCalls):
         if t.dtype is not torch.float32 or t.get_device() != self._index or t.shape != (self.tokens, vocab):
             self._refuse(name, t, (self.tokens, vocab), torch.float32)
         row, one = t.stride()
-        if vocab > 1 and one != 1:
+        if self.tokens and vocab > 1 and one != 1:  # an empty tensor's strides say nothing
             raise ValueError(f"the elements of a row of {name} must be contiguous")
         return t.data_ptr(), row if self.tokens > 1 else vocab
 

@@ -415,6 +415,16 @@ def test_verify(fd, V, tree):
         same_verdicts(*verdicts(fd, drafts, V, 10 * V + seed, tree, kind=kind))
 
 
+def test_verify_without_tokens(fd):
+    """Empty rows may have any strides."""
+    import torch
+    t = fd.TreeDecoder(4, 2, 64, [5, 0], [0, 0])
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    for p in (torch.empty((0, 7), device="cuda"), torch.empty((7, 0), device="cuda").t(), torch.empty((5, 14), device="cuda")[5:, ::2]):
+        path, emitted, count = t.verify(p, none, none.float(), draft=p)
+        assert path.shape == emitted.shape == (2, 0) and count.tolist() == [0, 0]
+
+
 def test_verify_strides_and_many(fd):
     for tree in (True, False):
         same_verdicts(*verdicts(fd, [3, 0, 7], 501, 5, tree, stride=509))
