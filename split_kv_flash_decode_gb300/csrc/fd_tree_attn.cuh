@@ -57,6 +57,15 @@ __device__ __forceinline__ void regs_dec() {
 constexpr uint32_t kTmemAll = 512, kTmemS = 128, kTmemO = 256;
 constexpr int kMaxOperandSlots = 4;  // of 8- and 4-bit caches
 constexpr int kPrefetch = 4;         // operand tiles that a CTA brings into L2 ahead of its turn
+// Weights are held as 2^(their exponent + this).  A weight reaches 2^kRescaleThreshold, so fp16 weights can use 7 powers
+// more, up to 2^15: they are then normal numbers (11 bits) down to 2^-21 of the maximum in use, and off by at most 2^-32
+// of it below.  (As they are, a weight of 2^-25 was 0 in the product and still counted in the sum: 128K such tokens
+// behind one that leads were lost, 0.4 % of the row.)  bf16 has fp32's exponents.
+template <typename Op>
+FD_HD constexpr float weight_exponent() {
+  return std::is_same<Op, __half>::value ? 7.f : 0.f;
+}
+static_assert(dev::kRescaleThreshold + 7 <= 15, "fp16 weights stay finite");
 
 // ------------------------------------------------------------------ primitives
 
@@ -262,7 +271,8 @@ struct Waiter {
 
 // ------------------------------------------------------------------ softmax
 
-// A row's weights of one tile; m is a score, without the scale.  ts, to: its lane's S (which its weights replace) and O; first: O holds nothing yet.
+// A row's weights of one tile, 2^(weight_exponent + score - maximum in use), and their sum l; m is a score, without the
+// scale.  ts, to: its lane's S (which its weights replace) and O; first: O holds nothing yet.
 template <int D, typename Op>
 __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint64_t mask, int off, float scale, bool mine,
                                       bool first, float& m, float& l) {
@@ -305,7 +315,8 @@ __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint6
     }
   }
   const float mm = m == -INFINITY ? 0.f : m;
-  const uint64_t scale2 = pair(scale, scale), minus2 = pair(-mm, -mm);
+  constexpr float kUp = weight_exponent<Op>();
+  const uint64_t scale2 = pair(scale, scale), minus2 = pair(-mm, -mm), up2 = pair(kUp, kUp);
   uint64_t sum[2] = {0, 0};
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -314,8 +325,8 @@ __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint6
     for (int k = 0; k < 16; ++k) {
       // Difference, then product: the largest score minus the maximum in use is then exact, however large both are.  (A
       // product and a difference behind it become one instruction, rounding modes or not, which rounds m alone.)
-      const float2 e = unpair(mul_pair(
-          add_pair(pair(__uint_as_float(x[32 * c + 2 * k]), __uint_as_float(x[32 * c + 2 * k + 1])), minus2), scale2));
+      const uint64_t less = add_pair(pair(__uint_as_float(x[32 * c + 2 * k]), __uint_as_float(x[32 * c + 2 * k + 1])), minus2);
+      const float2 e = unpair(kUp != 0.f ? fma_pair(less, scale2, up2) : mul_pair(less, scale2));
       const float f = dev::ex2(e.x), g = dev::ex2(e.y);
       const uint64_t fg = pair(f, g);
       sum[k & 1] = add_pair(sum[k & 1], fg);
@@ -525,7 +536,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       }
 
       // The item's end (or this CTA's share of it).
-      m *= scale;
+      m = fmaf(m, scale, -weight_exponent<Op>());  // l and O are sums of 2^(score - m) from here on
       const bool both = !o.two && jobs > 1;
       if (!o.two) *reinterpret_cast<float2*>(ml + 256 * w + 2 * wl) = make_float2(m, l);
 #pragma unroll

@@ -1,0 +1,75 @@
+"""More of a speculative step on the GPU: long tails of small weights."""
+import numpy as np
+import pytest
+
+import oracle
+from test_tree import ALL, f64, fd  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ attention: the weights' range
+
+def tail_caches(dtype, L, d, rows):
+    """K and V of one KV head: keys 0 but for element 0 of the given rows ({row: key}); values 1, but 0 in the
+    upper half of a given row.  (k, v, the keys as stored)."""
+    import torch
+    if dtype.endswith("e2m1kv"):
+        codes, scales = np.zeros((2, L, 1, d), np.uint8), np.full((2, L, 1, d // 16), 0x38, np.uint8)
+        codes[1] = 2                                                     # 1.0
+        kept = {}
+        for row, key in rows.items():
+            code, scale, kept[row] = (6, 0x40, 8.0) if key == 8.0 else (7, 0x3D, 9.75)
+            codes[0, row, 0, 0], scales[0, row, 0, 0] = code, scale
+            codes[1, row, 0, d // 2:] = 0
+        return [torch.from_numpy(oracle.pack_blocks(c, s, w)).cuda() for c, s, w in zip(codes, scales, "kv")] + [kept]
+    t = torch.float8_e4m3fn if dtype == "f16_e4m3kv" else torch.bfloat16 if dtype == "bf16" else torch.float16
+    keys = {row: float(torch.tensor(key).to(t).float()) for row, key in rows.items()}
+    k, v = torch.zeros((L, 1, d), dtype=torch.float16, device="cuda"), torch.ones((L, 1, d), dtype=torch.float16, device="cuda")
+    for row, key in keys.items():
+        k[row, 0, 0], v[row, 0, d // 2:] = key, 0
+    if t is torch.float8_e4m3fn:
+        return k.to(t).view(torch.uint8), v.to(t).view(torch.uint8), keys
+    return k.to(t), v.to(t), keys
+
+
+def behind_a_dominant_token(fd, dtype, L, n, G, sms, second):  # noqa: F811
+    """(out, lse, weight of the tokens that lead, weight of the others for each token, score of the largest): rows 0
+    and 128, the first of either softmax group's tiles, lead all others by 25 bits; `second`, row 300 leads these two by up to
+    8 bits, for which the maximum in use does not move.  out's upper half is the share of the others, its lower half 1."""
+    import torch
+    d = 128
+    rows = {0: 8.0, 128: 8.0}
+    if second:
+        rows[300] = 10.0 if dtype == "f16_e4m3kv" else 10.53125
+    k, v, keys = tail_caches(dtype, L, d, rows)
+    t16 = torch.bfloat16 if dtype.startswith("bf16") else torch.float16
+    q = torch.zeros((n, G, d), dtype=t16, device="cuda")
+    q[..., 0] = 24.515625
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = fd.TreeDecoder(G, 1, d, [L], [n], dtype, num_sms=sms)(q, k, v, status=status)
+    assert int(status) == 0
+    score = {row: float(q[0, 0, 0]) * key / np.sqrt(d) for row, key in keys.items()}
+    top = max(score.values())
+    assert not second or 4 < (top - score[0]) / np.log(2) < 8
+    tail = (L - n + 1 + np.arange(n) - len(rows)) * np.exp(-top)         # a chain: each token sees one more
+    return f64(out), f64(lse), sum(np.exp(x - top) for x in score.values()), tail, top
+
+
+LONG = [(t, 131072) for t in ALL] + [("f16", 1 << 20), ("f16_e4m3kv", 1 << 20)]
+
+
+@pytest.mark.parametrize("second", [False, True])
+@pytest.mark.parametrize("n,G,sms", [(4, 4, 1), (33, 4, 1), (33, 4, 0)])
+@pytest.mark.parametrize("dtype,L", LONG)
+def test_long_tail_of_small_weights(fd, dtype, L, n, G, sms, second):  # noqa: F811
+    """Each of the others weighs 2^-25 of the first, which fp16 holds only in larger units.
+
+    A weight over these caches is off by 2^-11 of itself or, where that is more, by 2^-32 of the largest; ex2 and the
+    scores' fp32 (25 bits, to 2^-22 each) by less than 2^-16 of it.  out's upper half sums equal powers of two, so
+    |out - exact| <= L 2^-32 + (2^-11 + 2^-16) out and a rounding of the output."""
+    out, _, lead, tail, _ = behind_a_dominant_token(fd, dtype, L, n, G, sms, second)
+    eps = 2.0 ** -8 if dtype.startswith("bf16") else 2.0 ** -11
+    want = (tail / (lead + tail))[:, None, None]
+    err = np.abs(out[..., out.shape[2] // 2:] - want)
+    assert (err <= L * 2.0 ** -32 + (2.0 ** -11 + 2.0 ** -16 + eps) * want + 2.0 ** -25).all(), (err.max(), want[0, 0, 0])
