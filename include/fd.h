@@ -535,7 +535,9 @@ int fd_tree_get_info(fd_tree_t tree, fd_tree_info* info);
  *   status     device word or NULL
  *
  * out = sum_j softmax(s)_j V_j over the visible rows j, s_j = <q, K_j> / sqrt(d), lse = ln sum_j exp(s_j);
- * a token that sees no row has out = 0 and lse = -inf.  Scores, softmax statistics and sums are fp32.
+ * a token that sees no row has out = 0 and lse = -inf.  Scores, softmax statistics and sums are fp32; products with V
+ * add up in the tensor cores' accumulators, which cut towards 0, over at most 8320 tokens (4224 over a bf16 cache), and
+ * these sums in plain fp32.
  * Softmax weights enter the product with V rounded once: over a bf16 cache to 16 significant bits, over the others to 11
  * (off by 2^-11 of themselves; below 2^-21 of the row's largest by up to 2^-32 of that: 2^20 tokens together by 2^-12).
  * Rows that no token of a sequence sees (behind its last row, of nodes in no mask) may hold anything; a row

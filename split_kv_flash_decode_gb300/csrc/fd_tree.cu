@@ -633,7 +633,16 @@ int fd_tree_plan(int B, int Hq, int Hkv, int d, const int32_t* seqlens, const in
   }
   p.cu_q[B] = cu;
   p.unit_base[B] = unit;
-  t->ws_bytes = t->splits ? sizeof(float) * 2 * p.ctas * (size_t)fd::tree_record_floats(d, p.rec_rows) : 0;
+  t->sums_at = t->splits ? sizeof(float) * 2 * p.ctas * (size_t)fd::tree_record_floats(d, p.rec_rows) : 0;
+  // A portion has no more tiles than its sequence, nor than a run has units; a group takes each (two row tiles), or every
+  // other one.
+  const bool two_parts = dtype == FD_BF16;
+  for (int b = 0; b < B && !p.whole_items; ++b) {
+    const int tiles_here = std::min(fd::tree_tiles(seqlens[b]), p.run_len + 1);
+    const int jobs = drafts[b] * G > fd::kTreeTile ? tiles_here : (tiles_here + 1) / 2;
+    if (drafts[b] && jobs > fd::tree_sum_tiles(two_parts)) t->long_runs = true;
+  }
+  t->ws_bytes = t->sums_at + (t->long_runs ? sizeof(float) * 2 * p.ctas * (size_t)d * fd::kTreeTile : 0);
   *out_tree = t;
   return FD_OK;
 }
@@ -676,6 +685,7 @@ int fd_tree_decode(fd_tree_t t, const void* q, const void* k, const void* v, int
   if (rc != FD_OK) return rc;
   p.q = q; p.mask = mask; p.out = out; p.lse = lse; p.status = status;
   p.part = static_cast<float*>(workspace);
+  p.sums = t->long_runs ? p.part + t->sums_at / sizeof(float) : nullptr;
   p.block_table = block_table; p.bt_stride = bt_stride; p.num_pages = num_pages;
   const int kind = fd::kv_kind(t->dtype);
   const bool bf16 = fd::is_bf16(t->dtype);

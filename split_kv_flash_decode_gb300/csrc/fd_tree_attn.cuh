@@ -345,9 +345,44 @@ __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint6
   l += s2.x + s2.y;
 }
 
+// A row's O goes on outside of tensor memory: sums = coef x sums + O; or, at the end (`back`), O += coef x sums.  Where coef
+// is 0 there are no sums yet, or none that count.  A call, once in 64 tiles: in line it made the loop around it slower (64 x
+// 32K tokens of 4 bits: 1278 us; 1207 so, and 1150 without it).
+template <int D>
+__device__ __noinline__ void move_sums(uint32_t to, float* sums, float coef, bool back) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float4 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      o[k] = coef != 0.f ? __ldcg(reinterpret_cast<const float4*>(sums + (c + 4 * k) * kTreeTile)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncwarp();
+    uint32_t y[32];
+    ld32(to + c, y);
+    tc::wait_ld();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      o[k].x = fmaf(coef, o[k].x, __uint_as_float(y[4 * k]));
+      o[k].y = fmaf(coef, o[k].y, __uint_as_float(y[4 * k + 1]));
+      o[k].z = fmaf(coef, o[k].z, __uint_as_float(y[4 * k + 2]));
+      o[k].w = fmaf(coef, o[k].w, __uint_as_float(y[4 * k + 3]));
+    }
+    if (back) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(k % 4 == 0 ? o[k / 4].x : k % 4 == 1 ? o[k / 4].y : k % 4 == 2 ? o[k / 4].z : o[k / 4].w);
+      st32(to + c, y);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) __stcg(reinterpret_cast<float4*>(sums + (c + 4 * k) * kTreeTile), o[k]);
+    }
+  }
+  tc::wait_st();
+}
+
 // ------------------------------------------------------------------ the kernel
 
-template <typename T, int D, int KV>
+// kLong: some portion is longer than what a group's products may add up to in tensor memory (tree_sum_tiles).
+template <typename T, int D, int KV, bool kLong>
 __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_constant__ TreeParams p) {
   // Operands: bf16 over a bf16 cache, else fp16.
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value && KV == kKv16;
@@ -375,6 +410,10 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
   float* ml = reinterpret_cast<float*>(meta + kTreeMetaBytes - 2048);  // [2][128][2]: the groups' m and l at an item's end
   static_assert(kBars + 8 + 3 * sizeof(Portion) + 2 * kTreeRows + 2048 <= kTreeMetaBytes, "meta");
   const int nload = KV == kKv16 ? nslot : nraw;  // slots of the loads' ring
+  // O begins anew in tensor memory with a group's i-th tile of a portion where i & kSumMask == 0, but with the last: there
+  // it takes back what has gone on outside.
+  constexpr int kSumMask = kLong ? tree_sum_tiles(kBf16) - 1 : -1;
+  auto begins_anew = [](int job, int jobs) { return kLong ? ((job >> 1) & kSumMask) == 0 && (job < 2 || job + 2 < jobs) : job < 2; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   dev::pdl_launch_dependents();
@@ -481,6 +520,8 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = lanes + w * kTmemS, to = lanes + kTmemO + w * kTmemS;
     uint32_t base = 0, s_phase = 0, o_phase[2] = {0, 0};
+    // The m and l of sums outside of tensor memory lie where the item's end leaves its own.
+    float2* const own_ml = reinterpret_cast<float2*>(ml + 256 * w + 2 * wl);
     // The first item's queries, for which everybody waits, are brought in by all.
     put_queries(said[0], tid, 256 + 32 * kQueryWarps, -1);
     tc::named_sync(2, 256 + 32 * kQueryWarps);
@@ -508,7 +549,24 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
         __syncwarp();
         tc::fence_after_sync();
         if (busy) {
-          weigh<D, Op>(ts, to, edge, mask, off, scale, mine, j <= 1, m, l);
+          const bool anew = begins_anew(j, jobs);
+          if (kLong && j > 1) {  // the group's earlier products are done: this tile's scores were committed behind them
+            const bool last = j + 2 >= jobs, has_sums = j >> 1 > kSumMask + 1;
+            if (last ? has_sums : anew) {
+              float coef = 0.f;
+              if (has_sums) {
+                const float2 has = *own_ml;
+                coef = has.x == -INFINITY ? 0.f : dev::ex2((has.x - m) * scale);
+                l = fmaf(coef, has.y, l);
+              }
+              move_sums<D>(to, p.sums + (int64_t)(2 * blockIdx.x + w) * D * kTreeTile + 4 * wl, coef, last);
+              if (!last) {
+                *own_ml = make_float2(m, l);
+                l = 0.f;
+              }
+            }
+          }
+          weigh<D, Op>(ts, to, edge, mask, off, scale, mine, anew, m, l);
           tc::wait_st();
         }
         if (KV == kKv16 && edge) {
@@ -538,7 +596,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       // The item's end (or this CTA's share of it).
       m = fmaf(m, scale, -weight_exponent<Op>());  // l and O are sums of 2^(score - m) from here on
       const bool both = !o.two && jobs > 1;
-      if (!o.two) *reinterpret_cast<float2*>(ml + 256 * w + 2 * wl) = make_float2(m, l);
+      if (!o.two) *own_ml = make_float2(m, l);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (k < jobs) {
@@ -731,7 +789,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
           const uint32_t ps = w * kTmemS, od = kTmemO + w * kTmemS;
 #pragma unroll
           for (int kk = 0; kk < kTreeTile / 16; ++kk) {
-            mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8, vd + (kk * 2048 >> 4), kIdO, j > 1 || kk > 0);
+            mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8, vd + (kk * 2048 >> 4), kIdO, !begins_anew(j, jobs) || kk > 0);
             if (kBf16) mma_f16_ts(od, ps + (kk >> 1) * 32 + (kk & 1) * 8 + 16, vd + (kk * 2048 >> 4), kIdO, 1u);
           }
           if (!two || w == 1) tc::commit(op_empty0 + 8 * slot);
@@ -987,16 +1045,19 @@ __global__ void __launch_bounds__(32 * GROUPS * combine_parts(GROUPS)) fd_tree_c
 
 template <typename T, int D, int KV>
 cudaError_t launch(const TreeParams& p, int splits, cudaStream_t stream) {
-  const void* fn = reinterpret_cast<const void*>(&fd_tree_kernel<T, D, KV>);
+  const bool is_long = p.sums != nullptr;
+  const void* fn = is_long ? reinterpret_cast<const void*>(&fd_tree_kernel<T, D, KV, true>)
+                           : reinterpret_cast<const void*>(&fd_tree_kernel<T, D, KV, false>);
   int dev_id = 0;
   cudaError_t err = cudaGetDevice(&dev_id);
   if (err != cudaSuccess) return err;
-  static uint64_t done_mask = 0;  // devices whose shared-memory limit is set for this kernel
+  static uint64_t done_masks[2] = {0, 0};  // devices whose shared-memory limit is set for these kernels
+  uint64_t* const done_mask = &done_masks[is_long];
   const uint64_t bit = 1ull << (dev_id & 63);
-  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & bit)) {
+  if (!(__atomic_load_n(done_mask, __ATOMIC_ACQUIRE) & bit)) {
     err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmemBytes);
     if (err != cudaSuccess) return err;
-    __atomic_fetch_or(&done_mask, bit, __ATOMIC_RELEASE);
+    __atomic_fetch_or(done_mask, bit, __ATOMIC_RELEASE);
   }
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,9 +1,9 @@
-"""More of a speculative step on the GPU: long tails of small weights."""
+"""More of a speculative step on the GPU: long tails of small weights, long sums."""
 import numpy as np
 import pytest
 
 import oracle
-from test_tree import ALL, f64, fd  # noqa: F401
+from test_tree import ALL, LSE_TOL, f64, fd  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,44 @@ def test_long_tail_of_small_weights(fd, dtype, L, n, G, sms, second):  # noqa: F
     want = (tail / (lead + tail))[:, None, None]
     err = np.abs(out[..., out.shape[2] // 2:] - want)
     assert (err <= L * 2.0 ** -32 + (2.0 ** -11 + 2.0 ** -16 + eps) * want + 2.0 ** -25).all(), (err.max(), want[0, 0, 0])
+
+
+@pytest.mark.parametrize("second", [False, True])
+@pytest.mark.parametrize("n,G,sms", [(4, 4, 1), (33, 4, 1), (33, 4, 0)])
+@pytest.mark.parametrize("dtype,L", LONG)
+def test_long_sums_of_small_addends(fd, dtype, L, n, G, sms, second):  # noqa: F811
+    """The same tokens where every value is 1: the others are added to a sum that is 2^25 times each of them.  The bounds
+    are test_tree.py's, for any length: sums in tensor memory go on in plain fp32 before their truncation comes to 2^-11, and
+    a sum of fp32 weights of at most 64 tiles of 128, then of at most 2^13 / 64 such sums, is off by 2^-15."""
+    out, lse, lead, tail, top = behind_a_dominant_token(fd, dtype, L, n, G, sms, second)
+    eps = 2.0 ** -8 if dtype.startswith("bf16") else 2.0 ** -11
+    err = np.abs(out[..., :out.shape[2] // 2] - 1)
+    assert (err <= 2.0 ** -10 + eps).all(), err.max()
+    assert np.abs(lse - (top + np.log(lead + tail))[:, None]).max() <= LSE_TOL
+
+
+@pytest.mark.parametrize("n,G", [(4, 4), (33, 4)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f16_e4m3kv"])
+@pytest.mark.parametrize("page", [0, 256])
+def test_long_means(fd, dtype, n, G, page):  # noqa: F811
+    """2^20 tokens that weigh alike, all in one CTA: out is their mean, within the bounds of test_tree.py."""
+    import torch
+    d, L = 64, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(5)
+    v = 1 + torch.rand((L, 1, d), device="cuda", generator=g)
+    t16 = torch.bfloat16 if dtype == "bf16" else torch.float16
+    v = v.to(torch.float8_e4m3fn if dtype == "f16_e4m3kv" else t16)
+    sums = v.double().cumsum(0)[L - n:, 0]                                # a chain: token t sees L - n + 1 + t rows
+    want = (sums / (L - n + 1 + torch.arange(n, device="cuda"))[:, None]).cpu().numpy()[:, None]
+    k, v = torch.zeros_like(v), v.view(torch.uint8) if dtype == "f16_e4m3kv" else v
+    k, table = k.view(v.dtype), None
+    if page:
+        perm = torch.randperm(L // page, device="cuda", generator=g)
+        k, v = (torch.empty_like(x.view(-1, page, 1, d)).index_copy_(0, perm, x.view(-1, page, 1, d)) for x in (k, v))
+        table = perm.int()[None]
+    q = torch.randn((n, G, d), device="cuda", generator=g).to(t16)
+    out, lse = fd.TreeDecoder(G, 1, d, [L], [n], dtype, page_size=page, num_sms=1)(q, k, v, block_table=table)
+    eps = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    err = np.abs(f64(out) - want)
+    assert (err <= 2.0 ** -10 * 2 + eps * want).all(), err.max()
+    assert np.abs(f64(lse) - np.log(L - n + 1 + np.arange(n))[:, None]).max() <= LSE_TOL
