@@ -743,6 +743,9 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     constexpr uint32_t kIdO = tc::idesc_f16(kBf16, false, true, kTreeTile, D);
     const uint32_t q0 = dev::smem_addr(smem), slot0 = dev::smem_addr(slots);
     const bool leader = elect_one();
+    // The queries come behind this wait in other warps.  A bounded wait for them that began ahead of it would count the time
+    // that the kernels before take, however long, and give the CTA up over a second of it.
+    dev::pdl_wait();
     Place first;  // of the portion's loads
     uint32_t p_parity[2] = {0, 0};
     for (uint32_t k = 0;; ++k) {

@@ -1,9 +1,9 @@
-"""More of a speculative step on the GPU: long tails of small weights, long sums."""
+"""More of a speculative step on the GPU: long tails of small weights, long sums, long kernels ahead."""
 import numpy as np
 import pytest
 
 import oracle
-from test_tree import ALL, LSE_TOL, f64, fd  # noqa: F401
+from test_tree import ALL, LSE_TOL, Case, f64, fd  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +114,39 @@ def test_long_means(fd, dtype, n, G, page):  # noqa: F811
     err = np.abs(f64(out) - want)
     assert (err <= 2.0 ** -10 * 2 + eps * want).all(), err.max()
     assert np.abs(f64(lse) - np.log(L - n + 1 + np.arange(n))[:, None]).max() <= LSE_TOL
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f16_e4m3kv"])
+def test_no_bounded_wait_counts_the_kernels_before(fd, dtype):  # noqa: F811
+    """A call behind a kernel that lets its successors in at once and then takes over a second: waits of 1 s in the later
+    kernel begin when the earlier one is done."""
+    import torch
+    c = Case(fd, dtype, 128, 4, 2, [700, 300], [16, 5], seed=4)
+    tree = c.tree(num_sms=8)
+    want = c.run(tree)
+    # One CTA through one long sequence, all of its pages one page.
+    q, pool = torch.randn((1, 8, 128), device="cuda").half(), torch.randn((2, 1, 256, 8, 128), device="cuda").half()
+    out, lse = torch.empty_like(q), torch.empty((1, 8), device="cuda")
+
+    def ahead(tokens):
+        long = fd.TreeDecoder(8, 8, 128, [tokens], [1], "f16", page_size=256, num_sms=1)
+        table = torch.zeros((1, tokens // 256), dtype=torch.int32, device="cuda")
+        return lambda: long(q, *pool, block_table=table, out=out, lse=lse)
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    tokens = 1 << 18
+    run = ahead(tokens)
+    for e in events:
+        run()
+        e.record()
+    torch.cuda.synchronize()
+    run = ahead(min(1 << 27, int(tokens * 1500 / events[0].elapsed_time(events[1])) // 256 * 256))
+    got, got_lse = torch.zeros_like(c.q), torch.zeros((21, 8), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    events[0].record()
+    run()
+    tree(c.q, c.k, c.v, c.mask, out=got, lse=got_lse, status=status)
+    events[1].record()
+    torch.cuda.synchronize()
+    assert int(status) == 0 and np.array_equal(f64(got), want[0]) and np.array_equal(f64(got_lse), want[1])
+    assert events[0].elapsed_time(events[1]) > 1100
