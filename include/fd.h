@@ -574,7 +574,7 @@ int fd_tree_decode(fd_tree_t tree, const void* q, const void* k, const void* v, 
  *                  NaN and negative values count as 0, values over 1 as 1
  *   draft          device float [T, vocab], rows draft_stride apart, or NULL
  *   vocab          1 .. FD_MAX_VOCAB
- *   tokens         device int32 [T]; a token outside [0, vocab) never stands
+ *   tokens         device int32 [T]; a token outside [0, vocab), or of which the target's probability is 0, never stands
  *   parents        device int32 [T]: each node's parent within its sequence, below the node itself (a node
  *                  with any other value but the root's is never reached); NULL: a chain
  *   uniform        device float [T] in [0, 1)

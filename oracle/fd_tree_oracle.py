@@ -61,13 +61,13 @@ def verify_walk(target, tokens, uniform, parents=None, draft=None):
             there = 0 <= x < V
             if draft is not None:
                 q = weights(draft[i])
-                if there and u[i] * q[x] < p[x]:
+                if there and p[x] > 0 and u[i] * q[x] < p[x]:
                     went = i
                     break
                 left = np.maximum(p - q, 0.0)
             else:
                 w = left[x] if there else 0.0
-                if u[i] * mass < w:
+                if w > 0 and u[i] * mass < w:
                     went = i
                     break
                 mass -= w

@@ -173,14 +173,15 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
         below &= below - 1;
         const float pi = __shfl_sync(0xffffffffu, i < 32 ? pt[0] : pt[1], src);
         const float ui = __shfl_sync(0xffffffffu, i < 32 ? u[0] : u[1], src);
+        // A probability of 0 is looked at by itself: beside a random number outside [0, 1) a product can be below it.
         if (p.draft != nullptr) {
           const float qi = __shfl_sync(0xffffffffu, i < 32 ? qt[0] : qt[1], src);
-          if ((double)ui * (double)qi < (double)pi) went = i;
+          if (pi > 0.f && (double)ui * (double)qi < (double)pi) went = i;
         } else {
           const int ti = __shfl_sync(0xffffffffu, i < 32 ? tok[0] : tok[1], src);
           const uint64_t same = bits(tok[0] == ti, tok[1] == ti);
           const float left = (same & tried) ? 0.f : pi;
-          if ((double)ui * mass < (double)left) went = i;
+          if (left > 0.f && (double)ui * mass < (double)left) went = i;
           else mass -= (double)left;
         }
         if (went >= 0) break;

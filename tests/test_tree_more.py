@@ -1,4 +1,6 @@
-"""More of a speculative step on the GPU: long tails of small weights, long sums, long kernels ahead."""
+"""More of a speculative step on the GPU: long tails of small weights, long sums, long kernels ahead; tokens that
+never stand.
+"""
 import numpy as np
 import pytest
 
@@ -150,3 +152,29 @@ def test_no_bounded_wait_counts_the_kernels_before(fd, dtype):  # noqa: F811
     torch.cuda.synchronize()
     assert int(status) == 0 and np.array_equal(f64(got), want[0]) and np.array_equal(f64(got_lse), want[1])
     assert events[0].elapsed_time(events[1]) > 1100
+
+
+# ------------------------------------------------------------------ verify: tokens that never stand
+
+@pytest.mark.parametrize("u", [-0.0, -1e-30, -0.5, -2.0, -float("inf"), 5.0, float("inf"), float("nan")])
+def test_tokens_without_probability_never_stand(fd, u):  # noqa: F811
+    """Whatever the random number: tokens outside the vocabulary, and those that the target gives nothing."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    p = torch.tensor([[0.0, 0.5, 0.5, 0.0]] * 6).cuda()
+    uniform = torch.tensor([0.3] + [u] * 5).cuda()
+    tree = fd.TreeDecoder(4, 2, 64, [6], [6])
+    for tokens in ([1, -1, 4, 0, 3, 2 ** 31 - 1], [1, 2 ** 31 - 1, -2 ** 31, 4, -1, 3]):
+        path, emitted, count = tree.verify(p, torch.tensor(tokens, **i32), uniform, parents=torch.tensor([-1, 0, 0, 0, 0, 0], **i32))
+        assert int(count) == 1 and path[0].tolist() == [0] + [-1] * 5
+        assert emitted[0].tolist() == [1] + [-1] * 5   # 0.3 of what the target says
+    # Behind tokens that did not stand, with random numbers beyond 1: their sum goes past the whole.
+    over = torch.tensor([[0.0, 0.75, 0.75, 0.0]] * 6).cuda()
+    path, emitted, count = tree.verify(over, torch.tensor([1, 1, 2, 4, -1, 0], **i32), torch.tensor([0.3, 9.0, 9.0, 9.0, 9.0, 9.0]).cuda(),
+                                       parents=torch.tensor([-1, 0, 0, 0, 0, 0], **i32))
+    assert int(count) == 1
+    # Chains with the draft's probabilities.
+    draft = torch.full((6, 4), 0.25).cuda()
+    for token in (-1, 4, 0, 3):
+        path, emitted, count = tree.verify(p, torch.tensor([1] + [token] * 5, **i32), uniform, draft=draft)
+        assert int(count) == 1 and int(emitted[0, 0]) in (1, 2)
