@@ -1,5 +1,5 @@
-"""More of a speculative step on the GPU: long tails of small weights, long sums, long kernels ahead; tokens that
-never stand.
+"""More of a speculative step on the GPU: long tails of small weights, long sums, long kernels ahead, the
+largest queries' outputs; tokens that never stand.
 """
 import numpy as np
 import pytest
@@ -152,6 +152,39 @@ def test_no_bounded_wait_counts_the_kernels_before(fd, dtype):  # noqa: F811
     torch.cuda.synchronize()
     assert int(status) == 0 and np.array_equal(f64(got), want[0]) and np.array_equal(f64(got_lse), want[1])
     assert events[0].elapsed_time(events[1]) > 1100
+
+
+@pytest.mark.parametrize("power", [40, 80, 118])
+@pytest.mark.parametrize("dtype", ["bf16", "bf16_e2m1kv"])
+def test_largest_queries_give_the_rows_that_lead(fd, dtype, power):  # noqa: F811
+    """Scores whose last bit is far over 1.  A score is 64 products, each sum of them off by at most 2^-22 of their sizes
+    together, and a product with the scale behind it: within 2^-16 of that sum S.  So only rows whose exact score is within
+    2^-15 S of the largest (and 64, behind which a weight is 0) can have a weight, and out lies between their values;
+    of a single one it is its value, rounded once.  A query of zeros gives the mean of what its token sees."""
+    c = Case(fd, dtype, 64, 4, 2, [300, 40], [9, 3], seed=12, q_size=2.0 ** power)
+    c.q[0, 0] = 0.0
+    out, _ = c.run()
+    want, _ = c.reference()
+    q, (k, v), at, t, alone = f64(c.q), c.values, 0, 0, 0
+    for L, n, s in zip(c.seqlens, c.drafts, c.sees):
+        full = np.concatenate((np.ones((n, L - n), dtype=bool), s), 1)
+        for i in range(n):
+            for h in range(c.Hq):
+                if not q[t + i, h].any():
+                    assert (t, i, h) == (0, 0, 0)
+                    v_top = np.abs(v[at:at + L, 0]).max()
+                    assert (np.abs(out[0, 0] - want[0, 0]) <= 2.0 ** -10 * v_top + 2.0 ** -8 * np.abs(want[0, 0])).all()
+                    continue
+                sees = at + np.flatnonzero(full[i])
+                terms = k[sees, h // c.G] * q[t + i, h]
+                x, size = terms.sum(1) / np.sqrt(c.d), np.abs(terms).sum(1).max() / np.sqrt(c.d)
+                rows = v[sees[x >= x.max() - 2.0 ** -15 * size - 64], h // c.G]
+                alone += len(rows) == 1
+                lo, hi = rows.min(0), rows.max(0)
+                slack = 2.0 ** -8 * np.maximum(np.abs(lo), np.abs(hi)) + 2.0 ** -11 * (hi - lo)
+                assert ((out[t + i, h] >= lo - slack) & (out[t + i, h] <= hi + slack)).all()
+        at, t = at + L, t + n
+    assert alone >= 90                                 # of the 95 rows with a query
 
 
 # ------------------------------------------------------------------ verify: tokens that never stand
