@@ -517,7 +517,11 @@ int fd_tree_get_info(fd_tree_t tree, fd_tree_info* info);
  * calls. */
 #define FD_TREE_BAD_PAGE 1u  /* fd_tree_keep: a page index outside the pool */
 #define FD_TREE_BAD_PATH 2u  /* fd_tree_keep: a path that does not ascend within its sequence */
-#define FD_TREE_TIMEOUT 4u   /* fd_tree_decode: a bounded in-kernel wait gave up; out and lse are unusable */
+#define FD_TREE_TIMEOUT 4u   /* fd_tree_decode: a bounded in-kernel wait gave up; out and lse of its CTA's rows are NaN */
+
+/* Test hook for fd_tree_decode's bounded waits: CTA 0 of later calls with this handle loads no K or V, so that its waits
+ * run out (~1 s).  To be called before the handle is used.  No CUDA call. */
+int fd_tree_test_skip_loads(fd_tree_t tree);
 
 /*
  * fd_tree_decode -- attention of the drafted tokens over the cache (one launch, or two: partial

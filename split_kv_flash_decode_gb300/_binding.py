@@ -66,7 +66,7 @@ EXPORTED = (
     "fd_decode_noalloc", "fd_noalloc_status", "fd_plan_paged", "fd_decode_paged",
     "fd_rows_plan", "fd_rows_destroy", "fd_rows_get_info", "fd_append", "fd_gather",
     "fd_tree_plan", "fd_tree_destroy", "fd_tree_get_info", "fd_tree_decode", "fd_tree_verify",
-    "fd_tree_keep",
+    "fd_tree_keep", "fd_tree_test_skip_loads",
 )
 FD_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -202,6 +202,8 @@ def lib() -> ctypes.CDLL:
             L.fd_tree_plan.restype = ctypes.c_int
             L.fd_tree_destroy.argtypes = [vp]
             L.fd_tree_destroy.restype = ctypes.c_int
+            L.fd_tree_test_skip_loads.argtypes = [vp]
+            L.fd_tree_test_skip_loads.restype = ctypes.c_int
             L.fd_tree_get_info.argtypes = [vp, ctypes.POINTER(TreeInfo)]
             L.fd_tree_get_info.restype = ctypes.c_int
             L.fd_tree_decode.argtypes = [vp, vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp,
@@ -461,6 +463,11 @@ def fd_tree_plan(B, Hq, Hkv, d, seqlens, drafts, page_size=0, dtype="f16", num_s
 
 def fd_tree_destroy(tree: Tree) -> None:
     tree.close()
+
+
+def fd_tree_test_skip_loads(tree: Tree) -> None:
+    """fd_tree_test_skip_loads: the first CTA's bounded waits run out (for tests)."""
+    _check(lib().fd_tree_test_skip_loads(tree.handle), "fd_tree_test_skip_loads")
 
 
 def fd_tree_get_info(tree: Tree) -> dict:

@@ -653,6 +653,12 @@ int fd_tree_destroy(fd_tree_t tree) {
   return FD_OK;
 }
 
+int fd_tree_test_skip_loads(fd_tree_t t) {
+  if (!t) return FD_ERR_INVALID;
+  t->params.test_skip_loads = 1;
+  return FD_OK;
+}
+
 int fd_tree_get_info(fd_tree_t t, fd_tree_info* info) {
   if (!t || !info) return FD_ERR_INVALID;
   info->tokens = t->T;

@@ -73,6 +73,7 @@ struct TreeParams {
   int32_t ctas, run_len, run_extra;  // units per CTA; the first run_extra CTAs take one more
   int32_t whole_items;     // 1: a unit is an item, one for each CTA; else a tile
   int32_t item_units;      // units of an item beyond its tiles
+  int32_t test_skip_loads; // 1: CTA 0 brings nothing in (a test of the bounded waits)
   float scale_log2;        // log2(e) / sqrt(d)
   int32_t cu_q[FD_MAX_BATCH + 1];
   int32_t len[FD_MAX_BATCH];

@@ -246,8 +246,8 @@ __device__ __forceinline__ uint64_t seen_by_any(uint64_t m) {
   return m;
 }
 
-// Waits for a barrier's phase.  Where that takes over a second the CTA is given up: the status word says so, and
-// no later wait of the CTA waits.
+// Waits for a barrier's phase.  Where that takes over a second the CTA is given up: the status word and NaN in its rows say
+// so, and no later wait of the CTA waits.
 struct Waiter {
   volatile int* dead;
   uint32_t* status;
@@ -380,6 +380,28 @@ __device__ __noinline__ void move_sums(uint32_t to, float* sums, float coef, boo
 }
 
 // ------------------------------------------------------------------ the kernel
+
+// What a CTA that was given up leaves: NaN in all rows of its portions that are its own, NaN records of the others (which
+// make their rows NaN).  A thread takes a row of the 256 that an item can have.
+template <int D>
+__device__ __noinline__ void leave_nan(const TreeParams& p) {
+  const float nan = __int_as_float(0x7fffffff);
+  const int row = threadIdx.x;
+  Cursor cur(p, blockIdx.x);
+  Portion o;
+  while (cur.next(p, o)) {
+    if (row >= o.rows) continue;
+    if (!o.whole) {
+      __stcg(p.part + (int64_t)(2 * blockIdx.x + o.slot) * tree_record_floats(D, p.rec_rows) + row, nan);
+      continue;
+    }
+    const int R = o.r0 + row, t = R / p.G;
+    const int64_t at = (int64_t)(p.cu_q[o.b] + t) * p.Hq + o.kvh * p.G + (R - t * p.G);
+    uint4* out = static_cast<uint4*>(p.out) + at * (D / 8);
+    for (int c = 0; c < D / 8; ++c) out[c] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);  // fp16's, bf16's
+    if (p.lse != nullptr) p.lse[at] = nan;
+  }
+}
 
 // kLong: some portion is longer than what a group's products may add up to in tensor memory (tree_sum_tiles).
 template <typename T, int D, int KV, bool kLong>
@@ -698,6 +720,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
       for (int s = 0; s < min(2 * o.nt, kPrefetch); ++s)
         dev::tma_prefetch_l2_3d(o.is_v(s) ? &p.tm_v : &p.tm_k, bx * 64, o.kvh, row_of((o.tile0 + o.load_tile(s)) * kTreeTile) / kUnit);
     dev::pdl_wait();
+    if (p.test_skip_loads && blockIdx.x == 0) more = false;
     const uint32_t ring = dev::smem_addr(KV == kKv16 ? slots : raws);
     Place at;
     at.parity = 1;  // a slot that was never used is free
@@ -944,6 +967,7 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
     const uint64_t start = dev::global_timer_ns();
     while (dev::global_timer_ns() - start < 20000000ull) {}
     __syncthreads();
+    if (warp < kMmaWarp) leave_nan<D>(p);
   }
   if (warp == kMmaWarp) {
     tc::fence_after_sync();

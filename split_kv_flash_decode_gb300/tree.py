@@ -82,7 +82,8 @@ class TreeDecoder(CacheCalls):
         """(out, lse) of the drafted tokens: q and out [T, Hq, d], lse [T, Hq].
 
         mask: int64 [T], bit j of a token's mask set where it sees node j of its sequence (tree_masks);
-        None: each token sees itself and the nodes before it.
+        None: each token sees itself and the nodes before it.  status: an int32 word for FD_TREE_ bits; without one
+        a bounded wait that gave up shows in out and lse, which are NaN there.
         """
         if self._bad(q, self._q_shape, self._t16):
             self._refuse("q", q, self._q_shape, self._t16)

@@ -1,5 +1,5 @@
-"""More of a speculative step on the GPU: long tails of small weights, long sums, long kernels ahead, the
-largest queries' outputs; tokens that never stand.
+"""More of a speculative step on the GPU: long tails of small weights, long sums, long kernels ahead, waits
+that give up, the largest queries' outputs; tokens that never stand.
 """
 import numpy as np
 import pytest
@@ -152,6 +152,35 @@ def test_no_bounded_wait_counts_the_kernels_before(fd, dtype):  # noqa: F811
     torch.cuda.synchronize()
     assert int(status) == 0 and np.array_equal(f64(got), want[0]) and np.array_equal(f64(got_lse), want[1])
     assert events[0].elapsed_time(events[1]) > 1100
+
+
+@pytest.mark.parametrize("dtype,n", [("f16", 5), ("f16", 40), ("bf16", 5), ("f16_e4m3kv", 5), ("bf16_e2m1kv", 40)])
+def test_rows_of_a_wait_that_gave_up_are_nan(fd, dtype, n):  # noqa: F811
+    """The first of four CTAs loads nothing (test hook): it has one of six (sequence, KV head) pairs alone and begins the
+    second.  Rows of both are NaN without a look at the status word, which says so too; all others are as ever."""
+    import torch
+    c = Case(fd, dtype, 128, 4, 2, [3000] * 3, [n] * 3, seed=6)
+    want = c.run(c.tree(num_sms=4))
+    tree = c.tree(num_sms=4)
+    fd.fd_tree_test_skip_loads(tree.tree)
+    out, lse = torch.full((3 * n + 1, 8, 128), 7.0, dtype=c.q.dtype, device="cuda"), torch.full((3 * n + 1, 8), 7.0, device="cuda")
+    status = torch.full((1,), 8, dtype=torch.int32, device="cuda")
+    tree(c.q, c.k, c.v, c.mask, out=out[:-1], lse=lse[:-1], status=status)
+    assert int(status) == 8 | fd.FD_TREE_TIMEOUT
+    assert out[:n].isnan().all() and lse[:n].isnan().all() and (out[-1] == 7).all() and (lse[-1] == 7).all()
+    assert np.array_equal(f64(out[n:-1]), want[0][n:]) and np.array_equal(f64(lse[n:-1]), want[1][n:])
+    again = c.run(c.tree(num_sms=4))
+    assert np.array_equal(again[0], want[0]) and np.array_equal(again[1], want[1])
+
+
+def test_rows_of_a_long_run_that_gave_up_are_nan(fd):  # noqa: F811
+    import torch
+    c = Case(fd, "f16", 64, 2, 1, [20000], [3], seed=7)
+    tree = c.tree(num_sms=1)
+    fd.fd_tree_test_skip_loads(tree.tree)
+    out, lse = tree(c.q, c.k, c.v, c.mask)               # no status word
+    assert out.isnan().all() and lse.isnan().all()
+    c.check(*c.run(c.tree(num_sms=1)))
 
 
 @pytest.mark.parametrize("power", [40, 80, 118])
