@@ -229,20 +229,21 @@ __global__ void __launch_bounds__(kVerifyThreads) __cluster_dims__(kVerifyCluste
     const uint64_t gone = rest && p.draft == nullptr ? tried : 0;
     Sum part;
     int at0 = w0 + lane;
-    // 16 bytes at a time where both rows allow it.
+    // 16 bytes at a time where both rows allow it.  (Plain loads: the read-only path is for memory that nobody writes while
+    // the kernel runs, and this one may begin while a kernel before it still writes the rows.)
     if (((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) & 15) == 0) {
       const int whole = w1 & ~3;
       if (draft != nullptr) {
 #pragma unroll 4
         for (int i = w0 + 4 * lane; i < whole; i += kStep) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(target + i)), b = __ldg(reinterpret_cast<const float4*>(draft + i));
+          const float4 a = *reinterpret_cast<const float4*>(target + i), b = *reinterpret_cast<const float4*>(draft + i);
           part.add_left(a.x, b.x, a.y, b.y);
           part.add_left(a.z, b.z, a.w, b.w);
         }
       } else {
 #pragma unroll 4
         for (int i = w0 + 4 * lane; i < whole; i += kStep) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(target + i));
+          const float4 a = *reinterpret_cast<const float4*>(target + i);
           part.add(a.x, a.y);
           part.add(a.z, a.w);
         }
