@@ -118,6 +118,23 @@ def test_long_means(fd, dtype, n, G, page):  # noqa: F811
     assert np.abs(f64(lse) - np.log(L - n + 1 + np.arange(n))[:, None]).max() <= LSE_TOL
 
 
+@pytest.mark.parametrize("sms", [1, 2, 5])
+@pytest.mark.parametrize("dtype", ALL)
+def test_long_runs_of_several_items(fd, dtype, sms):  # noqa: F811
+    """CTAs that go from long items to short ones and back, with one and two row tiles; lengths at which a portion's last
+    tile is the one that would begin a new sum, and the one behind it."""
+    if sms == 1:
+        lens, drafts, page = [20000, 300, 17000, 8320, 8321, 4224, 4225], [33, 5, 4, 40, 64, 33, 64], 64
+    else:
+        lens, drafts, page = [33000, 1, 16640, 16641, 8448, 700, 8449], [16, 1, 8, 3, 1, 64, 20], 0
+    c = Case(fd, dtype, 64 if sms == 2 else 128, 4, 2, lens, drafts, page_size=page, seed=sms)
+    tree = c.tree(num_sms=sms)
+    first = c.run(tree)
+    c.check(*first)
+    again = c.run(tree)
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
 @pytest.mark.parametrize("dtype", ["f16", "f16_e4m3kv"])
 def test_no_bounded_wait_counts_the_kernels_before(fd, dtype):  # noqa: F811
     """A call behind a kernel that lets its successors in at once and then takes over a second: waits of 1 s in the later
