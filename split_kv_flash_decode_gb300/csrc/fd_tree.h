@@ -12,8 +12,9 @@ constexpr int kTreeRows = 256;    // query rows that stream the cache together: 
 constexpr int kTreeMaxCtas = 512;
 // What an item (a sequence's KV head and up to kTreeRows of its query rows) costs a CTA beyond its tiles, in tiles: up to
 // 10, as much as its records and its end take, so that few items are cut in two; 3/4 of a CTA's tiles where it has few, so
-// that small work still spreads.  (With 2, 6, 10 and 17: 32K tokens with a tree of 16: 30.8, 28.3, 26.9, 26.9 us; a ragged
-// batch of 17: 56.6, 30.2, 29.4, 31.3; 517 tokens: 7.3, 7.8, 8.6, 8.9.)
+// that small work still spreads.  A tile counts the same with one row tile and with two, which take longer.  (With 2, 6, 10
+// and 17: 32K tokens with a tree of 16: 30.8, 28.3, 26.9, 26.9 us; a ragged batch of 17: 56.6, 30.2, 29.4, 31.3; 517 tokens:
+// 7.3, 7.8, 8.6, 8.9.)
 constexpr int kTreeMinItemUnits = 2, kTreeMaxItemUnits = 10;
 // Items of at most this many tiles, no more of them than SMs, are each one CTA's: combining records would take longer.
 constexpr int kTreeWholeTiles = 3;
@@ -23,7 +24,7 @@ constexpr int kTreeWholeTiles = 3;
 // it, always towards 0.  So a tile can take up to 1.25 x 2^-18 of the sum away (twice that where weights have two parts), and
 // the sums go on in plain fp32 once that may have come to 1.25 x 2^-12.  (In one sum, 128K tokens of 2^-25 behind one that
 // leads were lost whole: 0.2 % of out.)  It costs long runs 1 to 2 %, over 4 bits 5: 64 x 32K tokens, 16 drafts, bf16 1260
-// -> 1280 us; 8 drafts, E4M3 860 -> 873, 4 bits 1150 -> 1207.
+// -> 1280 us; 8 drafts, E4M3 860 -> 874, 4 bits 1150 -> 1220.
 FD_HD constexpr int tree_sum_tiles(bool two_parts) { return two_parts ? 32 : 64; }
 
 // One CTA: operand tiles in the 16-bit swizzled layout (Q, then K and V in a ring of slots); over 8- and 4-bit

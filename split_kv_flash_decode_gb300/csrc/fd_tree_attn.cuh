@@ -13,14 +13,18 @@
 // several CTAs share leaves fp32 records (m, l, O), which a second launch combines: no CTA waits for
 // another.  (The records of an item that one CTA had alone are never written.)
 //
-// What bounds it, at 8 KV heads of 128 elements: 16-bit caches and one row tile HBM (64 x 8192 tokens, 16 drafts, groups
-// of 4: 334 us, 6.47 TB/s; 32768 tokens 26.7 us, with the first loads, the records and their combination around 20 us of
-// stream).  Two row tiles: the products and the shared memory that feeds them (32768 tokens, 64 drafts, groups of 8: 80
-// us, 861 TFLOP/s).  8- and 4-bit caches: the way of a tile through a converter team, about 1800 clocks from its load's
-// arrival to its operand's (4 bits, 131072 tokens, 24 drafts, groups of 8: 127 us, 811 TFLOP/s), and over pages of 16
-// tokens the issue of the loads, 70 to 100 ns a box (E4M3, 64 x 4096 tokens, 5 drafts, groups of 4: 174 us; 131 without
-// pages).  Tiles whose tokens the two
+// What bounds it, at 8 KV heads of 128 elements: 16-bit caches and one row tile HBM, most of the time (64 x 8192 tokens, 16
+// drafts, groups of 4: 326 to 339 us from box to box, 6.4 to 6.6 TB/s, where a decode reads the same bytes in 303; 32768
+// tokens 26.7 us, with the first loads, the records and their combination around 20 us of stream).  Two row tiles: the
+// products and the shared memory that feeds them (32768 tokens, 64 drafts, groups of 8: 81 us, 848 TFLOP/s).  8- and 4-bit
+// caches: the way of a tile through a converter team, about 1800 clocks from its load's arrival to its operand's (4 bits,
+// 131072 tokens, 24 drafts, groups of 8: 131 us, 787 TFLOP/s), and over pages of 16 tokens the issue of the loads, 70 to
+// 100 ns a box (E4M3, 64 x 4096 tokens, 5 drafts, groups of 4: 175 us; 127 without pages).  Tiles whose tokens the two
 // groups split (S twice in tensor memory): equal over 16 bits, 10 to 22 % slower over the others.
+//
+// Weights are rounded once to 16 bits, over bf16 caches to two parts of 8 bits.  Two parts of fp16 as well (22 bits) would
+// take the error of an fp16 output from 2.8e-4 to 2.1e-4 of it, and 189 instead of 176 us of this E4M3 batch, 172 instead of
+// 131 of these 4 bits, 1115 instead of 863 of 32 x 32768 tokens with 64 drafts over f16.
 //
 // Warps: 0-3 and 4-7 softmax, 8 issues the products, 9 the TMA loads, 10 and 11 bring the next item's queries in, and
 // over 8- and 4-bit caches 12 on widen the stored rows to fp16 in the layout that the products read.
@@ -347,7 +351,7 @@ __device__ __forceinline__ void weigh(uint32_t ts, uint32_t to, bool edge, uint6
 
 // A row's O goes on outside of tensor memory: sums = coef x sums + O; or, at the end (`back`), O += coef x sums.  Where coef
 // is 0 there are no sums yet, or none that count.  A call, once in 64 tiles: in line it made the loop around it slower (64 x
-// 32K tokens of 4 bits: 1278 us; 1207 so, and 1150 without it).
+// 32K tokens of 4 bits: 1278 us; 1220 so, and 1150 without it).
 template <int D>
 __device__ __noinline__ void move_sums(uint32_t to, float* sums, float coef, bool back) {
 #pragma unroll 1
@@ -979,8 +983,8 @@ __global__ void __launch_bounds__(threads(KV), 1) fd_tree_kernel(const __grid_co
 
 // 32 query rows (lanes) of one item that several CTAs share: a warp takes an eighth of the columns and every GROUPS-th
 // record, then the groups meet in shared memory.  Bound by the latency of the records' loads from L2: more groups where
-// records are many or blocks few.  (Always 8: 64 heads x 64 drafts over 32K tokens 81.6 us instead of 77; always 2: 4K
-// tokens, with 19 records an item, 16.5 us instead of 11.3.)
+// records are many or blocks few.  (Always 8: 64 heads x 64 drafts over 32K tokens 81.6 us instead of 80.7; always 2: 4K
+// tokens, with 19 records an item, 18.9 us instead of 11.4.)
 FD_HD constexpr int combine_parts(int groups) { return groups == 2 ? 8 : groups == 4 ? 4 : 1; }  // eighths of a block
 template <typename T, int D, int GROUPS>
 __global__ void __launch_bounds__(32 * GROUPS * combine_parts(GROUPS)) fd_tree_combine_kernel(const __grid_constant__ TreeParams p) {
